@@ -297,6 +297,89 @@ int mla_qk_rope_concat_and_cache(const mla_tensor_t* q_nope, const mla_tensor_t*
                                  int32_t* error_word, mla_stream_t stream);
 
 /*
+ * The three entry points below serve layers whose heads keep their own keys and values
+ * (grouped heads: Hk key/value heads, each shared by G = Hq / Hk query heads): a drafter's
+ * layers next to the latent decode that verifies its tokens, and the prompt of a latent
+ * layer with its keys and values expanded to heads ("[Kimi-K3 MLA TP8] MLA performance" §2:
+ * 192 key and 128 value columns a head).  They run in this order: the append (rotation and
+ * cache write), then the prompt's attention or the decode of one new token.
+ *
+ * mla_gqa_rope_and_cache: for token t < T, with p = positions[t] and the table row
+ * cos_sin[p] = (cos th_0 .. cos th_{R/2-1}, sin th_0 .. sin th_{R/2-1}):
+ *   rot(x)  the row x with its pairs turned by th_i: pair i is (x[2i], x[2i+1])
+ *           (is_neox = 0) or (x[i], x[i+R/2]) (is_neox = 1), (a, b) becomes
+ *           (a cos th_i - b sin th_i, b cos th_i + a sin th_i), every product and sum rounded
+ *           to fp32 (no fused multiply-add); columns from R on pass through;
+ *   q_out[t, h] = bf16(rot(q[t, h])),   k_out[t, h] = bf16(rot(k[t, h]))
+ *   k_cache / v_cache slot slot_mapping[t] (= page * PS + slot), head h
+ *               = bf16(rot(k[t, h])), v[t, h]                         (BF16 caches)
+ *               = e(rot(k[t, h]), k_scale), e(v[t, h], v_scale)       (E4M3FN caches)
+ *   e(x, s) the e4m3fn code nearest to fp32(x / s) (ties to even, saturating at +-448).
+ *   q             (T, Hq, D) BF16, Hq a multiple of Hk, D 64 or 128
+ *   k, v          (T, Hk, D) BF16
+ *                 (each: last dim contiguous, 16-byte aligned, other strides non-negative
+ *                 multiples of 8 elements: views into one wider projection are fine)
+ *   positions     (T,) INT32;  slot_mapping (T,) INT32, < 0: no entry (padding)
+ *   cos_sin       (max_pos, R) FP32, R <= D a multiple of 16, last dim contiguous, row
+ *                 stride a multiple of 4, 16-byte aligned
+ *   k_scale, v_scale  0-dim (or 1-element) FP32 with E4M3FN caches; NULL with BF16
+ *   q_out, k_out  as q and k (written); may be q and k themselves (same pointer and strides).
+ *                 k_out may be NULL (a decode step needs no copy of the new keys).
+ *   k_cache, v_cache  (N_pages, PS, Hk, D) BF16 or E4M3FN, both of one type and one set of
+ *                 strides, PS a power of two <= 1024, last dim contiguous, the other strides
+ *                 multiples of 16 bytes (slots or heads may be the inner dim of a page),
+ *                 N_pages * PS < 2^31 (written at the mapped slots only)
+ *   error_word    device int32 (required): a slot >= N_pages * PS is skipped and sets bit 64;
+ *                 a position outside [0, max_pos) sets bit 1 and leaves that token's rotated
+ *                 columns (of q_out, k_out and its key entry) unwritten.
+ * Two tokens mapped to one slot race.  T = 0 does nothing.  Shapes, dtypes, strides or
+ * alignments outside these return MLA_ERR_INVALID_ARG (another D or PS:
+ * MLA_ERR_UNSUPPORTED) before anything is enqueued.  Asynchronous on `stream`.
+ */
+int mla_gqa_rope_and_cache(const mla_tensor_t* q, const mla_tensor_t* k, const mla_tensor_t* v,
+                           const mla_tensor_t* positions, const mla_tensor_t* cos_sin,
+                           int32_t is_neox, const mla_tensor_t* slot_mapping,
+                           const mla_tensor_t* k_scale, const mla_tensor_t* v_scale,
+                           const mla_tensor_t* q_out, const mla_tensor_t* k_out,
+                           const mla_tensor_t* k_cache, const mla_tensor_t* v_cache,
+                           int32_t* error_word, mla_stream_t stream);
+
+/*
+ * Bytes of workspace mla_gqa_decode needs for calls of this shape on a GPU with num_sms SMs
+ * (<= 0: the current device's).  It does not grow with the batch or the lengths.
+ */
+int mla_get_gqa_decode_workspace_size(int32_t batch_size, int32_t num_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t num_sms, size_t* bytes_out);
+
+/*
+ * Attention of one new token a request over the cache mla_gqa_rope_and_cache writes.  For
+ * request b, query head h and its KV head h / G, over the request's positions j < L_b (as
+ * mla_decode: (pages - 1) * PS + kv_last_page_lens[b], 0 without pages):
+ *   s_j = sm_scale * k_scale * sum_d q[b, h, d] * k_j[d]
+ *   lse = ln sum_j exp(s_j),   o[b, h] = v_scale * sum_j exp(s_j - lse) * v_j
+ * No position (or no finite maximum: every score -inf) gives o = 0 and lse = -inf.
+ *   q             (B, Hq, D) BF16, D 64 or 128, as above
+ *   k_cache, v_cache, k_scale, v_scale  as above; bytes past a request's positions (a last
+ *                 page's tail, other pages) are never read
+ *   o             (B, Hq, D) BF16 or FP32, last dim contiguous (written)
+ *   kv_indptr, kv_indices, kv_last_page_lens  the page table as mla_decode takes it
+ *   lse_out       (B, Hq) FP32 contiguous, or NULL
+ *   workspace     mla_get_gqa_decode_workspace_size(...) bytes, 256-byte aligned, zeroed
+ *                 before its first use; a call leaves its counters as it found them.  Calls
+ *                 that share one must not overlap on the GPU.
+ * The result does not depend on the order in which the pieces of a split request finish.
+ * Device-side errors go to the workspace's error word (mla_check_error): a page list that is
+ * not monotone or leaves kv_indices makes that request empty, a page id outside the cache
+ * reads as zeros; both give MLA_ERR_BAD_INDEX.  B = 0 does nothing.
+ */
+int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla_tensor_t* v_cache,
+                   const mla_tensor_t* o, const mla_tensor_t* kv_indptr,
+                   const mla_tensor_t* kv_indices, const mla_tensor_t* kv_last_page_lens,
+                   float sm_scale, const mla_tensor_t* k_scale, const mla_tensor_t* v_scale,
+                   const mla_tensor_t* lse_out, void* workspace, size_t workspace_bytes,
+                   mla_stream_t stream);
+
+/*
  * Debug check of a decode call's index inputs on the device, then a host status:
  * MLA_OK, MLA_ERR_BAD_INPUT (indptr not monotone or not starting at 0 for qo, kv_len <
  * q_len, kv_last_page_lens outside [1, PS] (!= 1 when PS = 1), qo_indptr[B] != sum_T) or

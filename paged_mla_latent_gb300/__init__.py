@@ -27,7 +27,8 @@ __all__ = [
     "MlaError", "mla_decode", "mla_decode_shared_prefix", "mla_decode_noalloc", "mla_merge_partials",
     "mla_validate", "mla_check_error", "mla_get_workspace_size", "mla_get_shared_prefix_workspace_size",
     "mla_status_string", "make_workspace", "library_path", "PreparedDecode", "mla_latent_to_v",
-    "mla_selftest_bounded_wait", "mla_qk_rope_concat_and_cache",
+    "mla_selftest_bounded_wait", "mla_qk_rope_concat_and_cache", "mla_gqa_rope_and_cache",
+    "mla_gqa_decode", "mla_get_gqa_decode_workspace_size", "make_gqa_decode_workspace",
 ]
 
 MLA_DTYPE_FP8_E4M3FN = 1
@@ -83,6 +84,13 @@ def _load() -> ctypes.CDLL:
     lib.mla_latent_to_v.argtypes = [P, P, P, vp]
     lib.mla_qk_rope_concat_and_cache.restype = ctypes.c_int
     lib.mla_qk_rope_concat_and_cache.argtypes = [P, P, P, P, P, P, c_i32, P, P, P, P, P, vp, vp]
+    lib.mla_gqa_rope_and_cache.restype = ctypes.c_int
+    lib.mla_gqa_rope_and_cache.argtypes = [P, P, P, P, P, c_i32, P, P, P, P, P, P, P, vp, vp]
+    lib.mla_get_gqa_decode_workspace_size.restype = ctypes.c_int
+    lib.mla_get_gqa_decode_workspace_size.argtypes = [c_i32, c_i32, c_i32, c_i32, c_i32,
+                                                      ctypes.POINTER(c_sz)]
+    lib.mla_gqa_decode.restype = ctypes.c_int
+    lib.mla_gqa_decode.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P, vp, c_sz, vp]
     lib.mla_selftest_bounded_wait.restype = ctypes.c_int
     lib.mla_selftest_bounded_wait.argtypes = [vp, vp, ctypes.c_int64, vp]
     return lib
@@ -356,6 +364,66 @@ def mla_qk_rope_concat_and_cache(q_nope, q_pe, kv_c, k_pe, positions, cos_sin, i
                                            ctypes.c_void_p(error_word.data_ptr()),
                                            _stream(stream, q_out.device))
     _check(rc, "mla_qk_rope_concat_and_cache")
+
+
+def _error_word(error_word, device):
+    if not isinstance(error_word, torch.Tensor) or error_word.dtype != torch.int32 or \
+            error_word.numel() < 1 or error_word.device != device:
+        raise ValueError(f"error_word must be an int32 tensor on {device}")
+    return ctypes.c_void_p(error_word.data_ptr())
+
+
+def mla_gqa_rope_and_cache(q, k, v, positions, cos_sin, is_neox, slot_mapping, q_out, k_cache,
+                           v_cache, error_word, k_scale=None, v_scale=None, k_out=None,
+                           stream=None):
+    """Rotate q's and the new keys' first cos_sin.shape[1] columns and write each token's keys
+    and values into the per-head caches at its slot (see include/paged_mla.h).  q_out and
+    k_out may be q and k; k_scale and v_scale belong to e4m3 caches.  error_word: an int32
+    device tensor (>= 1 element)."""
+    ew = _error_word(error_word, q.device)
+    d = [_desc(t) for t in (q, k, v, positions, cos_sin, slot_mapping, k_scale, v_scale, q_out,
+                            k_out, k_cache, v_cache)]
+    r = [_ref(x) for x in d]
+    rc = _lib.mla_gqa_rope_and_cache(*r[:5], int(is_neox), *r[5:], ew, _stream(stream, q.device))
+    _check(rc, "mla_gqa_rope_and_cache")
+
+
+def mla_get_gqa_decode_workspace_size(batch_size: int, num_heads: int, num_kv_heads: int,
+                                      head_dim: int, num_sms: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.mla_get_gqa_decode_workspace_size(batch_size, num_heads, num_kv_heads, head_dim,
+                                                  num_sms, ctypes.byref(out)),
+           "mla_get_gqa_decode_workspace_size")
+    return int(out.value)
+
+
+def make_gqa_decode_workspace(batch_size: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                              device=None) -> torch.Tensor:
+    """A zero-initialised device workspace for mla_gqa_decode calls of this shape."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = mla_get_gqa_decode_workspace_size(batch_size, num_heads, num_kv_heads, head_dim)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale,
+                   k_scale=None, v_scale=None, lse_out=None, workspace=None, stream=None):
+    """Attention of one new token a request over paged per-head caches (see
+    include/paged_mla.h).  Returns the workspace used."""
+    if workspace is None:
+        # made (and zeroed) on the stream that uses it
+        st = stream if stream is None or isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(int(stream), device=q.device)
+        with torch.cuda.stream(st):
+            workspace = make_gqa_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[2],
+                                                  q.shape[2], q.device)
+    d = [_desc(t) for t in (q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_lens,
+                            k_scale, v_scale, lse_out)]
+    r = [_ref(x) for x in d]
+    rc = _lib.mla_gqa_decode(*r[:7], float(sm_scale), *r[7:], ctypes.c_void_p(workspace.data_ptr()),
+                             workspace.numel() * workspace.element_size(), _stream(stream, q.device))
+    _check(rc, "mla_gqa_decode")
+    return workspace
 
 
 def mla_selftest_bounded_wait(error_word, result, limit_ns, stream=None):

@@ -1,0 +1,717 @@
+// mla_gqa_decode: attention of one new token a request over a paged cache of per-head keys
+// and values, split over the cache's length and joined in the same launch.
+//
+//   s_j = sm_scale * k_scale * q . k_j,   o = v_scale * sum_j e^{s_j - lse} v_j,
+//   lse = ln sum_j e^{s_j}, over the request's L positions, for each of the G = Hq / Hk query
+//   heads of a KV head.
+//
+// Bound by the cache's bytes: 2 D elements a position and KV head, each used by G heads.
+//
+// Work split.  A unit is (request, KV head, chunk of 8 NT query heads); its positions are cut
+// into tiles of 16.  All units' tiles form one line and every CTA takes an equal span of it,
+// so ragged lengths, few long requests and many short ones all fill the GPU.  A unit that
+// crosses a span's end leaves partials (m, l, o in fp32) in workspace slots; the CTA that
+// arrives last at the unit's counter joins them in the order of the spans, so the result does
+// not depend on the order of arrival.
+//
+// Inside a CTA four warps take tiles in turn, each with its own ring of cp.async stages, its
+// own running maximum, sum and output, and no barrier until the span's piece ends.
+//   S^T (16 positions x 8 heads) = K (16 x D) . q^T by mma.sync m16n8k16 with K as the A
+//   operand, so that 8 heads fill the MMA's N exactly (a step has at most a few heads a KV
+//   head; tcgen05's smallest M of 64 rows would be mostly padding, and the MMAs hide under
+//   the loads); softmax over positions; O^T (D x 8) += V^T . P^T, where P^T's fragments come
+//   from S^T's by one 8x8 transpose (movmatrix).
+// A bf16 cache multiplies in bf16, P rounded to bf16 (2^-8 of each weight at most, the sum l
+// kept in fp32 from the unrounded weights).  An e4m3 cache multiplies in f16, into which its
+// codes convert exactly: each q row is scaled by a power of two to a maximum in [2^13, 2^14)
+// (q's 8 bits fit f16's 11; what falls below f16's range is under 2^-38 of the row's
+// maximum), P carries a factor 2^14 that cancels against l (rounded by at most 2^-11).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "../../include/paged_mla.h"
+#include "mla_gqa_check.h"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace pmla;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16;            // positions a warp takes at a time
+constexpr int kHeaderBytes = 256;    // error word
+constexpr int kCtasPerSm = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct GqaDecodeParams {
+  const uint16_t* q;
+  int64_t q_tok, q_head;
+  const uint8_t *k, *v;
+  int64_t page_pitch, slot_pitch, head_pitch;
+  int log2_page;
+  int64_t n_pages;
+  const int32_t *kv_indptr, *kv_indices, *last;
+  int64_t n_idx;
+  const float *k_scale, *v_scale;
+  float sm_scale;
+  void* o;
+  int o_f32;
+  int64_t o_tok, o_head;
+  float* lse;
+  int B, Hq, Hk, G, chunks;
+  int min_span;
+  int* err;
+  int* counters;                     // one a CTA: the unit that leaves its span's end
+  float* slots;                      // two a CTA: m[R], l[R], o[R][D] with R = 8 NT
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool kF16>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (kF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// D columns, cache type, n-tiles of 8 query heads; kStages tiles in flight a warp.
+template <int D_, bool kFp8_, int NT_>
+struct DecodeShape {
+  static constexpr int D = D_, NT = NT_;
+  static constexpr bool kFp8 = kFp8_;
+  static constexpr int kRow = D * (kFp8 ? 1 : 2);          // bytes of a K or V row
+  static constexpr int kTileBytes = 2 * kTile * kRow;      // K then V
+  static constexpr int kHeads = 8 * NT;
+  // about 24 KB in flight a warp (eight warps a SM: 192 KB)
+  static constexpr int kStages = 24576 / kTileBytes < 8 ? 24576 / kTileBytes : 8;
+  static constexpr int kWarpBytes = kStages * kTileBytes;
+  static constexpr int kJoinBytes = kWarps * kHeads * D * 4;   // per-warp outputs, over the rings
+  static constexpr int kBuf = kWarps * kWarpBytes > kJoinBytes ? kWarps * kWarpBytes : kJoinBytes;
+  static constexpr int kSmem = kBuf + 2 * kWarps * kHeads * 4;
+  static constexpr int kSlotFloats = kHeads * (D + 2);
+};
+
+// Byte offset of 16-byte chunk c of row r: chunks are permuted within 128 bytes so that
+// eight rows' equal chunks fall into different banks.
+template <int kRow>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (kRow >= 128) return r * kRow + ((c ^ (r & 7)) << 4);
+  else return r * kRow + ((c ^ ((r >> 1) & 3)) << 4);      // 64-byte rows: two a line
+}
+
+// Positions of request b, 0 where its page list makes no sense.
+__device__ __forceinline__ int request_len(const GqaDecodeParams& p, int b, bool flag) {
+  const int64_t s = p.kv_indptr[b], e = p.kv_indptr[b + 1];
+  if (s < 0 || e < s || e > p.n_idx) {
+    if (flag) atomicOr(p.err, kErrBadIndptr);
+    return 0;
+  }
+  if (e == s) return 0;
+  const int ps = 1 << p.log2_page;
+  int last = p.last ? p.last[b] : ps;
+  last = last < 1 ? 1 : (last > ps ? ps : last);
+  const int64_t len = ((e - s - 1) << p.log2_page) + last;
+  if (len > 0x7FFFFF00) {
+    if (flag) atomicOr(p.err, kErrBadIndptr);
+    return 0;
+  }
+  return static_cast<int>(len);
+}
+
+__device__ __forceinline__ void store_o(const GqaDecodeParams& p, int b, int h, int d, float x) {
+  const int64_t at = b * p.o_tok + h * p.o_head + d;
+  if (p.o_f32) static_cast<float*>(p.o)[at] = x;
+  else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
+}
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const GqaDecodeParams p) {
+  constexpr int D = S::D, NT = S::NT, kRow = S::kRow, kHeads = S::kHeads;
+  constexpr bool kFp8 = S::kFp8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* s_m = reinterpret_cast<float*>(smem + S::kBuf);       // [warp][head]
+  float* s_l = s_m + kWarps * kHeads;
+  __shared__ int64_t sh_scan[kWarps];
+  __shared__ int64_t sh_base;
+  __shared__ int sh_b, sh_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = p.Hk * p.chunks;
+  const int cta = blockIdx.x;
+
+  // ---- the line: total tiles, this CTA's span, and the request its span starts in
+  int64_t mine = 0;
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int len = request_len(p, b, cta == 0);
+    mine += (len + kTile - 1) / kTile;
+  }
+  for (int b = cta; b < p.B; b += gridDim.x) {     // empty requests: o = 0, lse = -inf
+    if (request_len(p, b, false) != 0) continue;
+    for (int e = tid; e < p.Hq * D; e += kThreads) {
+      store_o(p, b, e / D, e % D, 0.f);
+      if (e % D == 0 && p.lse) p.lse[static_cast<int64_t>(b) * p.Hq + e / D] = -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 16; i; i >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, i);
+  if (lane == 0) sh_scan[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sh_scan[w];
+  total *= units;
+  int64_t span = (total + gridDim.x - 1) / gridDim.x;
+  if (span < p.min_span) span = p.min_span;
+  const int64_t x_begin = cta * span;
+  const int64_t x_end = x_begin + span < total ? x_begin + span : total;
+  if (x_begin >= x_end) return;
+  __syncthreads();
+  {
+    int64_t done = 0;      // tiles of the requests before this block of kThreads
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      const int64_t n = b < p.B ? static_cast<int64_t>(request_len(p, b, false) + kTile - 1) / kTile * units : 0;
+      int64_t inc = n;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, i);
+        if (lane >= i) inc += o;
+      }
+      if (lane == 31) sh_scan[warp] = inc;
+      __syncthreads();
+      int64_t before = done, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh_scan[w];
+        all += sh_scan[w];
+      }
+      const int64_t start = before + inc - n;
+      if (n > 0 && x_begin >= start && x_begin < start + n) {
+        sh_b = b;
+        sh_base = start;
+      }
+      done += all;
+      __syncthreads();
+      if (done > x_begin) break;
+    }
+  }
+  int b = sh_b;
+  int64_t base = sh_base;              // the line position of request b's first tile
+  int len = request_len(p, b, false);
+  int n_tiles = (len + kTile - 1) / kTile;
+
+  const uint32_t ring = smem_u32(smem) + warp * S::kWarpBytes;
+  const float kscale = kFp8 ? __ldg(p.k_scale) : 1.f;
+  const float vscale = kFp8 ? __ldg(p.v_scale) : 1.f;
+  const int g = lane >> 2, cq = lane & 3;
+
+  for (int64_t x = x_begin; x < x_end;) {
+    while (x >= base + static_cast<int64_t>(n_tiles) * units) {   // the next request with work
+      base += static_cast<int64_t>(n_tiles) * units;
+      ++b;
+      len = request_len(p, b, false);
+      n_tiles = (len + kTile - 1) / kTile;
+    }
+    const int u = static_cast<int>((x - base) / n_tiles);
+    const int64_t u0 = base + static_cast<int64_t>(u) * n_tiles;   // the unit's first tile
+    const int t0 = static_cast<int>(x - u0);
+    const int t1 = x_end - u0 < n_tiles ? static_cast<int>(x_end - u0) : n_tiles;
+    x = u0 + t1;
+    const int hk = u / p.chunks;
+    const int h0 = (u - hk * p.chunks) * kHeads;                   // first head of the chunk
+    const int nh = p.G - h0 < kHeads ? p.G - h0 : kHeads;
+    const int64_t idx0 = p.kv_indptr[b];
+
+    // ---- loads of one tile: its page ids one tile ahead, then 16-byte cp.asyncs
+    const uint8_t* kh = p.k + hk * p.head_pitch;
+    const uint8_t* vh = p.v + hk * p.head_pitch;
+    const int ps_mask = (1 << p.log2_page) - 1;
+    auto page_of = [&](int t) -> int {       // lane's page id for tile t (-1: no position)
+      const int j = t * kTile + (lane & (kTile - 1));
+      return t < t1 && j < len ? __ldg(p.kv_indices + idx0 + (j >> p.log2_page)) : -1;
+    };
+    auto issue = [&](int t, int stage, int page) {
+      if (t < t1) {
+        const int j = t * kTile + (lane & (kTile - 1));
+        int64_t off = -1;
+        if (j < len) {
+          if (page >= 0 && page < p.n_pages) off = page * p.page_pitch + (j & ps_mask) * p.slot_pitch;
+          else atomicOr(p.err, kErrBadRowId);                      // reads as zeros
+        }
+        constexpr int kChunks = kRow / 16, kRowsAt = 32 / kChunks;
+        const uint32_t dst = ring + stage * S::kTileBytes;
+        const int c = lane % kChunks;
+#pragma unroll
+        for (int i = 0; i < kTile / kRowsAt; ++i) {
+          const int r = i * kRowsAt + lane / kChunks;
+          const int64_t ro = __shfl_sync(0xffffffffu, off, r);
+          const uint32_t n = ro >= 0 ? 16u : 0u;
+          const int64_t at = (ro >= 0 ? ro : 0) + 16 * c;
+          const uint32_t d = dst + chunk_at<kRow>(r, c);
+          cp_async_16(d, kh + at, n);
+          cp_async_16(d + kTile * kRow, vh + at, n);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int t_load = t0 + warp;
+    int page = page_of(t_load);
+#pragma unroll 1
+    for (int s = 0; s < S::kStages - 1; ++s) {
+      const int next = page_of(t_load + kWarps);
+      issue(t_load, s, page);
+      page = next;
+      t_load += kWarps;
+    }
+
+    // ---- q fragments: head 8 nt + g, columns as the K fragments hold them
+    uint32_t qf[NT][D / 16][2];
+    float sc[NT][2];                   // softmax scale in log2 units of heads 2 cq, 2 cq + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = 8 * nt + g;
+      const bool live = h < nh;
+      const uint16_t* row = p.q + b * p.q_tok + (static_cast<int64_t>(hk) * p.G + h0 + (live ? h : 0)) * p.q_head;
+      if constexpr (!kFp8) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qf[nt][kk][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(row + 16 * kk + 2 * cq)) : 0u;
+          qf[nt][kk][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(row + 16 * kk + 8 + 2 * cq)) : 0u;
+        }
+        sc[nt][0] = sc[nt][1] = p.sm_scale * kLog2e;
+      } else {
+        // the fragment's k columns 2cq, 2cq+1, 8+2cq, 9+2cq are the row's 4cq .. 4cq+3
+        float mx = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(row + 16 * kk + 4 * cq)) : make_uint2(0, 0);
+          qf[nt][kk][0] = w.x;
+          qf[nt][kk][1] = w.y;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx = fmaxf(mx, fabsf(__uint_as_float(qf[nt][kk][i] << 16)));
+            mx = fmaxf(mx, fabsf(__uint_as_float(qf[nt][kk][i] & 0xFFFF0000u)));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = 267 - static_cast<int>(__float_as_uint(mx) >> 23);   // 2^(13 - exponent), biased
+        e = e > 253 ? 253 : e;
+        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[nt][kk][i];
+            qf[nt][kk][i] = f32x2_to_f16x2(__uint_as_float(w & 0xFFFF0000u) * up, __uint_as_float(w << 16) * up);
+          }
+        // heads 2cq and 2cq+1 of this n-tile: their q rows sit at lanes 8cq and 8cq+4
+        const float d0 = __shfl_sync(0xffffffffu, down, 8 * cq);
+        const float d1 = __shfl_sync(0xffffffffu, down, 8 * cq + 4);
+        const float f = p.sm_scale * kscale * kLog2e;
+        sc[nt][0] = f * d0;
+        sc[nt][1] = f * d1;
+      }
+    }
+
+    float acc[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    int stage = 0;
+#pragma unroll 1
+    for (int t = t0 + warp; t < t1; t += kWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+      __syncwarp();                        // every lane's part of the tile; the freed stage too
+      {
+        const int next = page_of(t_load + kWarps);
+        int s = stage + S::kStages - 1;
+        if (s >= S::kStages) s -= S::kStages;
+        issue(t_load, s, page);
+        page = next;
+        t_load += kWarps;
+      }
+      const uint32_t kt = ring + stage * S::kTileBytes, vt = kt + kTile * kRow;
+
+      float sT[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sT[nt][0] = sT[nt][1] = sT[nt][2] = sT[nt][3] = 0.f;
+      if constexpr (!kFp8) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t a[4];
+          ldsm4(kt + chunk_at<kRow>(lane & 15, 2 * kk + (lane >> 4)), a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<false>(sT[nt], a, qf[nt][kk][0], qf[nt][kk][1]);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+          uint32_t r[4];                   // rows g / g+8, bytes 4cq..4cq+3 of two 16-column steps
+          ldsm4(kt + chunk_at<kRow>(lane & 15, 2 * kk + (lane >> 4)), r);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * i]), e4m3x2_to_f16x2(r[2 * i + 1]),
+                                   e4m3x2_to_f16x2(r[2 * i] >> 16), e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<true>(sT[nt], a, qf[nt][2 * kk + i][0], qf[nt][2 * kk + i][1]);
+          }
+        }
+      }
+      // ---- softmax over the tile's 16 positions (rows g, g + 8), per head (columns)
+      const int j0 = t * kTile + g;
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mt[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sT[nt][i] = j0 < len ? sT[nt][i] * sc[nt][i] : -INFINITY;
+          sT[nt][2 + i] = j0 + 8 < len ? sT[nt][2 + i] * sc[nt][i] : -INFINITY;
+          mt[i] = fmaxf(sT[nt][i], sT[nt][2 + i]);
+        }
+#pragma unroll
+        for (int x16 = 4; x16 < 32; x16 <<= 1) {
+          mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], x16));
+          mt[1] = fmaxf(mt[1], __shfl_xor_sync(0xffffffffu, mt[1], x16));
+        }
+        const bool grew = mt[0] > m[nt][0] || mt[1] > m[nt][1];
+        if (__any_sync(0xffffffffu, grew)) {
+          float f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mn = fmaxf(m[nt][i], mt[i]);
+            // nothing finite yet: the old sum is zero and stays so
+            f[i] = m[nt][i] == -INFINITY ? 0.f : ex2_approx(m[nt][i] - mn);
+            m[nt][i] = mn;
+            l[nt][i] *= f[i];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[nt][i][0] *= f[0];
+            acc[nt][i][1] *= f[1];
+            acc[nt][i][2] *= f[0];
+            acc[nt][i][3] *= f[1];
+          }
+        }
+        // weights; with e4m3 they carry 2^14, in l too
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float mm = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
+          w[i] = ex2_approx(sT[nt][i] - mm + (kFp8 ? 14.f : 0.f));
+          l[nt][i & 1] += w[i];
+        }
+        pf[nt][0] = transpose8x8(kFp8 ? f32x2_to_f16x2(w[1], w[0]) : pack_bf16(w[0], w[1]));
+        pf[nt][1] = transpose8x8(kFp8 ? f32x2_to_f16x2(w[3], w[2]) : pack_bf16(w[2], w[3]));
+      }
+      // ---- O^T += V^T . P^T
+      const int vr = (lane & 7) + ((lane >> 4) << 3);      // position row of the transposed load
+      const int vc = (lane >> 3) & 1;
+      if constexpr (!kFp8) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t a[4];                   // columns 16 i + g / + 8, positions 2cq.. / + 8
+          ldsm4_t(vt + chunk_at<kRow>(vr, 2 * i + vc), a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[nt][i], a, pf[nt][0], pf[nt][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          // each register: column pair (2g, 2g+1) of a 16-column group at positions 2cq, 2cq+1
+          uint32_t r[4];
+          ldsm4_t(vt + chunk_at<kRow>(vr, 2 * i + vc), r);
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const uint32_t lo = __byte_perm(r[k2], 0, 0x3120), hi = __byte_perm(r[k2 + 2], 0, 0x3120);
+            const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
+                                   e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(acc[nt][2 * i + k2], a, pf[nt][0], pf[nt][1]);
+          }
+        }
+      }
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // ---- the piece's four partial results meet in shared memory (over the idle rings)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x16 = 4; x16 < 32; x16 <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x16);
+        if (g == 0) {
+          s_m[warp * kHeads + 8 * nt + 2 * cq + i] = m[nt][i];
+          s_l[warp * kHeads + 8 * nt + 2 * cq + i] = l[nt][i];
+        }
+      }
+    __syncthreads();                       // rings idle in every warp, m and l written
+    float* s_o = reinterpret_cast<float*>(smem);            // [warp][head][D]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int h = 8 * nt + 2 * cq + (j & 1);
+          const int d = kFp8 ? 16 * i + 2 * g + (j >> 1) : 16 * i + g + 8 * (j >> 1);
+          s_o[(warp * kHeads + h) * D + d] = acc[nt][i][j];
+        }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == n_tiles;
+    float* slot = p.slots + (2 * static_cast<int64_t>(cta) + (t0 == 0 ? 1 : 0)) * S::kSlotFloats;
+    for (int e = tid; e < nh * D; e += kThreads) {
+      const int h = e / D, d = e - h * D;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * kHeads + h]);
+      float ll = 0.f, oo = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = s_m[w * kHeads + h];
+        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mm);
+        // a warp with no position keeps m = -inf, l = 0; one whose scores are all -inf or
+        // NaN keeps its l
+        ll += mw == -INFINITY ? s_l[w * kHeads + h] : f * s_l[w * kHeads + h];
+        oo += mw == -INFINITY ? s_o[(w * kHeads + h) * D + d] : f * s_o[(w * kHeads + h) * D + d];
+      }
+      if (whole) {
+        const int hq = hk * p.G + h0 + h;
+        const bool none = ll == 0.f;
+        store_o(p, b, hq, d, none ? 0.f : oo / ll * vscale);
+        if (d == 0 && p.lse)
+          p.lse[static_cast<int64_t>(b) * p.Hq + hq] =
+              none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - (kFp8 ? 14.f * kLn2 : 0.f);
+      } else {
+        slot[2 * kHeads + e] = oo;
+        if (d == 0) {
+          slot[h] = mm;
+          slot[kHeads + h] = ll;
+        }
+      }
+    }
+    if (!whole) {
+      // ---- the last span to arrive joins the unit's pieces, in the spans' order
+      const int64_t first = u0 / span, last = (u0 + n_tiles - 1) / span;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        int* c = p.counters + first;
+        const int seen = atomicAdd(c, 1);
+        sh_last = seen == last - first;
+        if (sh_last) *c = 0;               // as it was found, for the next call
+      }
+      __syncthreads();
+      if (sh_last) {
+        __threadfence();
+        for (int e = tid; e < nh * D; e += kThreads) {
+          const int h = e / D, d = e - h * D;
+          float mm = -INFINITY, ll = 0.f, oo = 0.f;
+          for (int64_t w = first; w <= last; ++w) {
+            const float* sl = p.slots + (2 * w + (w == first ? 1 : 0)) * S::kSlotFloats;
+            const float mw = __ldcg(sl + h), lw = __ldcg(sl + kHeads + h), ow = __ldcg(sl + 2 * kHeads + e);
+            const float mn = fmaxf(mm, mw);
+            const float f0 = mm == -INFINITY ? 1.f : ex2_approx(mm - mn);
+            const float f1 = mw == -INFINITY ? 1.f : ex2_approx(mw - mn);
+            ll = ll * f0 + lw * f1;
+            oo = oo * f0 + ow * f1;
+            mm = mn;
+          }
+          const int hq = hk * p.G + h0 + h;
+          const bool none = ll == 0.f;
+          store_o(p, b, hq, d, none ? 0.f : oo / ll * vscale);
+          if (d == 0 && p.lse)
+            p.lse[static_cast<int64_t>(b) * p.Hq + hq] =
+                none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - (kFp8 ? 14.f * kLn2 : 0.f);
+        }
+      }
+    }
+    __syncthreads();                       // the rings are free for the next piece
+  }
+}
+
+int ctas_for(int* out) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  *out = sms * kCtasPerSm;
+  return MLA_OK;
+}
+
+int head_tiles(int64_t G) { return G <= 8 ? 1 : (G <= 16 ? 2 : 4); }
+
+size_t workspace_for(int ctas, int64_t G, int64_t D) {
+  const size_t counters = (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256;
+  return kHeaderBytes + counters +
+         2 * static_cast<size_t>(ctas) * 8 * head_tiles(G) * static_cast<size_t>(D + 2) * 4;
+}
+
+template <int D, bool kFp8, int NT>
+cudaError_t launch(const GqaDecodeParams& p, int ctas, cudaStream_t stream) {
+  using S = DecodeShape<D, kFp8, NT>;
+  static std::mutex mu;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!attr_set[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(gqa_decode_kernel<S>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      if (e != cudaSuccess) return e;
+      attr_set[dev] = true;
+    }
+  }
+  gqa_decode_kernel<S><<<ctas, kThreads, S::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kFp8>
+cudaError_t launch_nt(const GqaDecodeParams& p, int ctas, cudaStream_t s) {
+  switch (head_tiles(p.G)) {
+    case 1: return launch<D, kFp8, 1>(p, ctas, s);
+    case 2: return launch<D, kFp8, 2>(p, ctas, s);
+    default: return launch<D, kFp8, 4>(p, ctas, s);
+  }
+}
+
+}  // namespace
+
+extern "C" int mla_get_gqa_decode_workspace_size(int32_t batch_size, int32_t num_heads,
+                                                 int32_t num_kv_heads, int32_t head_dim,
+                                                 int32_t num_sms, size_t* bytes_out) {
+  if (!bytes_out || batch_size < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads > 1024 ||
+      num_heads % num_kv_heads != 0 || head_dim < 1 || num_sms > 65536)
+    return MLA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return MLA_ERR_UNSUPPORTED;
+  int ctas = num_sms * kCtasPerSm;
+  if (num_sms <= 0) {
+    const int st = ctas_for(&ctas);
+    if (st != MLA_OK) return st;
+  }
+  *bytes_out = workspace_for(ctas, num_heads / num_kv_heads, head_dim);
+  return MLA_OK;
+}
+
+extern "C" int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache,
+                              const mla_tensor_t* v_cache, const mla_tensor_t* o,
+                              const mla_tensor_t* kv_indptr, const mla_tensor_t* kv_indices,
+                              const mla_tensor_t* kv_last_page_lens, float sm_scale,
+                              const mla_tensor_t* k_scale, const mla_tensor_t* v_scale,
+                              const mla_tensor_t* lse_out, void* workspace, size_t workspace_bytes,
+                              mla_stream_t stream_) {
+  if (!q || !k_cache || q->ndim != 3 || k_cache->ndim != 4) return MLA_ERR_INVALID_ARG;
+  const int64_t B = q->shape[0], Hq = q->shape[1], D = q->shape[2], Hk = k_cache->shape[2];
+  if (B < 0 || B > 0xFFFFFF || Hq < 1 || Hq > 1024 || Hk < 1 || Hq % Hk != 0) return MLA_ERR_INVALID_ARG;
+  if (!gqa_check_bf16(q, B, Hq, D, 8)) return MLA_ERR_INVALID_ARG;
+  GqaCache c;
+  const int st = gqa_check_cache(k_cache, v_cache, k_scale, v_scale, Hk, D, &c);
+  if (st != MLA_OK) return st;
+  if (!o || (!o->ptr && B > 0) || o->ndim != 3 || (o->dtype != MLA_DTYPE_BF16 && o->dtype != MLA_DTYPE_FP32) ||
+      o->shape[0] != B || o->shape[1] != Hq || o->shape[2] != D || o->stride[2] != 1 ||
+      o->stride[0] < 0 || o->stride[1] < 0 || !gqa_aligned(o->ptr, o->dtype == MLA_DTYPE_FP32 ? 4 : 2))
+    return MLA_ERR_INVALID_ARG;
+  if (!gqa_check_i32(kv_indptr, B + 1)) return MLA_ERR_INVALID_ARG;
+  if (!kv_indices || kv_indices->ndim != 1 || !gqa_check_i32(kv_indices, kv_indices->shape[0]))
+    return MLA_ERR_INVALID_ARG;
+  if (c.log2_page > 0 && !kv_last_page_lens) return MLA_ERR_INVALID_ARG;
+  if (kv_last_page_lens && !gqa_check_i32(kv_last_page_lens, B)) return MLA_ERR_INVALID_ARG;
+  if (lse_out && ((!lse_out->ptr && B > 0) || lse_out->dtype != MLA_DTYPE_FP32 || lse_out->ndim != 2 ||
+                  lse_out->shape[0] != B || lse_out->shape[1] != Hq || (Hq > 1 && lse_out->stride[1] != 1) ||
+                  (B > 1 && lse_out->stride[0] != Hq) || !gqa_aligned(lse_out->ptr, 4)))
+    return MLA_ERR_INVALID_ARG;
+  if (!(sm_scale == sm_scale)) return MLA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return MLA_ERR_UNSUPPORTED;
+  if (!workspace || !gqa_aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  const int64_t G = Hq / Hk;
+  if (workspace_bytes < workspace_for(1, G, D)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  int ctas = 0;
+  const int cs = ctas_for(&ctas);
+  if (cs != MLA_OK) return cs;
+  if (workspace_bytes < workspace_for(ctas, G, D)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (B == 0) return MLA_OK;
+
+  GqaDecodeParams p;
+  p.q = static_cast<const uint16_t*>(q->ptr);
+  p.q_tok = q->stride[0];
+  p.q_head = q->stride[1];
+  p.k = c.k;
+  p.v = c.v;
+  p.page_pitch = c.page_pitch;
+  p.slot_pitch = c.slot_pitch;
+  p.head_pitch = c.head_pitch;
+  p.log2_page = c.log2_page;
+  p.n_pages = c.n_pages;
+  p.kv_indptr = static_cast<const int32_t*>(kv_indptr->ptr);
+  p.kv_indices = static_cast<const int32_t*>(kv_indices->ptr);
+  p.last = kv_last_page_lens ? static_cast<const int32_t*>(kv_last_page_lens->ptr) : nullptr;
+  p.n_idx = kv_indices->shape[0];
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.sm_scale = sm_scale;
+  p.o = o->ptr;
+  p.o_f32 = o->dtype == MLA_DTYPE_FP32;
+  p.o_tok = o->stride[0];
+  p.o_head = o->stride[1];
+  p.lse = lse_out ? static_cast<float*>(lse_out->ptr) : nullptr;
+  p.B = static_cast<int>(B);
+  p.Hq = static_cast<int>(Hq);
+  p.Hk = static_cast<int>(Hk);
+  p.G = static_cast<int>(G);
+  p.chunks = static_cast<int>((G + 8 * head_tiles(G) - 1) / (8 * head_tiles(G)));
+  p.min_span = 8;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.err = reinterpret_cast<int*>(ws);
+  p.counters = reinterpret_cast<int*>(ws + kHeaderBytes);
+  p.slots = reinterpret_cast<float*>(ws + kHeaderBytes + (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e;
+  if (D == 64) e = c.fp8 ? launch_nt<64, true>(p, ctas, s) : launch_nt<64, false>(p, ctas, s);
+  else e = c.fp8 ? launch_nt<128, true>(p, ctas, s) : launch_nt<128, false>(p, ctas, s);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
