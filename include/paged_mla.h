@@ -380,6 +380,34 @@ int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla
                    mla_stream_t stream);
 
 /*
+ * Causal attention of whole prompts packed one after another, grouped heads.  Request b has
+ * T_b = qo_indptr[b+1] - qo_indptr[b] query tokens and L_b = kv_indptr[b+1] - kv_indptr[b]
+ * key positions, the last T_b of which are the queries' own (L_b > T_b: a prefix cached
+ * before; L_b < T_b: the first queries see nothing).  Query t, head h, KV head h / G:
+ *   J = { j : 0 <= j <= L_b - T_b + t },  s_j = sm_scale * sum_d q[r, h, d] * k[i_j, h/G, d]
+ *   lse = ln sum_{j in J} exp(s_j),  o[r, h] = sum_{j in J} exp(s_j - lse) * v[i_j, h/G]
+ * with r = qo_indptr[b] + t, i_j = kv_indptr[b] + j.  An empty J gives o = 0, lse = -inf.
+ * Values outside J (later positions, other requests, anything past the last row) do not
+ * reach a row, infinities and NaN among them.
+ *   q         (n_tok, Hq, D) BF16, k (n_keys, Hk, D) BF16, v (n_keys, Hk, Dv) BF16 with
+ *             (D, Dv) = (64, 64), (128, 128) or (192, 128), Hq / Hk <= 128; each: last dim
+ *             contiguous, 16-byte aligned, other strides positive multiples of 8 elements
+ *   o         (n_tok, Hq, Dv) BF16, strides non-negative multiples of 8, 16-byte aligned
+ *             (written); rows of no request are not
+ *   qo_indptr, kv_indptr  (B+1,) INT32
+ *   sm_scale  positive and finite
+ *   lse_out   (n_tok, Hq) FP32 contiguous, or NULL
+ *   error_word  device int32 (required): a request whose query range is not one inside
+ *             n_tok is left out, one whose key range is not inside n_keys has no keys; both
+ *             set bit 2.  Bit 4: a wait inside the kernel ran out (outputs not written).
+ * Other head widths and larger groups return MLA_ERR_UNSUPPORTED.  Asynchronous on `stream`.
+ */
+int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k, const mla_tensor_t* v,
+                         const mla_tensor_t* o, const mla_tensor_t* qo_indptr,
+                         const mla_tensor_t* kv_indptr, float sm_scale,
+                         const mla_tensor_t* lse_out, int32_t* error_word, mla_stream_t stream);
+
+/*
  * Debug check of a decode call's index inputs on the device, then a host status:
  * MLA_OK, MLA_ERR_BAD_INPUT (indptr not monotone or not starting at 0 for qo, kv_len <
  * q_len, kv_last_page_lens outside [1, PS] (!= 1 when PS = 1), qo_indptr[B] != sum_T) or

@@ -29,6 +29,7 @@ __all__ = [
     "mla_status_string", "make_workspace", "library_path", "PreparedDecode", "mla_latent_to_v",
     "mla_selftest_bounded_wait", "mla_qk_rope_concat_and_cache", "mla_gqa_rope_and_cache",
     "mla_gqa_decode", "mla_get_gqa_decode_workspace_size", "make_gqa_decode_workspace",
+    "mla_prompt_attention",
 ]
 
 MLA_DTYPE_FP8_E4M3FN = 1
@@ -91,6 +92,8 @@ def _load() -> ctypes.CDLL:
                                                       ctypes.POINTER(c_sz)]
     lib.mla_gqa_decode.restype = ctypes.c_int
     lib.mla_gqa_decode.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P, vp, c_sz, vp]
+    lib.mla_prompt_attention.restype = ctypes.c_int
+    lib.mla_prompt_attention.argtypes = [P, P, P, P, P, P, ctypes.c_float, P, vp, vp]
     lib.mla_selftest_bounded_wait.restype = ctypes.c_int
     lib.mla_selftest_bounded_wait.argtypes = [vp, vp, ctypes.c_int64, vp]
     return lib
@@ -424,6 +427,17 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
                              workspace.numel() * workspace.element_size(), _stream(stream, q.device))
     _check(rc, "mla_gqa_decode")
     return workspace
+
+
+def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word, lse_out=None,
+                         stream=None):
+    """Causal attention of packed whole prompts (see include/paged_mla.h).  error_word: an
+    int32 device tensor (>= 1 element)."""
+    ew = _error_word(error_word, q.device)
+    d = [_desc(t) for t in (q, k, v, o, qo_indptr, kv_indptr, lse_out)]
+    r = [_ref(x) for x in d]
+    rc = _lib.mla_prompt_attention(*r[:6], float(sm_scale), r[6], ew, _stream(stream, q.device))
+    _check(rc, "mla_prompt_attention")
 
 
 def mla_selftest_bounded_wait(error_word, result, limit_ns, stream=None):

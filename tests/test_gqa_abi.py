@@ -165,3 +165,48 @@ def test_error_word_is_checked(pm):
     x = torch.zeros(1)
     with pytest.raises(ValueError):
         pm.mla_gqa_rope_and_cache(x, x, x, x, x, 0, x, x, x, x, torch.zeros(1))
+
+
+def _prompt_args(pm):
+    Hq, Hk, D = 8, 2, 128
+    return dict(q=_t(pm, 0, BF, [7, Hq, D]), k=_t(pm, 1, BF, [9, Hk, D]), v=_t(pm, 2, BF, [9, Hk, D]),
+                o=_t(pm, 3, BF, [7, Hq, D]), qo=_t(pm, 4, I32, [3]), kv=_t(pm, 5, I32, [3]), sm=0.1,
+                lse=_t(pm, 6, F32, [7, Hq]), err=BASE + (7 << 28))
+
+
+def _prompt(pm, a):
+    return pm._lib.mla_prompt_attention(_r(a["q"]), _r(a["k"]), _r(a["v"]), _r(a["o"]), _r(a["qo"]),
+                                        _r(a["kv"]), a["sm"], _r(a["lse"]), ctypes.c_void_p(a["err"]), None)
+
+
+@pytest.mark.parametrize("name,change,status", [
+    ("q type", lambda pm: dict(q=_t(pm, 0, F32, [7, 8, 128])), INVALID),
+    ("q missing", lambda pm: dict(q=None), INVALID),
+    ("q head stride 0", lambda pm: dict(q=_t(pm, 0, BF, [7, 8, 128], [1024, 0, 1])), INVALID),
+    ("k head stride 0", lambda pm: dict(k=_t(pm, 1, BF, [9, 2, 128], [256, 0, 1])), INVALID),
+    ("k base", lambda pm: dict(k=_t(pm, 1, BF, [9, 2, 128], ptr=BASE + 2)), INVALID),
+    ("heads not grouped", lambda pm: dict(k=_t(pm, 1, BF, [9, 3, 128]), v=_t(pm, 2, BF, [9, 3, 128])), INVALID),
+    ("k and v lengths", lambda pm: dict(v=_t(pm, 2, BF, [8, 2, 128])), INVALID),
+    ("o width", lambda pm: dict(o=_t(pm, 3, BF, [7, 8, 64])), INVALID),
+    ("o type", lambda pm: dict(o=_t(pm, 3, F32, [7, 8, 128])), INVALID),
+    ("indptr lengths differ", lambda pm: dict(kv=_t(pm, 5, I32, [4])), INVALID),
+    ("indptr empty", lambda pm: dict(qo=_t(pm, 4, I32, [0])), INVALID),
+    ("scale zero", lambda pm: dict(sm=0.0), INVALID),
+    ("scale negative", lambda pm: dict(sm=-1.0), INVALID),
+    ("scale NaN", lambda pm: dict(sm=float("nan")), INVALID),
+    ("scale infinite", lambda pm: dict(sm=float("inf")), INVALID),
+    ("lse shape", lambda pm: dict(lse=_t(pm, 6, F32, [7, 2])), INVALID),
+    ("no error word", lambda pm: dict(err=0), INVALID),
+    ("head widths", lambda pm: dict(v=_t(pm, 2, BF, [9, 2, 64]), o=_t(pm, 3, BF, [7, 8, 64])), UNSUPPORTED),
+    ("group too large", lambda pm: dict(q=_t(pm, 0, BF, [7, 258, 128]), o=_t(pm, 3, BF, [7, 258, 128]),
+                                        lse=None), UNSUPPORTED),
+])
+def test_prompt_refuses(pm, name, change, status):
+    assert _prompt(pm, {**_prompt_args(pm), **change(pm)}) == status, name
+
+
+def test_prompt_of_nothing_is_ok(pm):
+    a = _prompt_args(pm)
+    a.update(q=_t(pm, 0, BF, [0, 8, 128], ptr=0), o=_t(pm, 3, BF, [0, 8, 128], ptr=0), lse=None)
+    assert _prompt(pm, a) == 0
+    assert _prompt(pm, {**_prompt_args(pm), "qo": _t(pm, 4, I32, [1]), "kv": _t(pm, 5, I32, [1])}) == 0
