@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -86,14 +87,14 @@ def _load() -> ctypes.CDLL:
     lib.mla_qk_rope_concat_and_cache.restype = ctypes.c_int
     lib.mla_qk_rope_concat_and_cache.argtypes = [P, P, P, P, P, P, c_i32, P, P, P, P, P, vp, vp]
     lib.mla_gqa_rope_and_cache.restype = ctypes.c_int
-    lib.mla_gqa_rope_and_cache.argtypes = [P, P, P, P, P, c_i32, P, P, P, P, P, P, P, vp, vp]
+    lib.mla_gqa_rope_and_cache.argtypes = [vp] * 5 + [c_i32] + [vp] * 9   # _packed() descriptors
     lib.mla_get_gqa_decode_workspace_size.restype = ctypes.c_int
     lib.mla_get_gqa_decode_workspace_size.argtypes = [c_i32, c_i32, c_i32, c_i32, c_i32,
                                                       ctypes.POINTER(c_sz)]
     lib.mla_gqa_decode.restype = ctypes.c_int
-    lib.mla_gqa_decode.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P, vp, c_sz, vp]
+    lib.mla_gqa_decode.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 4 + [c_sz, vp]
     lib.mla_prompt_attention.restype = ctypes.c_int
-    lib.mla_prompt_attention.argtypes = [P, P, P, P, P, P, ctypes.c_float, P, vp, vp]
+    lib.mla_prompt_attention.argtypes = [vp] * 6 + [ctypes.c_float] + [vp] * 3
     lib.mla_selftest_bounded_wait.restype = ctypes.c_int
     lib.mla_selftest_bounded_wait.argtypes = [vp, vp, ctypes.c_int64, vp]
     return lib
@@ -369,11 +370,48 @@ def mla_qk_rope_concat_and_cache(q_nope, q_pe, kv_c, k_pe, positions, cos_sin, i
     _check(rc, "mla_qk_rope_concat_and_cache")
 
 
+_TENSOR = struct.Struct("<Qii8q")     # mla_tensor_t: ptr, ndim, dtype, shape[4], stride[4]
+
+
+def _packed(t, device):
+    """The mla_tensor_t of a torch tensor on CUDA device `device` (an index) as bytes, whose
+    buffer ctypes passes as the pointer: a seventh of the time of filling the ctypes
+    structure, which one-shot calls of a few microseconds notice."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if t.get_device() != device:
+        raise ValueError(f"expected a tensor on CUDA device {device}, got one on {t.device}")
+    shape = t.shape
+    n = len(shape)
+    if n > 4:
+        raise ValueError("at most 4 dimensions")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    pad = _PAD[4 - n]
+    return _TENSOR.pack(t.data_ptr(), n, code, *shape, *pad, *t.stride(), *pad)
+
+
+def _cuda_index(t):
+    """The CUDA device index of the tensor that says where a call runs."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.get_device()
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _error_word(error_word, device):
     if not isinstance(error_word, torch.Tensor) or error_word.dtype != torch.int32 or \
-            error_word.numel() < 1 or error_word.device != device:
-        raise ValueError(f"error_word must be an int32 tensor on {device}")
-    return ctypes.c_void_p(error_word.data_ptr())
+            error_word.numel() < 1 or error_word.get_device() != device:
+        raise ValueError(f"error_word must be an int32 tensor on CUDA device {device}")
+    return error_word.data_ptr()
 
 
 def mla_gqa_rope_and_cache(q, k, v, positions, cos_sin, is_neox, slot_mapping, q_out, k_cache,
@@ -383,11 +421,13 @@ def mla_gqa_rope_and_cache(q, k, v, positions, cos_sin, is_neox, slot_mapping, q
     and values into the per-head caches at its slot (see include/paged_mla.h).  q_out and
     k_out may be q and k; k_scale and v_scale belong to e4m3 caches.  error_word: an int32
     device tensor (>= 1 element)."""
-    ew = _error_word(error_word, q.device)
-    d = [_desc(t) for t in (q, k, v, positions, cos_sin, slot_mapping, k_scale, v_scale, q_out,
-                            k_out, k_cache, v_cache)]
-    r = [_ref(x) for x in d]
-    rc = _lib.mla_gqa_rope_and_cache(*r[:5], int(is_neox), *r[5:], ew, _stream(stream, q.device))
+    d = _cuda_index(q)
+    ew = _error_word(error_word, d)
+    rc = _lib.mla_gqa_rope_and_cache(
+        _packed(q, d), _packed(k, d), _packed(v, d), _packed(positions, d), _packed(cos_sin, d),
+        int(is_neox), _packed(slot_mapping, d), _packed(k_scale, d), _packed(v_scale, d),
+        _packed(q_out, d), _packed(k_out, d), _packed(k_cache, d), _packed(v_cache, d), ew,
+        _raw_stream(stream, d))
     _check(rc, "mla_gqa_rope_and_cache")
 
 
@@ -413,6 +453,7 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
                    k_scale=None, v_scale=None, lse_out=None, workspace=None, stream=None):
     """Attention of one new token a request over paged per-head caches (see
     include/paged_mla.h).  Returns the workspace used."""
+    d = _cuda_index(q)
     if workspace is None:
         # made (and zeroed) on the stream that uses it
         st = stream if stream is None or isinstance(stream, torch.cuda.Stream) else \
@@ -420,11 +461,14 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
         with torch.cuda.stream(st):
             workspace = make_gqa_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[2],
                                                   q.shape[2], q.device)
-    d = [_desc(t) for t in (q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_lens,
-                            k_scale, v_scale, lse_out)]
-    r = [_ref(x) for x in d]
-    rc = _lib.mla_gqa_decode(*r[:7], float(sm_scale), *r[7:], ctypes.c_void_p(workspace.data_ptr()),
-                             workspace.numel() * workspace.element_size(), _stream(stream, q.device))
+    elif workspace.get_device() != d:
+        raise ValueError(f"the workspace must be on CUDA device {d}")
+    rc = _lib.mla_gqa_decode(
+        _packed(q, d), _packed(k_cache, d), _packed(v_cache, d), _packed(o, d),
+        _packed(kv_indptr, d), _packed(kv_indices, d), _packed(kv_last_page_lens, d),
+        float(sm_scale), _packed(k_scale, d), _packed(v_scale, d), _packed(lse_out, d),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _raw_stream(stream, d))
     _check(rc, "mla_gqa_decode")
     return workspace
 
@@ -433,10 +477,11 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
                          stream=None):
     """Causal attention of packed whole prompts (see include/paged_mla.h).  error_word: an
     int32 device tensor (>= 1 element)."""
-    ew = _error_word(error_word, q.device)
-    d = [_desc(t) for t in (q, k, v, o, qo_indptr, kv_indptr, lse_out)]
-    r = [_ref(x) for x in d]
-    rc = _lib.mla_prompt_attention(*r[:6], float(sm_scale), r[6], ew, _stream(stream, q.device))
+    d = _cuda_index(q)
+    ew = _error_word(error_word, d)
+    rc = _lib.mla_prompt_attention(
+        _packed(q, d), _packed(k, d), _packed(v, d), _packed(o, d), _packed(qo_indptr, d),
+        _packed(kv_indptr, d), float(sm_scale), _packed(lse_out, d), ew, _raw_stream(stream, d))
     _check(rc, "mla_prompt_attention")
 
 

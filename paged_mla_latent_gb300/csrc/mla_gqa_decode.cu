@@ -548,22 +548,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
       __syncthreads();
       if (sh_last) {
         __threadfence();
-        for (int e = tid; e < nh * D; e += kThreads) {
+        // a warp a head: the pieces' maxima and sums, lanes over pieces
+        const int np = static_cast<int>(last - first) + 1;
+        float* s_f = reinterpret_cast<float*>(smem);         // [piece][head], over the rings
+        auto slot_of = [&](int i) {
+          return p.slots + (2 * (first + i) + (i == 0 ? 1 : 0)) * S::kSlotFloats;
+        };
+        for (int h = warp; h < nh; h += kWarps) {
+          float mm = -INFINITY, ll = 0.f;
+          for (int i = lane; i < np; i += 32) {
+            const float mw = __ldcg(slot_of(i) + h);
+            s_f[i * kHeads + h] = mw;
+            mm = fmaxf(mm, mw);
+          }
+#pragma unroll
+          for (int x16 = 16; x16; x16 >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x16));
+          for (int i = lane; i < np; i += 32) {
+            const float mw = s_f[i * kHeads + h];
+            const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - mm);
+            s_f[i * kHeads + h] = f;
+            ll += f * __ldcg(slot_of(i) + kHeads + h);
+          }
+#pragma unroll
+          for (int x16 = 16; x16; x16 >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x16);
+          if (lane == 0) {
+            s_m[h] = mm;
+            s_l[h] = ll;
+          }
+        }
+        __syncthreads();
+        for (int e = 4 * tid; e < nh * D; e += 4 * kThreads) {
           const int h = e / D, d = e - h * D;
-          float mm = -INFINITY, ll = 0.f, oo = 0.f;
-          for (int64_t w = first; w <= last; ++w) {
-            const float* sl = p.slots + (2 * w + (w == first ? 1 : 0)) * S::kSlotFloats;
-            const float mw = __ldcg(sl + h), lw = __ldcg(sl + kHeads + h), ow = __ldcg(sl + 2 * kHeads + e);
-            const float mn = fmaxf(mm, mw);
-            const float f0 = mm == -INFINITY ? 1.f : ex2_approx(mm - mn);
-            const float f1 = mw == -INFINITY ? 1.f : ex2_approx(mw - mn);
-            ll = ll * f0 + lw * f1;
-            oo = oo * f0 + ow * f1;
-            mm = mn;
+          float oo[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+          for (int i = 0; i < np; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(slot_of(i) + 2 * kHeads + e));
+            const float f = s_f[i * kHeads + h];
+            oo[0] += f * x.x;
+            oo[1] += f * x.y;
+            oo[2] += f * x.z;
+            oo[3] += f * x.w;
           }
           const int hq = hk * p.G + h0 + h;
+          const float ll = s_l[h], mm = s_m[h];
           const bool none = ll == 0.f;
-          store_o(p, b, hq, d, none ? 0.f : oo / ll * vscale);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store_o(p, b, hq, d + i, none ? 0.f : oo[i] / ll * vscale);
           if (d == 0 && p.lse)
             p.lse[static_cast<int64_t>(b) * p.Hq + hq] =
                 none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - (kFp8 ? 14.f * kLn2 : 0.f);
