@@ -64,7 +64,6 @@ struct GqaDecodeParams {
   int64_t o_tok, o_head;
   float* lse;
   int B, Hq, Hk, G, chunks;
-  int min_span;
   int* err;
   int* counters;                     // one a CTA: the unit that leaves its span's end
   float* slots;                      // two a CTA: m[R], l[R], o[R][D] with R = 8 NT
@@ -120,7 +119,31 @@ struct DecodeShape {
   static constexpr int kBuf = kWarps * kWarpBytes > kJoinBytes ? kWarps * kWarpBytes : kJoinBytes;
   static constexpr int kSmem = kBuf + 2 * kWarps * kHeads * 4;
   static constexpr int kSlotFloats = kHeads * (D + 2);
+  // what a unit costs besides its tiles (page ids, the first tile's way from DRAM, the joins:
+  // about 2.5 us), in tiles at a CTA's share of the bandwidth (22 bytes a ns)
+  static constexpr int kUnitCost = 55000 / kTileBytes;
 };
+
+// Weight of one unit of a request on the line of work.
+template <class S>
+__device__ __forceinline__ int64_t line_weight(int len) {
+  return len > 0 ? (len + kTile - 1) / kTile + S::kUnitCost : 0;
+}
+
+// Where a span's border, x tiles into a unit of n, cuts it: pieces shorter than their fixed
+// cost go to the neighbouring span, so units of fewer than 2 kUnitCost tiles stay whole.
+template <class S>
+__device__ __forceinline__ int snap(int64_t x, int n) {
+  if (x >= n) return n;
+  if (x < S::kUnitCost) return 0;
+  return n - x < S::kUnitCost ? n : static_cast<int>(x);
+}
+
+// a / b for a >= 0, b > 0, by the 32-bit divide where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // Byte offset of 16-byte chunk c of row r: chunks are permuted within 128 bytes so that
 // eight rows' equal chunks fall into different banks.
@@ -164,72 +187,102 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
   float* s_l = s_m + kWarps * kHeads;
   __shared__ int64_t sh_scan[kWarps];
   __shared__ int64_t sh_base;
-  __shared__ int sh_b, sh_last;
+  __shared__ int sh_b, sh_len, sh_last, sh_empty;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int units = p.Hk * p.chunks;
   const int cta = blockIdx.x;
 
-  // ---- the line: total tiles, this CTA's span, and the request its span starts in
-  int64_t mine = 0;
+  // ---- the line: its length, this CTA's span, and the request its span starts in.  The
+  // first kThreads requests' lengths stay in registers, so that a batch of up to kThreads
+  // pays one round trip to memory here.
+  if (tid == 0) sh_empty = 0;
+  __syncthreads();
+  int64_t mine = 0, inc = 0;
+  int len0 = 0;
   for (int b = tid; b < p.B; b += kThreads) {
     const int len = request_len(p, b, cta == 0);
-    mine += (len + kTile - 1) / kTile;
+    if (b < kThreads) len0 = len;
+    mine += line_weight<S>(len);
+    if (len == 0 && b % gridDim.x == cta) sh_empty = 1;
   }
-  for (int b = cta; b < p.B; b += gridDim.x) {     // empty requests: o = 0, lse = -inf
-    if (request_len(p, b, false) != 0) continue;
-    for (int e = tid; e < p.Hq * D; e += kThreads) {
-      store_o(p, b, e / D, e % D, 0.f);
-      if (e % D == 0 && p.lse) p.lse[static_cast<int64_t>(b) * p.Hq + e / D] = -INFINITY;
-    }
-  }
+  const int64_t mine0 = line_weight<S>(len0);
+  inc = mine0;
 #pragma unroll
-  for (int i = 16; i; i >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, i);
+  for (int i = 1; i < 32; i <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, i);
+    if (lane >= i) inc += o;
+  }
+  if (p.B > kThreads) {
+#pragma unroll
+    for (int i = 16; i; i >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, i);
+  } else {
+    mine = __shfl_sync(0xffffffffu, inc, 31);
+  }
   if (lane == 0) sh_scan[warp] = mine;
   __syncthreads();
-  int64_t total = 0;
+  int64_t total = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sh_scan[w];
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh_scan[w];
+    total += sh_scan[w];
+  }
   total *= units;
-  int64_t span = (total + gridDim.x - 1) / gridDim.x;
-  if (span < p.min_span) span = p.min_span;
+  const int64_t span = quotient(total + gridDim.x - 1, gridDim.x);
   const int64_t x_begin = cta * span;
   const int64_t x_end = x_begin + span < total ? x_begin + span : total;
+  if (sh_empty)                                    // empty requests: o = 0, lse = -inf
+    for (int b = cta; b < p.B; b += gridDim.x) {
+      if (request_len(p, b, false) != 0) continue;
+      for (int e = tid; e < p.Hq * D; e += kThreads) {
+        store_o(p, b, e / D, e % D, 0.f);
+        if (e % D == 0 && p.lse) p.lse[static_cast<int64_t>(b) * p.Hq + e / D] = -INFINITY;
+      }
+    }
   if (x_begin >= x_end) return;
-  __syncthreads();
-  {
-    int64_t done = 0;      // tiles of the requests before this block of kThreads
+  if (p.B <= kThreads) {
+    const int64_t start = (before + inc - mine0) * units;
+    if (mine0 > 0 && x_begin >= start && x_begin < start + mine0 * units) {
+      sh_b = tid;
+      sh_len = len0;
+      sh_base = start;
+    }
+    __syncthreads();
+  } else {
+    int64_t done = 0;      // the line before this block of kThreads requests
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
       const int b = b0 + tid;
-      const int64_t n = b < p.B ? static_cast<int64_t>(request_len(p, b, false) + kTile - 1) / kTile * units : 0;
-      int64_t inc = n;
+      const int len = b < p.B ? request_len(p, b, false) : 0;
+      const int64_t n = line_weight<S>(len) * units;
+      int64_t run = n;
 #pragma unroll
       for (int i = 1; i < 32; i <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, inc, i);
-        if (lane >= i) inc += o;
+        const int64_t o = __shfl_up_sync(0xffffffffu, run, i);
+        if (lane >= i) run += o;
       }
-      if (lane == 31) sh_scan[warp] = inc;
       __syncthreads();
-      int64_t before = done, all = 0;
+      if (lane == 31) sh_scan[warp] = run;
+      __syncthreads();
+      int64_t start = done + run - n, all = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh_scan[w];
+        if (w < warp) start += sh_scan[w];
         all += sh_scan[w];
       }
-      const int64_t start = before + inc - n;
       if (n > 0 && x_begin >= start && x_begin < start + n) {
         sh_b = b;
+        sh_len = len;
         sh_base = start;
       }
       done += all;
-      __syncthreads();
       if (done > x_begin) break;
     }
+    __syncthreads();
   }
-  int b = sh_b;
-  int64_t base = sh_base;              // the line position of request b's first tile
-  int len = request_len(p, b, false);
+  int b = sh_b, len = sh_len;
+  int64_t base = sh_base;              // the line position of request b
   int n_tiles = (len + kTile - 1) / kTile;
+  int64_t weight = line_weight<S>(len);
 
   const uint32_t ring = smem_u32(smem) + warp * S::kWarpBytes;
   const float kscale = kFp8 ? __ldg(p.k_scale) : 1.f;
@@ -237,17 +290,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
   const int g = lane >> 2, cq = lane & 3;
 
   for (int64_t x = x_begin; x < x_end;) {
-    while (x >= base + static_cast<int64_t>(n_tiles) * units) {   // the next request with work
-      base += static_cast<int64_t>(n_tiles) * units;
+    while (x >= base + weight * units) {           // the next request with work
+      base += weight * units;
       ++b;
       len = request_len(p, b, false);
       n_tiles = (len + kTile - 1) / kTile;
+      weight = line_weight<S>(len);
     }
-    const int u = static_cast<int>((x - base) / n_tiles);
-    const int64_t u0 = base + static_cast<int64_t>(u) * n_tiles;   // the unit's first tile
-    const int t0 = static_cast<int>(x - u0);
-    const int t1 = x_end - u0 < n_tiles ? static_cast<int>(x_end - u0) : n_tiles;
-    x = u0 + t1;
+    const int u = static_cast<int>(quotient(x - base, weight));
+    const int64_t u0 = base + u * weight + S::kUnitCost;           // the unit's first tile
+    const int t0 = snap<S>(x_begin - u0, n_tiles), t1 = snap<S>(x_end - u0, n_tiles);
+    x = u0 + n_tiles;
+    if (t0 >= t1) continue;                        // the neighbours' spans have all of it
     const int hk = u / p.chunks;
     const int h0 = (u - hk * p.chunks) * kHeads;                   // first head of the chunk
     const int nh = p.G - h0 < kHeads ? p.G - h0 : kHeads;
@@ -257,30 +311,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
     const uint8_t* kh = p.k + hk * p.head_pitch;
     const uint8_t* vh = p.v + hk * p.head_pitch;
     const int ps_mask = (1 << p.log2_page) - 1;
+    const bool one_page = p.log2_page >= 4;    // a tile never crosses a page
     auto page_of = [&](int t) -> int {       // lane's page id for tile t (-1: no position)
-      const int j = t * kTile + (lane & (kTile - 1));
+      const int j = t * kTile + (one_page ? 0 : lane & (kTile - 1));
       return t < t1 && j < len ? __ldg(p.kv_indices + idx0 + (j >> p.log2_page)) : -1;
     };
+    constexpr int kChunks = kRow / 16, kRowsAt = 32 / kChunks;
+    const int lc = lane % kChunks, lr = lane / kChunks;
     auto issue = [&](int t, int stage, int page) {
       if (t < t1) {
-        const int j = t * kTile + (lane & (kTile - 1));
-        int64_t off = -1;
-        if (j < len) {
-          if (page >= 0 && page < p.n_pages) off = page * p.page_pitch + (j & ps_mask) * p.slot_pitch;
-          else atomicOr(p.err, kErrBadRowId);                      // reads as zeros
-        }
-        constexpr int kChunks = kRow / 16, kRowsAt = 32 / kChunks;
         const uint32_t dst = ring + stage * S::kTileBytes;
-        const int c = lane % kChunks;
+        const bool ok = page >= 0 && page < p.n_pages;
+        if (one_page) {
+          if (!ok && lane == 0) atomicOr(p.err, kErrBadRowId);     // reads as zeros
+          const int64_t off = ok ? page * p.page_pitch + ((t * kTile) & ps_mask) * p.slot_pitch : 0;
+          int64_t at = off + lr * p.slot_pitch + 16 * lc;
+          const int rows = ok ? len - t * kTile : 0;
 #pragma unroll
-        for (int i = 0; i < kTile / kRowsAt; ++i) {
-          const int r = i * kRowsAt + lane / kChunks;
-          const int64_t ro = __shfl_sync(0xffffffffu, off, r);
-          const uint32_t n = ro >= 0 ? 16u : 0u;
-          const int64_t at = (ro >= 0 ? ro : 0) + 16 * c;
-          const uint32_t d = dst + chunk_at<kRow>(r, c);
-          cp_async_16(d, kh + at, n);
-          cp_async_16(d + kTile * kRow, vh + at, n);
+          for (int i = 0; i < kTile / kRowsAt; ++i) {
+            const int r = i * kRowsAt + lr;
+            const uint32_t n = r < rows ? 16u : 0u;
+            const uint32_t d = dst + chunk_at<kRow>(r, lc);
+            cp_async_16(d, kh + (n ? at : 0), n);
+            cp_async_16(d + kTile * kRow, vh + (n ? at : 0), n);
+            at += kRowsAt * p.slot_pitch;
+          }
+        } else {
+          const int j = t * kTile + (lane & (kTile - 1));
+          int64_t off = -1;
+          if (j < len) {
+            if (ok) off = page * p.page_pitch + (j & ps_mask) * p.slot_pitch;
+            else atomicOr(p.err, kErrBadRowId);
+          }
+#pragma unroll
+          for (int i = 0; i < kTile / kRowsAt; ++i) {
+            const int r = i * kRowsAt + lr;
+            const int64_t ro = __shfl_sync(0xffffffffu, off, r);
+            const uint32_t n = ro >= 0 ? 16u : 0u;
+            const int64_t at = (ro >= 0 ? ro : 0) + 16 * lc;
+            const uint32_t d = dst + chunk_at<kRow>(r, lc);
+            cp_async_16(d, kh + at, n);
+            cp_async_16(d + kTile * kRow, vh + at, n);
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -536,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
     }
     if (!whole) {
       // ---- the last span to arrive joins the unit's pieces, in the spans' order
-      const int64_t first = u0 / span, last = (u0 + n_tiles - 1) / span;
+      const int64_t first = quotient(u0 + S::kUnitCost - 1, span);
+      const int64_t last = quotient(u0 + n_tiles - S::kUnitCost, span);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -734,7 +807,6 @@ extern "C" int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache
   p.Hk = static_cast<int>(Hk);
   p.G = static_cast<int>(G);
   p.chunks = static_cast<int>((G + 8 * head_tiles(G) - 1) / (8 * head_tiles(G)));
-  p.min_span = 8;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.err = reinterpret_cast<int*>(ws);
   p.counters = reinterpret_cast<int*>(ws + kHeaderBytes);
