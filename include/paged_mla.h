@@ -400,12 +400,26 @@ int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla
  *   error_word  device int32 (required): a request whose query range is not one inside
  *             n_tok is left out, one whose key range is not inside n_keys has no keys; both
  *             set bit 2.  Bit 4: a wait inside the kernel ran out (outputs not written).
+ *   workspace   NULL, or mla_get_prompt_workspace_size(...) bytes, 16-byte aligned (its
+ *             contents do not matter): with it, long stretches of keys are cut between the
+ *             SMs and joined by a second kernel, so that few or unequal requests fill the
+ *             GPU; without, a stretch stays on one SM.  Calls that share one must not
+ *             overlap on the GPU.
  * Other head widths and larger groups return MLA_ERR_UNSUPPORTED.  Asynchronous on `stream`.
  */
 int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k, const mla_tensor_t* v,
                          const mla_tensor_t* o, const mla_tensor_t* qo_indptr,
                          const mla_tensor_t* kv_indptr, float sm_scale,
-                         const mla_tensor_t* lse_out, int32_t* error_word, mla_stream_t stream);
+                         const mla_tensor_t* lse_out, int32_t* error_word, void* workspace,
+                         size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * Bytes of workspace for mla_prompt_attention calls over n_keys key rows in all (0 where no
+ * request can be long enough to be cut) on a GPU with num_sms SMs (<= 0: the current
+ * device's).
+ */
+int mla_get_prompt_workspace_size(int64_t n_keys, int32_t v_head_dim, int32_t num_sms,
+                                  size_t* bytes_out);
 
 /*
  * Debug check of a decode call's index inputs on the device, then a host status:

@@ -30,7 +30,7 @@ __all__ = [
     "mla_status_string", "make_workspace", "library_path", "PreparedDecode", "mla_latent_to_v",
     "mla_selftest_bounded_wait", "mla_qk_rope_concat_and_cache", "mla_gqa_rope_and_cache",
     "mla_gqa_decode", "mla_get_gqa_decode_workspace_size", "make_gqa_decode_workspace",
-    "mla_prompt_attention",
+    "mla_prompt_attention", "mla_get_prompt_workspace_size",
 ]
 
 MLA_DTYPE_FP8_E4M3FN = 1
@@ -94,7 +94,9 @@ def _load() -> ctypes.CDLL:
     lib.mla_gqa_decode.restype = ctypes.c_int
     lib.mla_gqa_decode.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 4 + [c_sz, vp]
     lib.mla_prompt_attention.restype = ctypes.c_int
-    lib.mla_prompt_attention.argtypes = [vp] * 6 + [ctypes.c_float] + [vp] * 3
+    lib.mla_prompt_attention.argtypes = [vp] * 6 + [ctypes.c_float] + [vp] * 3 + [c_sz, vp]
+    lib.mla_get_prompt_workspace_size.restype = ctypes.c_int
+    lib.mla_get_prompt_workspace_size.argtypes = [ctypes.c_int64, c_i32, c_i32, ctypes.POINTER(c_sz)]
     lib.mla_selftest_bounded_wait.restype = ctypes.c_int
     lib.mla_selftest_bounded_wait.argtypes = [vp, vp, ctypes.c_int64, vp]
     return lib
@@ -455,10 +457,7 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
     include/paged_mla.h).  Returns the workspace used."""
     d = _cuda_index(q)
     if workspace is None:
-        # made (and zeroed) on the stream that uses it
-        st = stream if stream is None or isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(int(stream), device=q.device)
-        with torch.cuda.stream(st):
+        with _on_stream(stream, q.device):      # made and zeroed on the stream that uses it
             workspace = make_gqa_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[2],
                                                   q.shape[2], q.device)
     elif workspace.get_device() != d:
@@ -473,15 +472,43 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
     return workspace
 
 
+def mla_get_prompt_workspace_size(n_keys: int, v_head_dim: int, num_sms: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.mla_get_prompt_workspace_size(n_keys, v_head_dim, num_sms, ctypes.byref(out)),
+           "mla_get_prompt_workspace_size")
+    return int(out.value)
+
+
+def _on_stream(stream, device):
+    """A context whose allocations belong to the stream a call runs on."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
+
+
 def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word, lse_out=None,
-                         stream=None):
+                         workspace=None, stream=None):
     """Causal attention of packed whole prompts (see include/paged_mla.h).  error_word: an
-    int32 device tensor (>= 1 element)."""
+    int32 device tensor (>= 1 element).  workspace: a device tensor of
+    mla_get_prompt_workspace_size bytes; without one the call takes it from torch's allocator
+    on the call's stream."""
     d = _cuda_index(q)
     ew = _error_word(error_word, d)
+    if workspace is None:
+        n = mla_get_prompt_workspace_size(k.shape[0], v.shape[2])
+        if n and stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        elif n:
+            with _on_stream(stream, q.device):
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != d:
+        raise ValueError(f"the workspace must be on CUDA device {d}")
+    ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
     rc = _lib.mla_prompt_attention(
         _packed(q, d), _packed(k, d), _packed(v, d), _packed(o, d), _packed(qo_indptr, d),
-        _packed(kv_indptr, d), float(sm_scale), _packed(lse_out, d), ew, _raw_stream(stream, d))
+        _packed(kv_indptr, d), float(sm_scale), _packed(lse_out, d), ew, ws, n,
+        _raw_stream(stream, d))
     _check(rc, "mla_prompt_attention")
 
 

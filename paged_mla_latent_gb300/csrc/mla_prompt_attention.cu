@@ -9,10 +9,17 @@
 // exponential each: bound by the MMAs (M = N = 128, K = 16 at 8192 operations a cycle and SM)
 // while the exponentials of one tile hide under the MMAs of another.
 //
-// One CTA per (256 query rows, KV head), two tiles of 128 rows.  A row is one (token, query
-// head) pair: a tile holds 128 / G tokens with all G heads of the group, so short prompts fill
-// the MMA's M, a K/V tile is read once for the whole group, and the causal edge wastes G times
-// fewer columns than a tile of one head's tokens.
+// Work.  A unit is 256 query rows of one KV head, two tiles of 128.  A row is one (token,
+// query head) pair: a tile holds 128 / G tokens with all G heads of the group, so short
+// prompts fill the MMA's M, a K/V tile is read once for the whole group, and the causal edge
+// wastes G times fewer columns than a tile of one head's tokens.  All units form one line,
+// each as long as the positions it reads plus a fixed cost, and each of one CTA a SM takes an
+// equal span of it.  A long unit is cut where a span ends: the parts leave (m, l, O) in fp32
+// in the workspace and a second kernel joins them (12 heads of 4,089 queries behind 63,911
+// positions are 192 units for 152 SMs: whole units would leave a third of the SMs idle).
+// Spans are worked off from their ends: neighbouring spans of one head, whose units are
+// equally long, then read the same K/V tiles at the same time, from L2.
+//
 //   warps 0-3, 4-7 : softmax of tile 0 / 1, a thread a row: S from tensor memory, maximum,
 //                    exponentials, P as bf16 back over S's columns.
 //   warp 8         : TMA.  K and V tiles of 128 positions come in 16 KB chunks of 64 columns
@@ -20,10 +27,11 @@
 //   warp 9         : tcgen05.mma issuer.  S = Q K^T from shared memory; O += P V with P (the A
 //                    operand) in tensor memory.  Order: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1),
 //                    so that one tile's MMAs run while the other's softmax does.
-//   warps 10-11    : for the tiles on the causal edge and at a request's end, zero the V rows
-//                    past the request (another request's, or stale memory) and take non-finite
-//                    values out of V (0 * inf would reach rows that do not see them); rows that
-//                    do see one get it back at the end.
+//   warp 10        : for the tiles on the causal edge and at a request's end, zeroes the V rows
+//                    past the request (another request's, or stale memory) and takes
+//                    non-finite values out of V (0 * inf would reach rows that do not see
+//                    them); rows that do see one get it back at the end.
+//   warp 11        : walks the span and queues its pieces for the others.
 // Tensor memory: S_0 S_1 O_0 O_1, 128 columns each (all 512); P_s lies over S_s.
 //
 // The running maximum is only raised when it would grow by more than 8 (in log2): then the
@@ -51,10 +59,19 @@ constexpr int kRows = 128;                 // query rows of a tile (the MMA's M)
 constexpr int kKeys = 128;                 // positions of a K/V tile
 constexpr int kChunk = 128 * 128;          // 128 rows of 64 bf16 columns
 constexpr int kThreads = 384;
-constexpr int kMaxEdge = 4;                // K/V tiles on the causal edge of a CTA (at most 3)
+constexpr int kEdges = 8;                  // barriers of edge tiles; the ring holds at most 6 V tiles
+constexpr int kQueue = 4;                  // pieces queued
+constexpr int kConsumers = 11;             // warps that read a queued piece
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;              // log2 growth of the maximum that forces a rescale
+
+// Fixed cost of a unit on the line (its Q, the first tile's way, its result) in positions,
+// and the fewest K/V tiles a part of a cut unit may have: writing and joining a part moves
+// 266 KB, about four tiles' time of an SM.
+constexpr int kUnitCost = 256;
+constexpr int kMinCut = 8;                 // a power of two
+constexpr int kMaxParts = 512;             // parts of one unit: at most one a span
 
 template <int D_, int DV_>
 struct PromptShape {
@@ -63,7 +80,8 @@ struct PromptShape {
   static constexpr int kQBytes = 2 * KC * kChunk;
   static constexpr int NC = 14 - 2 * KC;                   // ring chunks: 224 KB with Q
   static constexpr int kBarOff = kQBytes + NC * kChunk;
-  static constexpr int kSmem = kBarOff + 512 + 1024;       // barriers, alignment
+  static constexpr int kSmem = kBarOff + 1024 + 1024;      // barriers and queue, alignment
+  static constexpr int kPartFloats = 2 * kRows * (DV + 2); // a cut part: m, l, O
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -78,8 +96,151 @@ struct PromptParams {
   float* lse;
   const uint16_t* v;                       // for the rows that see a non-finite value
   int64_t v_tok, v_head;
+  float* parts;                            // two a CTA; null: units are not cut
   int* err;
 };
+
+// Part of a unit: K/V tiles [j0, j1).
+struct Piece {
+  int row0;         // first query token's row of q and o
+  int toks;         // query tokens from there to the request's end
+  int pos0;         // position of the first of them among the keys (negative: sees nothing)
+  int kv0;          // the request's first key row
+  int hk;
+  int j0, j1;
+  int part;         // where a cut piece leaves its result; -1: the unit is whole
+};
+
+// K/V tiles that tile s of a unit needs (its last token's).
+__device__ __forceinline__ int tiles_of(const Piece& w, int s, int tok_tile) {
+  const int a = s * tok_tile;
+  if (a >= w.toks) return 0;
+  const int seen = w.pos0 + (a + tok_tile < w.toks ? a + tok_tile : w.toks);
+  return seen > 0 ? (seen + kKeys - 1) / kKeys : 0;
+}
+// The first K/V tile of a piece that holds positions some row of the unit does not see.
+__device__ __forceinline__ int first_edge(const Piece& w) {
+  const int clear = w.pos0 + 1 > 0 ? (w.pos0 + 1) / kKeys : 0;
+  return clear > w.j0 ? clear : w.j0;
+}
+
+// ---- the line of work
+struct Request {
+  int q0, T, kv0, L;
+  int units;                               // units of one KV head
+  // line length of the first i units of a head
+  __device__ int64_t cum(int i, int cta_tok) const {
+    if (units == 0) return 0;
+    const int64_t fixed = kUnitCost + (L > T ? L - T : 0);
+    const int64_t full = i < units ? i : units - 1;
+    int64_t x = full * fixed + cta_tok * (full * (full + 1) / 2);
+    if (i >= units) x += fixed + T;
+    return x;
+  }
+};
+__device__ __forceinline__ Request load_request(const PromptParams& p, int b, int cta_tok, bool flag) {
+  Request r = {0, 0, 0, 0, 0};
+  const int64_t s = p.qo_indptr[b], e = p.qo_indptr[b + 1], ks = p.kv_indptr[b], ke = p.kv_indptr[b + 1];
+  if (s < 0 || e < s || e > p.n_tok) {     // the request is left out
+    if (flag) atomicOr(p.err, kErrBadIndptr);
+    return r;
+  }
+  r.q0 = static_cast<int>(s);
+  r.T = static_cast<int>(e - s);
+  r.units = (r.T + cta_tok - 1) / cta_tok;
+  if (ks < 0 || ke < ks || ke > p.n_keys) {   // no keys
+    if (flag) atomicOr(p.err, kErrBadIndptr);
+    return r;
+  }
+  r.kv0 = static_cast<int>(ks);
+  r.L = static_cast<int>(ke - ks);
+  return r;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, x, i);
+    if (lane >= i) x += o;
+  }
+  return x;
+}
+// Length of the whole line (a warp together).
+__device__ __forceinline__ int64_t line_total(const PromptParams& p, int cta_tok, int lane, bool flag) {
+  int64_t x = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const Request r = load_request(p, b, cta_tok, flag);
+    x += r.cum(r.units, cta_tok);
+  }
+#pragma unroll
+  for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+  return x * p.Hk;
+}
+// A unit and where it starts on the line.
+struct Unit {
+  Request r;
+  int b, hk, i;
+  int64_t u0;
+};
+// The unit that holds point x of the line, 0 <= x < total (a warp together).
+__device__ __forceinline__ Unit find_unit(const PromptParams& p, int cta_tok, int lane, int64_t x) {
+  Unit u;
+  u.b = 0;
+  int64_t done = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    Request r = {0, 0, 0, 0, 0};
+    if (b < p.B) r = load_request(p, b, cta_tok, false);
+    const int64_t n = r.cum(r.units, cta_tok) * p.Hk;
+    const int64_t end = done + warp_scan(n, lane);
+    const uint32_t who = __ballot_sync(0xffffffffu, x < end && x >= end - n);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      u.b = b0 + src;
+      done = __shfl_sync(0xffffffffu, end - n, src);
+      break;
+    }
+    done = __shfl_sync(0xffffffffu, end, 31);
+  }
+  u.r = load_request(p, u.b, cta_tok, false);
+  const int64_t head = u.r.cum(u.r.units, cta_tok);
+  u.hk = static_cast<int>((x - done) / head);
+  const int64_t y = x - done - u.hk * head;
+  int lo = 0, hi = u.r.units - 1;
+  while (lo < hi) {                        // the last unit that starts at or before y
+    const int mid = (lo + hi + 1) >> 1;
+    if (u.r.cum(mid, cta_tok) <= y) lo = mid;
+    else hi = mid - 1;
+  }
+  u.i = lo;
+  u.u0 = done + u.hk * head + u.r.cum(lo, cta_tok);
+  return u;
+}
+__device__ __forceinline__ Piece unit_piece(const Unit& u, int cta_tok, int tok_tile) {
+  Piece w;
+  const int tok0 = u.i * cta_tok;
+  w.row0 = u.r.q0 + tok0;
+  w.toks = u.r.T - tok0;
+  w.pos0 = u.r.L - u.r.T + tok0;
+  w.kv0 = u.r.kv0;
+  w.hk = u.hk;
+  const int n0 = tiles_of(w, 0, tok_tile), n1 = tiles_of(w, 1, tok_tile);
+  w.j0 = 0;
+  w.j1 = n0 > n1 ? n0 : n1;
+  w.part = -1;
+  return w;
+}
+// The K/V tile at which a border at point x of the line cuts a unit of n tiles that starts at
+// u0 and is `weight` long.  Short units stay whole, with the span that holds their middle;
+// long ones are cut at multiples of kMinCut tiles.
+__device__ __forceinline__ int cut_at(int64_t u0, int64_t weight, int n, int64_t x, bool cuts) {
+  if (x <= u0) return 0;
+  if (x >= u0 + weight) return n;
+  if (!cuts || n < 2 * kMinCut) return x > u0 + weight / 2 ? n : 0;
+  const int64_t t = (x - u0 - kUnitCost) >> 7;
+  if (t >= n) return n;
+  if (t < kMinCut) return 0;
+  return n - t < kMinCut ? n : static_cast<int>(t) & ~(kMinCut - 1);
+}
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
                                        uint32_t bar) {
@@ -89,23 +250,53 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// D[tmem] (+)= A[smem] . B[smem], bf16, fp32 accumulator; a converged warp, one lane issuing.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Runs of MMAs by a converged warp, one elected lane issuing: bf16 operands, fp32 accumulator.
+// One election and one set of descriptors a run; a branch or an election between the MMAs
+// costs more than the MMA takes (issued one by one with a branch each, 16,384 tokens took 2280
+// us instead of 1770).
+//
+// D[tmem] (+)= A[smem] . B[smem] over 64 columns of K (four MMAs, 32 bytes apart in both).
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.and.b32 p, %4, 0, e;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// The same with A in tensor memory: lane = row, each 32-bit column two bf16 of consecutive k.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The same with A in tensor memory (lane = row, each 32-bit column two bf16 of consecutive k)
+// over 128 of K: eight MMAs, 8 columns of A and 16 rows (2048 bytes) of B apart.
+__device__ __forceinline__ void mma_ts8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.and.b32 p, %4, 0, e;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 32;\n\tadd.s64 b, %2, 512;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 40;\n\tadd.s64 b, %2, 640;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -131,23 +322,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
   const uint32_t ring = sbase + S::kQBytes;
-  // barriers: full[NC], empty[NC], q_full, s_full[2], p_full[2], o_full[2], clean[4], drain,
-  // edge[4][2] (the chunks of a V tile on the edge arrive there, each once, so that the warps
-  // that clean them need not follow the ring)
+  // barriers: full[NC], empty[NC], q_full, q_empty, s_full[2], p_full[2], o_full[2],
+  // clean[kEdges], edge[kEdges][2] (the chunks of a V tile on the edge arrive there, so that
+  // the warp that cleans them need not follow the ring), item_full[kQueue],
+  // item_empty[kQueue], drain
   const uint32_t bars = sbase + S::kBarOff;
-  const uint32_t full0 = bars, empty0 = full0 + 8 * NC, q_full = empty0 + 8 * NC;
-  const uint32_t s_full = q_full + 8, p_full = s_full + 16, o_full = p_full + 16;
-  const uint32_t clean0 = o_full + 16, drain = clean0 + 8 * kMaxEdge;
-  const uint32_t edge0 = drain + 8;
-  uint8_t* words = smem + S::kBarOff + 16 * NC + 8 + 48 + 8 * kMaxEdge + 8 + 16 * kMaxEdge;
+  const uint32_t full0 = bars, empty0 = full0 + 8 * NC, q_full = empty0 + 8 * NC, q_empty = q_full + 8;
+  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16;
+  const uint32_t clean0 = o_full + 16, edge0 = clean0 + 8 * kEdges;
+  const uint32_t item_full = edge0 + 16 * kEdges, item_empty = item_full + 8 * kQueue;
+  const uint32_t drain = item_empty + 8 * kQueue;
+  uint8_t* words = smem + S::kBarOff + 16 * NC + 16 + 48 + 24 * kEdges + 16 * kQueue + 8;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(words);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 4);
-  volatile int* bad_v = reinterpret_cast<volatile int*>(words + 8);
-  volatile int* work = reinterpret_cast<volatile int*>(words + 16);   // b, tile of b
+  volatile int* bad_v = reinterpret_cast<volatile int*>(words + 8);           // [kQueue]
+  volatile uint32_t* landing = reinterpret_cast<volatile uint32_t*>(words + 8 + 4 * kQueue);  // [NC]
+  Piece* queue = reinterpret_cast<Piece*>(words + 8 + 4 * kQueue + 4 * 12);   // [kQueue]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = blockIdx.x % p.Hk;
-  const int tile_id = blockIdx.x / p.Hk;
   const int cta_tok = 2 * p.tok_tile;
 
   if (warp == 8 && lane == 0) {
@@ -159,82 +351,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty0 + 8 * i, 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full + 8 * s, 1);
       mbar_init(p_full + 8 * s, 128);
       mbar_init(o_full + 8 * s, 1);
     }
-    for (int i = 0; i < kMaxEdge; ++i) mbar_init(clean0 + 8 * i, 64);
-    for (int i = 0; i < 2 * kMaxEdge; ++i) mbar_init(edge0 + 8 * i, 1);
+    for (int i = 0; i < kEdges; ++i) mbar_init(clean0 + 8 * i, 32);
+    for (int i = 0; i < 2 * kEdges; ++i) mbar_init(edge0 + 8 * i, 1);
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(item_full + 8 * i, 1);
+      mbar_init(item_empty + 8 * i, kConsumers);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *bad_v = 0;
     fence_mbar_init();
   }
-  // ---- which request and which of its tiles: a scan over the requests' tile counts
-  if (warp == 0) {
-    int64_t done = 0;
-    int fb = -1, ft = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      int64_t n = 0;
-      if (b < p.B) {
-        const int64_t s = p.qo_indptr[b], e = p.qo_indptr[b + 1];
-        if (s < 0 || e < s || e > p.n_tok) {
-          if (blockIdx.x == 0) atomicOr(p.err, kErrBadIndptr);    // the request is left out
-        } else {
-          n = (e - s + cta_tok - 1) / cta_tok;
-        }
-      }
-      int64_t inc = n;
-#pragma unroll
-      for (int i = 1; i < 32; i <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, inc, i);
-        if (lane >= i) inc += o;
-      }
-      const int64_t start = done + inc - n;
-      const bool hit = tile_id >= start && tile_id < start + n;
-      const uint32_t who = __ballot_sync(0xffffffffu, hit);
-      if (who) {
-        const int src = __ffs(who) - 1;
-        fb = b0 + src;
-        // the longest tiles (the last tokens) first
-        ft = __shfl_sync(0xffffffffu, static_cast<int>(start + n - 1 - tile_id), src);
-        break;
-      }
-      done += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) {
-      work[0] = fb;
-      work[1] = ft;
-    }
-  }
-  __syncthreads();
-  const int b = work[0];
-  if (b < 0) return;                       // past the last tile
-  const int tok0 = work[1] * cta_tok;      // the CTA's first token in the request
-  const int64_t q0 = p.qo_indptr[b];
-  const int T = static_cast<int>(p.qo_indptr[b + 1] - q0);
-  int64_t kv0 = p.kv_indptr[b];
-  int64_t L = p.kv_indptr[b + 1] - kv0;
-  if (kv0 < 0 || L < 0 || kv0 + L > p.n_keys) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrBadIndptr);
-    kv0 = L = 0;
-  }
-  // position of the tiles' first token; tiles of keys each tile needs (its last token's)
-  const int64_t pos0 = L - T + tok0;
-  int n_kv[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int a = tok0 + s * p.tok_tile;
-    const int e = a + p.tok_tile < T ? a + p.tok_tile : T;
-    const int64_t seen = a < T ? L - T + e : 0;
-    n_kv[s] = seen > 0 ? static_cast<int>((seen + kKeys - 1) / kKeys) : 0;
-  }
-  const int n_all = n_kv[0] > n_kv[1] ? n_kv[0] : n_kv[1];
-  // K/V tiles from here on hold positions that some row does not see
-  const int n_clear = pos0 + 1 > 0 ? static_cast<int>((pos0 + 1) / kKeys) : 0;
-
   if (warp == 9) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
     tmem_relinquish();
@@ -244,263 +376,381 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ TMA
-    if (lane == 0 && n_all > 0) {
-      const uint32_t box = static_cast<uint32_t>(p.tok_tile) * p.G * 128;
-      const int nq = n_kv[1] > 0 ? 2 : 1;
-      mbar_arrive_expect_tx(q_full, nq * KC * box);
-      for (int s = 0; s < nq; ++s)
-        for (int c = 0; c < KC; ++c)
-          tma_3d(sbase + (s * KC + c) * kChunk, &tm_q, 64 * c, hk * p.G,
-                 static_cast<int>(q0) + tok0 + s * p.tok_tile, q_full);
-      // the barrier (and its phase) that chunk i, the c-th of tile j, completes on
-      auto landing = [&](int i, int j, int c, uint32_t* parity) {
-        const bool edge = c >= KC && j >= n_clear;
-        *parity = edge ? 0 : (i / NC) & 1;
-        return edge ? edge0 + 8 * (2 * (j - n_clear) + c - KC) : full0 + 8 * (i % NC);
+  // The it-th piece for a consumer warp: false at the span's end (or on abort).
+  auto next_piece = [&](int it, Piece* w) -> bool {
+    if (!warp_bcast(mbar_wait(item_full + 8 * (it % kQueue), (it / kQueue) & 1, abort_flag, p.err))) return false;
+    *w = queue[it % kQueue];
+    return w->j0 >= 0;
+  };
+  auto piece_read = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty + 8 * (it % kQueue));
+  };
+
+  // A softmax thread holds a row of S: 128 registers.  At the launch's 168 it spills, into an
+  // L1 of which shared memory leaves almost nothing.  2 x 200 + 104 = 3 x 168.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 11) {
+      // ---------------------------------------------------------- the span's pieces
+      const int64_t total = line_total(p, cta_tok, lane, blockIdx.x == 0);
+      const int64_t span = (total + gridDim.x - 1) / gridDim.x;
+      const int64_t x0 = blockIdx.x * span;
+      const int64_t x1 = x0 + span < total ? x0 + span : total;
+      const bool cuts = p.parts != nullptr;
+      int it = 0;
+      bool ok = true;
+      auto push = [&](const Piece& w) {
+        const int q = it % kQueue;
+        if (it >= kQueue && !mbar_wait(item_empty + 8 * q, ((it / kQueue) - 1) & 1, abort_flag, p.err)) {
+          ok = false;
+          return;
+        }
+        queue[q] = w;
+        bad_v[q] = 0;
+        mbar_arrive(item_full + 8 * q);
+        ++it;
       };
-      int issued = 0;
-      for (int j = 0, i = 0; j < n_all; ++j) {
+      if (x0 < x1) {
+        Unit u = find_unit(p, cta_tok, lane, x1 - 1);
+        if (lane == 0) {
+          while (ok) {
+            const int64_t weight = u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
+            Piece w = unit_piece(u, cta_tok, p.tok_tile);
+            const int n = w.j1;
+            if (n == 0) {                    // rows that see nothing: with the span of their start
+              if (x0 <= u.u0 && u.u0 < x1) push(w);
+            } else {
+              w.j0 = cut_at(u.u0, weight, n, x0, cuts);
+              w.j1 = cut_at(u.u0, weight, n, x1, cuts);
+              if (w.j0 < w.j1) {
+                if (w.j0 > 0 || w.j1 < n) w.part = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+                push(w);
+              }
+            }
+            if (u.u0 <= x0) break;
+            if (--u.i < 0) {                 // the unit before
+              if (--u.hk < 0) {
+                do u.r = load_request(p, --u.b, cta_tok, false);
+                while (u.r.units == 0);
+                u.hk = p.Hk - 1;
+              }
+              u.i = u.r.units - 1;
+            }
+            u.u0 -= u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
+          }
+        }
+      }
+      if (lane == 0 && ok) {
+        Piece end = {};
+        end.j0 = -1;
+        push(end);
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      // ---------------------------------------------------------- TMA
+      if (lane == 0) {
+        const uint32_t box = static_cast<uint32_t>(p.tok_tile) * p.G * 128;
+        int i = 0, edges = 0, nq = 0;
         bool ok = true;
-        for (int c = 0; c < KC + VC; ++c, ++i) {
-          const int slot = i % NC;
-          if (i >= NC && !mbar_wait(empty0 + 8 * slot, ((i / NC) - 1) & 1, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          uint32_t parity;
-          const uint32_t bar = landing(i, j, c, &parity);
-          if (bar != full0 + 8 * slot) mbar_arrive(full0 + 8 * slot);   // keeps its phases in step
-          mbar_arrive_expect_tx(bar, kChunk);
-          const bool is_k = c < KC;
-          tma_3d(ring + slot * kChunk, is_k ? &tm_k : &tm_v, 64 * (is_k ? c : c - KC), hk,
-                 static_cast<int>(kv0) + j * kKeys, bar);
-          issued = i + 1;
-        }
-        if (!ok) break;
-      }
-      // no copy may be in flight when the CTA ends
-      mbar_wait_drain(q_full, 0);
-      for (int i = issued > NC ? issued - NC : 0; i < issued; ++i) {
-        uint32_t parity;
-        const uint32_t bar = landing(i, i / (KC + VC), i % (KC + VC), &parity);
-        mbar_wait_drain(bar, parity);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t id_qk = idesc_bf16(kKeys, false);
-    constexpr uint32_t id_pv = idesc_bf16(DV, true), id_pv64 = idesc_bf16(64, true);
-    bool ok = n_all > 0;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      ok = ok && warp_bcast(mbar_wait(bar, parity, abort_flag, p.err));
-      tc_fence_after();
-    };
-    auto wait_chunk = [&](int i) { wait(full0 + 8 * (i % NC), (i / NC) & 1); };
-    auto free_chunks = [&](int i, int n) {
-      for (int c = 0; c < n; ++c) mma_commit_warp(empty0 + 8 * ((i + c) % NC));
-    };
-    // S_s = Q_s K(j)^T, the chunks of K(j) from ring index i on
-    auto qk = [&](int s, int i, bool wait_k) {
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        if (wait_k) wait_chunk(i + c);
-        if (!ok) return;
-        const uint64_t a = smem_desc(sbase + (s * KC + c) * kChunk, 16, 1024, kSw128);
-        const uint64_t bd = smem_desc(ring + ((i + c) % NC) * kChunk, 16, 1024, kSw128);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + 128 * s, desc_at(a, 32 * k), desc_at(bd, 32 * k), id_qk, (c > 0 || k > 0) ? 1u : 0u);
-      }
-      mma_commit_warp(s_full + 8 * s);
-    };
-    // O_s += P_s V(j): 16 positions (8 columns of P, 16 rows of V) an MMA
-    auto pv = [&](int s, int i, bool first) {
-      const int slot = i % NC;
-      const bool split = VC == 2 && slot == NC - 1;      // V's chunks lie at the ring's two ends
-      const uint64_t v0 = smem_desc(ring + slot * kChunk, kChunk, 1024, kSw128);
-      const uint64_t v1 = smem_desc(ring, kChunk, 1024, kSw128);
-      const uint32_t o = tmem + 256 + 128 * s, pt = tmem + 128 * s;
-#pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k) {
-        const uint32_t acc = (!first || k > 0) ? 1u : 0u;
-        if (!split) {
-          mma_ts(o, pt + 8 * k, desc_at(v0, 2048 * k), id_pv, acc);
-        } else {
-          mma_ts(o, pt + 8 * k, desc_at(v0, 2048 * k), id_pv64, acc);
-          mma_ts(o + 64, pt + 8 * k, desc_at(v1, 2048 * k), id_pv64, acc);
-        }
-      }
-    };
-    if (ok) {
-      wait(q_full, 0);
-      if (ok) qk(0, 0, true);
-      if (ok && n_kv[1] > 0) qk(1, 0, n_kv[0] == 0);
-      if (ok) free_chunks(0, KC);
-    }
-    for (int j = 0; j < n_all && ok; ++j) {
-      const int iv = j * (KC + VC) + KC, ik = (j + 1) * (KC + VC);
-      const int s_first = j < n_kv[0] ? 0 : 1;
-      const int s_last = j < n_kv[1] ? 1 : 0;
-      const int k_first = j + 1 < n_kv[0] ? 0 : 1, k_last = j + 1 < n_kv[1] ? 1 : 0;
-      for (int s = s_first; s <= s_last && ok; ++s) {
-        wait(p_full + 8 * s, j & 1);
-        if (s == s_first) {
-          if (j >= n_clear) {
-            wait(clean0 + 8 * (j - n_clear), 0);
-          } else {
-            for (int c = 0; c < VC; ++c) wait_chunk(iv + c);
+        for (int it = 0; ok; ++it) {
+          if (!mbar_wait(item_full + 8 * (it % kQueue), (it / kQueue) & 1, abort_flag, p.err)) break;
+          const Piece w = queue[it % kQueue];
+          mbar_arrive(item_empty + 8 * (it % kQueue));
+          if (w.j0 < 0) break;
+          const int e0 = first_edge(w);
+          for (int j = w.j0; j < w.j1 && ok; ++j) {
+            const bool edge = j >= e0;
+            for (int c = 0; c < KC + VC; ++c, ++i) {
+              if (j == w.j0 && c == KC) {      // Q behind the first K tile
+                if (nq > 0 && !mbar_wait(q_empty, (nq - 1) & 1, abort_flag, p.err)) {
+                  ok = false;
+                  break;
+                }
+                const int tiles = w.toks > p.tok_tile ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, tiles * KC * box);
+                for (int s = 0; s < tiles; ++s)
+                  for (int k = 0; k < KC; ++k)
+                    tma_3d(sbase + (s * KC + k) * kChunk, &tm_q, 64 * k, w.hk * p.G,
+                           w.row0 + s * p.tok_tile, q_full);
+                ++nq;
+              }
+              const int slot = i % NC;
+              if (i >= NC && !mbar_wait(empty0 + 8 * slot, ((i / NC) - 1) & 1, abort_flag, p.err)) {
+                ok = false;
+                break;
+              }
+              const bool is_k = c < KC;
+              uint32_t bar = full0 + 8 * slot, parity = (i / NC) & 1;
+              if (!is_k && edge) {
+                mbar_arrive(bar);              // keeps the slot's phases in step
+                bar = edge0 + 16 * (edges % kEdges) + 8 * (c - KC);
+                parity = (edges / kEdges) & 1;
+              }
+              landing[slot] = bar | (parity << 31);
+              mbar_arrive_expect_tx(bar, kChunk);
+              tma_3d(ring + slot * kChunk, is_k ? &tm_k : &tm_v, 64 * (is_k ? c : c - KC), w.hk,
+                     w.kv0 + j * kKeys, bar);
+            }
+            if (edge) ++edges;
           }
         }
-        if (!ok) break;
-        pv(s, iv, j == 0);
-        if (s == s_last) free_chunks(iv, VC);
-        if (j + 1 < n_kv[s]) {
-          qk(s, ik, s == k_first);
-          if (!ok) break;
-          if (s == k_last) free_chunks(ik, KC);
-        } else {
-          mma_commit_warp(o_full + 8 * s);
-        }
+        // no copy may be in flight when the CTA ends
+        if (nq > 0) mbar_wait_drain(q_full, (nq - 1) & 1);
+        for (int s = 0; s < (i < NC ? i : NC); ++s)
+          mbar_wait_drain(landing[s] & 0x7FFFFFFFu, landing[s] >> 31);
       }
-    }
-    mma_commit_warp(drain);
-    __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ V on the edge
-    const int ct = threadIdx.x - 320;
-    bool ok = true;
-    for (int j = n_clear; j < n_all && ok; ++j) {
-      const int iv = j * (KC + VC) + KC;
-      bool bad = false;
-      for (int c = 0; c < VC && ok; ++c) {
-        const int slot = (iv + c) % NC;
-        ok = mbar_wait(edge0 + 8 * (2 * (j - n_clear) + c), 0, abort_flag, p.err);
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_qk = idesc_bf16(kKeys, false);
+      constexpr uint32_t id_pv = idesc_bf16(DV, true), id_pv64 = idesc_bf16(64, true);
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && warp_bcast(mbar_wait(bar, parity, abort_flag, p.err));
+        tc_fence_after();
+      };
+      auto wait_chunk = [&](int i) { wait(full0 + 8 * (i % NC), (i / NC) & 1); };
+      auto free_chunks = [&](int i, int n) {
+        for (int c = 0; c < n; ++c) mma_commit_warp(empty0 + 8 * ((i + c) % NC));
+      };
+      // S_s = Q_s K(j)^T, the chunks of K(j) from ring index i on
+      auto qk = [&](int s, int i, bool wait_k) {
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          if (wait_k) wait_chunk(i + c);
+          if (!ok) return;
+          const uint64_t a = smem_desc(sbase + (s * KC + c) * kChunk, 16, 1024, kSw128);
+          const uint64_t bd = smem_desc(ring + ((i + c) % NC) * kChunk, 16, 1024, kSw128);
+          mma_ss4(tmem + 128 * s, a, bd, id_qk, c > 0 ? 1u : 0u);
+        }
+        mma_commit_warp(s_full + 8 * s);
+      };
+      // O_s += P_s V(j): 16 positions (8 columns of P, 16 rows of V) an MMA
+      auto pv = [&](int s, int i, bool first) {
+        const int slot = i % NC;
+        const uint64_t v0 = smem_desc(ring + slot * kChunk, kChunk, 1024, kSw128);
+        const uint32_t o = tmem + 256 + 128 * s, pt = tmem + 128 * s;
+        const uint32_t acc = first ? 0u : 1u;
+        // V's two chunks lie at the ring's two ends (with an even KC a V tile starts in an even
+        // slot of the even ring: never)
+        if (VC == 2 && KC % 2 == 1 && slot == NC - 1) {
+          mma_ts8(o, pt, v0, id_pv64, acc);
+          mma_ts8(o + 64, pt, smem_desc(ring, kChunk, 1024, kSw128), id_pv64, acc);
+        } else {
+          mma_ts8(o, pt, v0, id_pv, acc);
+        }
+      };
+      int i = 0, edges = 0, nq = 0;
+      uint32_t done = 0;                       // parities of either row tile's tiles so far
+      Piece w;
+      for (int it = 0; ok && next_piece(it, &w); ++it) {
+        piece_read(it);
+        const int n = w.j1 - w.j0;
+        if (n <= 0) continue;
+        int c0 = tiles_of(w, 0, p.tok_tile), c1 = tiles_of(w, 1, p.tok_tile);
+        c0 = (c0 < w.j1 ? c0 : w.j1) - w.j0;   // K/V tiles of either row tile (may be negative)
+        c1 = (c1 < w.j1 ? c1 : w.j1) - w.j0;
+        const int e0 = first_edge(w) - w.j0;
+        wait(q_full, nq & 1);
+        ++nq;
+        if (ok && c0 > 0) qk(0, i, true);
+        if (ok && c1 > 0) qk(1, i, c0 <= 0);
         if (!ok) break;
-        uint8_t* chunk = smem + S::kQBytes + slot * kChunk;
-        // (the swizzle moves 16-byte words inside a 128-byte row only)
+        free_chunks(i, KC);
+        if (n == 1) mma_commit_warp(q_empty);
+        for (int t = 0; t < n && ok; ++t) {
+          const int iv = i + t * (KC + VC) + KC, ik = iv + VC;
+          const int s_first = t < c0 ? 0 : 1, s_last = t < c1 ? 1 : 0;
+          const int k_first = t + 1 < c0 ? 0 : 1, k_last = t + 1 < c1 ? 1 : 0;
+          for (int s = s_first; s <= s_last && ok; ++s) {
+            wait(p_full + 8 * s, (done >> s) & 1);
+            done ^= 1u << s;
+            if (s == s_first) {
+              if (t >= e0) {
+                wait(clean0 + 8 * (edges % kEdges), (edges / kEdges) & 1);
+                ++edges;
+              } else {
+                for (int c = 0; c < VC; ++c) wait_chunk(iv + c);
+              }
+            }
+            if (!ok) break;
+            pv(s, iv, t == 0);
+            if (s == s_last) free_chunks(iv, VC);
+            if (t + 1 < (s ? c1 : c0)) {
+              qk(s, ik, s == k_first);
+              if (!ok) break;
+              if (s == k_last) {
+                free_chunks(ik, KC);
+                if (t + 2 == n) mma_commit_warp(q_empty);
+              }
+            } else {
+              mma_commit_warp(o_full + 8 * s);
+            }
+          }
+        }
+        i += n * (KC + VC);
+      }
+      mma_commit_warp(drain);
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- V on the edge
+      int i = 0, edges = 0;
+      bool ok = true;
+      Piece w;
+      for (int it = 0; ok && next_piece(it, &w); ++it) {
+        const int len = w.pos0 + w.toks;       // the request's keys
+        for (int j = first_edge(w); j < w.j1 && ok; ++j, ++edges) {
+          const int iv = i + (j - w.j0) * (KC + VC) + KC;
+          bool bad = false;
+          for (int c = 0; c < VC && ok; ++c) {
+            ok = mbar_wait(edge0 + 16 * (edges % kEdges) + 8 * c, (edges / kEdges) & 1, abort_flag, p.err);
+            if (!ok) break;
+            uint4* chunk = reinterpret_cast<uint4*>(smem + S::kQBytes + ((iv + c) % NC) * kChunk);
+            // (the swizzle moves 16-byte words inside a 128-byte row only)
 #pragma unroll 4
-        for (int e = ct; e < 128 * 8; e += 64) {
-          uint4* at = reinterpret_cast<uint4*>(chunk) + e;
-          if (static_cast<int64_t>(j) * kKeys + (e >> 3) >= L) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 x = *at;
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          bool any = false;
+            for (int e = lane; e < 128 * 8; e += 32) {
+              if (j * kKeys + (e >> 3) >= len) {
+                chunk[e] = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 x = chunk[e];
+              uint32_t y[4] = {x.x, x.y, x.z, x.w};
+              bool any = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (half_nonfinite(w[i])) {
-              w[i] &= 0xFFFF0000u;
-              any = true;
-            }
-            if (half_nonfinite(w[i] >> 16)) {
-              w[i] &= 0xFFFFu;
-              any = true;
+              for (int k = 0; k < 4; ++k) {
+                if (half_nonfinite(y[k])) {
+                  y[k] &= 0xFFFF0000u;
+                  any = true;
+                }
+                if (half_nonfinite(y[k] >> 16)) {
+                  y[k] &= 0xFFFFu;
+                  any = true;
+                }
+              }
+              if (any) {
+                chunk[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                bad = true;
+              }
             }
           }
-          if (any) {
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
-            bad = true;
-          }
+          if (bad) bad_v[it % kQueue] = 1;
+          fence_proxy_async_smem();
+          if (ok) mbar_arrive(clean0 + 8 * (edges % kEdges));
         }
+        i += (w.j1 - w.j0) * (KC + VC);
+        piece_read(it);
       }
-      if (bad) *bad_v = 1;
-      fence_proxy_async_smem();
-      if (ok) mbar_arrive(clean0 + 8 * (j - n_clear));
     }
   } else {
     // ------------------------------------------------------------ softmax, one row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int s = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + 128 * s + lane_base, t_o = tmem + 256 + 128 * s + lane_base;
-    const int tt = r / p.G;
-    const int tok = tok0 + s * p.tok_tile + tt;
-    const bool live = tt < p.tok_tile && tok < T;
-    // the last position the row sees (rows of no token: as the tile's last)
-    const int64_t lim = L - T + (tok < T ? tok : T - 1);
-    float m = -INFINITY, l = 0.f;
+    const int tt = r / p.G, hg = r - tt * p.G;
+    const int tok = s * p.tok_tile + tt;       // in the unit
+    int done = 0, outs = 0, edges = 0;
     bool ok = true;
-    for (int j = 0; j < n_kv[s]; ++j) {
-      ok = warp_bcast(mbar_wait(s_full + 8 * s, j & 1, abort_flag, p.err));
-      if (!ok) break;
-      tc_fence_after();
-      float x[128];
-      tmem_ld32(t_s, x);
-      tmem_ld32(t_s + 32, x + 32);
-      tmem_ld32(t_s + 64, x + 64);
-      tmem_ld32(t_s + 96, x + 96);
-      tmem_wait_ld_regs(x, x + 16);
-      tmem_wait_ld_regs(x + 32, x + 48);
-      tmem_wait_ld_regs(x + 64, x + 80);
-      tmem_wait_ld_regs(x + 96, x + 112);
-      if (j >= n_clear) {
-        const int64_t rel = lim - static_cast<int64_t>(j) * kKeys;
-        const int last = rel < -1 ? -1 : (rel > kKeys ? kKeys : static_cast<int>(rel));
+    Piece w;
+    for (int it = 0; ok && next_piece(it, &w); ++it) {
+      const bool live = tt < p.tok_tile && tok < w.toks;
+      // the last position the row sees
+      const int lim = w.pos0 + tok;
+      const int nt = tiles_of(w, s, p.tok_tile);
+      const int j1 = nt < w.j1 ? nt : w.j1;
+      const int e0 = first_edge(w);
+      float m = -INFINITY, l = 0.f;
+      for (int j = w.j0; j < j1; ++j, ++done) {
+        ok = warp_bcast(mbar_wait(s_full + 8 * s, done & 1, abort_flag, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        float x[128];
+        tmem_ld32(t_s, x);
+        tmem_ld32(t_s + 32, x + 32);
+        tmem_ld32(t_s + 64, x + 64);
+        tmem_ld32(t_s + 96, x + 96);
+        tmem_wait_ld_regs(x, x + 16);
+        tmem_wait_ld_regs(x + 32, x + 48);
+        tmem_wait_ld_regs(x + 64, x + 80);
+        tmem_wait_ld_regs(x + 96, x + 112);
+        if (j >= e0) {
+          const int last = lim - j * kKeys;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+          for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // raise the maximum where it grew by more than kRaise (always from -inf); each row by
-      // itself, so that no row's result depends on its neighbours (or on idle rows)
-      const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
-      if (__any_sync(0xffffffffu, raise)) {
-        const float mn = raise ? mt : m;
-        const float f = m == mn ? 1.f : ex2_approx((m - mn) * p.scale_log2);   // 0 from -inf
-        m = mn;
-        l *= f;
-        if (j > 0) {
+        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // raise the maximum where it grew by more than kRaise (always from -inf); each row by
+        // itself, so that no row's result depends on its neighbours (or on idle rows)
+        const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = raise ? mt : m;
+          const float f = m == mn ? 1.f : ex2_approx((m - mn) * p.scale_log2);   // 0 from -inf
+          m = mn;
+          l *= f;
+          if (j > w.j0) {
 #pragma unroll 1
-          for (int c = 0; c < DV; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + c, o);
-            tmem_wait_ld_regs(o, o + 16);
+            for (int c = 0; c < DV; c += 16) {
+              float o[16];
+              tmem_ld16(t_o + c, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(t_o + c, o);
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(t_o + c, o);
+            }
           }
         }
-      }
-      const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      float pk[64];
+        const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float a = ex2_approx(fmaf(x[2 * i], p.scale_log2, off));
-        const float c = ex2_approx(fmaf(x[2 * i + 1], p.scale_log2, off));
-        sum[i & 1] += a;
-        sum[2 + (i & 1)] += c;
-        pk[i] = __uint_as_float(pack_bf16(a, c));
+        for (int half = 0; half < 2; ++half) {
+          float pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = ex2_approx(fmaf(x[64 * half + 2 * i], p.scale_log2, off));
+            const float c = ex2_approx(fmaf(x[64 * half + 2 * i + 1], p.scale_log2, off));
+            sum[i & 1] += a;
+            sum[2 + (i & 1)] += c;
+            pk[i] = __uint_as_float(pack_bf16(a, c));
+          }
+          tmem_st32(t_s + 32 * half, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full + 8 * s);
       }
-      tmem_st32(t_s, pk);
-      tmem_st32(t_s + 32, pk + 32);
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full + 8 * s);
-    }
-    // ---- the row's result
-    if (n_kv[s] > 0 && ok) ok = warp_bcast(mbar_wait(o_full + 8 * s, 0, abort_flag, p.err));
-    if (ok && tok0 + s * p.tok_tile < T) {
-      bool fix = false;
-      for (int j = n_clear; j < n_kv[s] && ok; ++j)
-        ok = warp_bcast(mbar_wait(clean0 + 8 * (j - n_clear), 0, abort_flag, p.err));
-      if (n_kv[s] > n_clear) fix = *bad_v != 0;
+      // ---- the row's result
+      const bool any = j1 > w.j0;
+      if (any && ok) ok = warp_bcast(mbar_wait(o_full + 8 * s, outs & 1, abort_flag, p.err));
+      outs += any ? 1 : 0;
+      const int n_edge = w.j1 > e0 ? w.j1 - e0 : 0;
+      if (n_edge > 0 && ok) {
+        const int e = edges + n_edge - 1;
+        ok = warp_bcast(mbar_wait(clean0 + 8 * (e % kEdges), (e / kEdges) & 1, abort_flag, p.err));
+      }
+      edges += n_edge;
+      if (!ok) break;
+      const bool fix = any && n_edge > 0 && bad_v[it % kQueue] != 0;
+      piece_read(it);
+      if (s * p.tok_tile >= w.toks) continue;
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int h = hk * p.G + r - tt * p.G;
-      uint16_t* orow = p.o + (q0 + tok) * p.o_tok + h * p.o_head;
+      const bool whole = w.part < 0;
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const bool none = whole && l == 0.f;
+      const int h = w.hk * p.G + hg;
+      const int64_t row = static_cast<int64_t>(w.row0) + tok;
+      uint16_t* orow = p.o + row * p.o_tok + h * p.o_head;
+      float* part = whole ? nullptr : p.parts + static_cast<int64_t>(w.part) * S::kPartFloats;
+      const float m2 = m == -INFINITY ? m : m * p.scale_log2;
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
         float o[32];
-        if (n_kv[s] > 0) {
+        if (any) {
           tmem_ld32(t_o + c, o);
           tmem_wait_ld_regs(o, o + 16);
         } else {
@@ -508,25 +758,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+        for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
         if (fix && live)
-          for (int64_t j = static_cast<int64_t>(n_clear) * kKeys; j <= lim; ++j) {
-            const uint16_t* vr = p.v + (kv0 + j) * p.v_tok + hk * p.v_head + c;
+          for (int j = e0 * kKeys; j <= lim && j < w.j1 * kKeys; ++j) {
+            const uint16_t* vr = p.v + static_cast<int64_t>(w.kv0 + j) * p.v_tok + w.hk * p.v_head + c;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (half_nonfinite(vr[i])) o[i] += __uint_as_float(static_cast<uint32_t>(vr[i]) << 16);
           }
-        if (live) {
+        if (!live) continue;
+        if (whole) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(orow + c + 8 * i) =
                 make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
                            pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+        } else {
+          float* at = part + 4 * kRows + (s * kRows + r) * DV + c;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(at + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
-      if (live && p.lse)
-        p.lse[(q0 + tok) * p.Hq + h] =
-            l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) * p.scale_log2) * kLn2 + logf(l);
+      if (live && whole && p.lse)
+        p.lse[row * p.Hq + h] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m2) * kLn2 + logf(l);
+      if (live && !whole) {
+        part[s * kRows + r] = m2;
+        part[2 * kRows + s * kRows + r] = l;
+      }
+      tc_fence_before();                       // O is read before the next piece's P arrives
     }
   }
   tc_fence_before();
@@ -537,6 +797,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the parts of the unit that starts in span blockIdx.x and is cut at its end; blockIdx.y
+// takes 32 of its 256 rows, eight threads a row.  Bytes bound: the parts, from L2.
+template <int DV>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, int spans) {
+  constexpr int kPart = 2 * kRows * (DV + 2);
+  __shared__ Piece sh_piece;
+  __shared__ int sh_n, sh_parts[kMaxParts];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta_tok = 2 * p.tok_tile;
+  const int first = blockIdx.x;
+  if (warp == 0) {
+    const int64_t total = line_total(p, cta_tok, lane, false);
+    const int64_t span = (total + spans - 1) / spans;
+    const int64_t x = (first + 1) * span;
+    int parts = 0;
+    if (x < total) {
+      const Unit u = find_unit(p, cta_tok, lane, x);
+      const int64_t weight = u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
+      const Piece w = unit_piece(u, cta_tok, p.tok_tile);
+      const int n = w.j1;
+      int t = cut_at(u.u0, weight, n, x, true);
+      if (lane == 0 && n >= 2 * kMinCut && t > 0 && t < n && cut_at(u.u0, weight, n, first * span, true) == 0) {
+        sh_parts[parts++] = 2 * first + 1;
+        for (int i = first + 1; t < n; ++i) {            // spans between two cuts, some empty
+          const int e = cut_at(u.u0, weight, n, (i + 1) * span, true);
+          if (e > t) sh_parts[parts++] = 2 * i;
+          t = e;
+        }
+        sh_piece = w;
+      }
+    }
+    if (lane == 0) sh_n = parts;
+  }
+  __syncthreads();
+  const int n_parts = sh_n;
+  if (n_parts == 0) return;
+  const Piece w = sh_piece;
+  const int row = 32 * blockIdx.y + (threadIdx.x >> 3), q = threadIdx.x & 7;
+  const int s = row / kRows, r = row - s * kRows;
+  const int tt = r / p.G, tok = s * p.tok_tile + tt;
+  if (tt >= p.tok_tile || tok >= w.toks) return;
+  auto part = [&](int i) { return p.parts + static_cast<int64_t>(sh_parts[i]) * kPart; };
+  float mm = -INFINITY;
+  for (int i = 0; i < n_parts; ++i) mm = fmaxf(mm, part(i)[row]);
+  float ll = 0.f, o[DV / 8];
+#pragma unroll
+  for (int k = 0; k < DV / 8; ++k) o[k] = 0.f;
+  for (int i = 0; i < n_parts; ++i) {
+    const float m = part(i)[row], l = part(i)[2 * kRows + row];
+    // a part that no key has weight in: m = -inf, l = 0 (NaN scores keep their l)
+    const float f = m == -INFINITY ? 1.f : ex2_approx(m - mm);
+    ll += f * l;
+    const float* at = part(i) + 4 * kRows + row * DV;
+#pragma unroll
+    for (int k = 0; k < DV / 32; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(at + 32 * k + 4 * q);
+      o[4 * k] += f * x.x;
+      o[4 * k + 1] += f * x.y;
+      o[4 * k + 2] += f * x.z;
+      o[4 * k + 3] += f * x.w;
+    }
+  }
+  const bool none = ll == 0.f;
+  const float inv = none ? 0.f : 1.f / ll;
+  const int h = w.hk * p.G + r - tt * p.G;
+  const int64_t at = static_cast<int64_t>(w.row0) + tok;
+#pragma unroll
+  for (int k = 0; k < DV / 32; ++k) {
+    uint2 y;
+    y.x = pack_bf16(none ? 0.f : o[4 * k] * inv, none ? 0.f : o[4 * k + 1] * inv);
+    y.y = pack_bf16(none ? 0.f : o[4 * k + 2] * inv, none ? 0.f : o[4 * k + 3] * inv);
+    *reinterpret_cast<uint2*>(p.o + at * p.o_tok + h * p.o_head + 32 * k + 4 * q) = y;
+  }
+  if (q == 0 && p.lse)
+    p.lse[at * p.Hq + h] = none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -563,7 +900,7 @@ int encode(EncodeTiledFn enc, CUtensorMap* m, const mla_tensor_t* t, int box_hea
 
 template <int D, int DV>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const PromptParams& p, unsigned grid, cudaStream_t stream) {
+                   const PromptParams& p, int sms, cudaStream_t stream) {
   using S = PromptShape<D, DV>;
   static std::mutex mu;
   static bool attr_set[64] = {};
@@ -578,8 +915,25 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
       attr_set[dev] = true;
     }
   }
-  prompt_attention_kernel<S><<<grid, kThreads, S::kSmem, stream>>>(tq, tk, tv, p);
+  prompt_attention_kernel<S><<<sms, kThreads, S::kSmem, stream>>>(tq, tk, tv, p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.parts) return e;
+  prompt_join_kernel<DV><<<dim3(sms - 1, 8), 256, 0, stream>>>(p, sms);
   return cudaGetLastError();
+}
+
+int sms_of_device(int* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+// Bytes of the parts a call may leave: none where no request can be long enough to be cut.
+size_t parts_for(int sms, int64_t n_keys, int64_t DV) {
+  if (n_keys <= (2 * kMinCut - 1) * kKeys || sms < 2 || sms > kMaxParts) return 0;
+  return 2 * static_cast<size_t>(sms) * 2 * kRows * static_cast<size_t>(DV + 2) * 4;
 }
 
 // Strides TMA can step: positive where the dim has more than one entry.
@@ -590,11 +944,26 @@ bool steppable(const mla_tensor_t* t) {
 }  // namespace
 }  // namespace pmla
 
+extern "C" int mla_get_prompt_workspace_size(int64_t n_keys, int32_t v_head_dim, int32_t num_sms,
+                                             size_t* bytes_out) {
+  using namespace pmla;
+  if (!bytes_out || n_keys < 0 || num_sms > 65536) return MLA_ERR_INVALID_ARG;
+  if (v_head_dim != 64 && v_head_dim != 128) return MLA_ERR_UNSUPPORTED;
+  int sms = num_sms;
+  if (num_sms <= 0) {
+    const int st = sms_of_device(&sms);
+    if (st != MLA_OK) return st;
+  }
+  *bytes_out = parts_for(sms, n_keys, v_head_dim);
+  return MLA_OK;
+}
+
 extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k,
                                     const mla_tensor_t* v, const mla_tensor_t* o,
                                     const mla_tensor_t* qo_indptr, const mla_tensor_t* kv_indptr,
                                     float sm_scale, const mla_tensor_t* lse_out,
-                                    int32_t* error_word, mla_stream_t stream_) {
+                                    int32_t* error_word, void* workspace, size_t workspace_bytes,
+                                    mla_stream_t stream_) {
   using namespace pmla;
   if (!q || !k || !v || q->ndim != 3 || k->ndim != 3 || v->ndim != 3) return MLA_ERR_INVALID_ARG;
   const int64_t n_tok = q->shape[0], Hq = q->shape[1], D = q->shape[2];
@@ -617,7 +986,13 @@ extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k
   const int64_t G = Hq / Hk;
   const bool s64 = D == 64 && DV == 64, s128 = D == 128 && DV == 128, s192 = D == 192 && DV == 128;
   if (!(s64 || s128 || s192) || G > kRows) return MLA_ERR_UNSUPPORTED;
+  if (workspace && !gqa_aligned(workspace, 16)) return MLA_ERR_INVALID_ARG;
   if (n_tok == 0 || B == 0) return MLA_OK;
+  int sms = 0;
+  const int cs = sms_of_device(&sms);
+  if (cs != MLA_OK) return cs;
+  const size_t need = parts_for(sms, n_keys, DV);
+  if (workspace && workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
 
   PromptParams p;
   p.qo_indptr = static_cast<const int32_t*>(qo_indptr->ptr);
@@ -638,10 +1013,7 @@ extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k
   p.v_tok = v->stride[0];
   p.v_head = v->stride[1];
   p.err = error_word;
-  // every request has at most one tile that is not full
-  const int64_t tiles = n_tok / (2 * p.tok_tile) + (B < n_tok ? B : n_tok);
-  if (tiles * Hk > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(tiles * Hk);
+  p.parts = workspace && need > 0 ? static_cast<float*>(workspace) : nullptr;
 
   EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
   if (!enc) return MLA_ERR_CUDA;
@@ -656,8 +1028,8 @@ extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k
   if (st != MLA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e;
-  if (s64) e = launch<64, 64>(tq, tk, tv, p, grid, s);
-  else if (s128) e = launch<128, 128>(tq, tk, tv, p, grid, s);
-  else e = launch<192, 128>(tq, tk, tv, p, grid, s);
+  if (s64) e = launch<64, 64>(tq, tk, tv, p, sms, s);
+  else if (s128) e = launch<128, 128>(tq, tk, tv, p, sms, s);
+  else e = launch<192, 128>(tq, tk, tv, p, sms, s);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

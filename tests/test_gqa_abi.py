@@ -176,7 +176,8 @@ def _prompt_args(pm):
 
 def _prompt(pm, a):
     return pm._lib.mla_prompt_attention(_r(a["q"]), _r(a["k"]), _r(a["v"]), _r(a["o"]), _r(a["qo"]),
-                                        _r(a["kv"]), a["sm"], _r(a["lse"]), ctypes.c_void_p(a["err"]), None)
+                                        _r(a["kv"]), a["sm"], _r(a["lse"]), ctypes.c_void_p(a["err"]),
+                                        ctypes.c_void_p(a.get("ws")), a.get("n", 0), None)
 
 
 @pytest.mark.parametrize("name,change,status", [
@@ -197,6 +198,7 @@ def _prompt(pm, a):
     ("scale infinite", lambda pm: dict(sm=float("inf")), INVALID),
     ("lse shape", lambda pm: dict(lse=_t(pm, 6, F32, [7, 2])), INVALID),
     ("no error word", lambda pm: dict(err=0), INVALID),
+    ("workspace base", lambda pm: dict(ws=BASE + 4, n=1 << 30), INVALID),
     ("head widths", lambda pm: dict(v=_t(pm, 2, BF, [9, 2, 64]), o=_t(pm, 3, BF, [7, 8, 64])), UNSUPPORTED),
     ("group too large", lambda pm: dict(q=_t(pm, 0, BF, [7, 258, 128]), o=_t(pm, 3, BF, [7, 258, 128]),
                                         lse=None), UNSUPPORTED),
@@ -210,3 +212,14 @@ def test_prompt_of_nothing_is_ok(pm):
     a.update(q=_t(pm, 0, BF, [0, 8, 128], ptr=0), o=_t(pm, 3, BF, [0, 8, 128], ptr=0), lse=None)
     assert _prompt(pm, a) == 0
     assert _prompt(pm, {**_prompt_args(pm), "qo": _t(pm, 4, I32, [1]), "kv": _t(pm, 5, I32, [1])}) == 0
+
+
+def test_prompt_workspace_size(pm):
+    f = pm.mla_get_prompt_workspace_size
+    # two parts a SM: maximum, sum and output of 256 rows in fp32
+    assert f(20000, 128, 152) == 2 * 152 * 256 * 130 * 4
+    assert f(20000, 64, 152) == 2 * 152 * 256 * 66 * 4
+    assert f(1920, 128, 152) == 0              # too short to be cut anywhere
+    for bad in ((-1, 128), (100, 96)):
+        with pytest.raises(pm.MlaError):
+            f(*bad, 152)

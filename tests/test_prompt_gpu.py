@@ -204,3 +204,60 @@ def test_prompt_in_a_graph(pm):
     c["o"].fill_(math.nan)
     graph.replay()
     assert torch.equal(c["o"], want)
+
+
+@pytest.mark.parametrize("D,DV", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("new,keys,Hq,Hk", [
+    ([16], [40000], 4, 2),                         # few rows over many keys: cut many times
+    ([1, 300, 700], [5000, 9000, 700], 6, 2),
+    ([2100, 5, 2100], [2100, 2049, 4200], 2, 1),
+])
+def test_prompt_cut_between_sms(pm, new, keys, Hq, Hk, D, DV):
+    """With a workspace long units are cut between SMs and joined; without one they are not.
+    Both are right, each gives the same bits again."""
+    c = _case(new, keys, Hq, Hk, D, DV)
+    _run(pm, c)
+    assert c["err"].item() == 0
+    _check(c, "cut", rows=100)
+    first, lse = c["o"].clone(), c["lse"].clone()
+    n = pm.mla_get_prompt_workspace_size(sum(keys), DV)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)       # stale NaN
+    pm.mla_prompt_attention(c["q"], c["k"], c["v"], c["o"], c["qo"], c["kv"], c["sm"], c["err"], c["lse"],
+                            workspace=ws)
+    assert torch.equal(first, c["o"]) and torch.equal(lse, c["lse"])
+    with pytest.raises(pm.MlaError):
+        pm.mla_prompt_attention(c["q"], c["k"], c["v"], c["o"], c["qo"], c["kv"], c["sm"], c["err"],
+                                workspace=ws[:n // 2])
+    c["o"].fill_(math.nan)
+    d = [pm._packed(c[x], 0) for x in ("q", "k", "v", "o", "qo", "kv")]
+    assert pm._lib.mla_prompt_attention(*d, c["sm"], pm._packed(c["lse"], 0), c["err"].data_ptr(), None, 0,
+                                        torch.cuda.current_stream().cuda_stream) == 0
+    _check(c, "whole", rows=100)
+
+
+def test_prompt_non_finite_values_in_cut_units(pm):
+    new, keys = [40, 30], [6000, 7000]
+    clean = _case(new, keys, 2, 1, 128, 128)
+    _run(pm, clean)
+    for at, rows in ((100, range(0, 40)), (6000 - 40 + 7, range(7, 40)), (6000 + 6990, range(60, 70))):
+        c = _case(new, keys, 2, 1, 128, 128)
+        c["v"][at, 0, 9] = math.inf
+        _run(pm, c)
+        hit = torch.zeros_like(c["o"], dtype=torch.bool)
+        hit[list(rows), :, 9] = True
+        assert torch.equal(c["o"][~hit], clean["o"][~hit])
+        assert (~torch.isfinite(c["o"][hit])).all()
+
+
+def test_prompt_on_another_stream(pm):
+    c = _case([500, 20], [5000, 500], 8, 2, 128, 128)
+    _run(pm, c)
+    want = c["o"].clone()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        c["o"].fill_(math.nan)
+        torch.cuda.synchronize()
+        pm.mla_prompt_attention(c["q"], c["k"], c["v"], c["o"], c["qo"], c["kv"], c["sm"], c["err"], c["lse"],
+                                stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(c["o"], want)
