@@ -60,6 +60,7 @@ constexpr int kKeys = 128;                 // positions of a K/V tile
 constexpr int kChunk = 128 * 128;          // 128 rows of 64 bf16 columns
 constexpr int kThreads = 384;
 constexpr int kEdges = 8;                  // barriers of edge tiles; the ring holds at most 6 V tiles
+constexpr int kLoads = 16;                 // barriers of K and V tiles; the ring holds at most 12
 constexpr int kQueue = 4;                  // pieces queued
 constexpr int kConsumers = 11;             // warps that read a queued piece
 constexpr float kLog2e = 1.4426950408889634f;
@@ -300,6 +301,30 @@ __device__ __forceinline__ void mma_ts8(uint32_t d, uint32_t a, uint64_t b, uint
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// Two fp32 values in one 64-bit register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // kind::f16, D f32, A and B bf16 (fields as in the other kernels); B MN-major or K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
@@ -322,31 +347,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
   const uint32_t ring = sbase + S::kQBytes;
-  // barriers: full[NC], empty[NC], q_full, q_empty, s_full[2], p_full[2], o_full[2],
-  // clean[kEdges], edge[kEdges][2] (the chunks of a V tile on the edge arrive there, so that
-  // the warp that cleans them need not follow the ring), item_full[kQueue],
-  // item_empty[kQueue], drain
+  // barriers: full[kLoads] and empty[kLoads] (K and V tiles in turn), q_full, q_empty, s_full[2],
+  // p_full[2], o_full[2], clean[kEdges], edge[kEdges] (a V tile on the edge lands there, so that
+  // the warp that cleans it need not follow the ring), item_full[kQueue], item_empty[kQueue],
+  // drain
   const uint32_t bars = sbase + S::kBarOff;
-  const uint32_t full0 = bars, empty0 = full0 + 8 * NC, q_full = empty0 + 8 * NC, q_empty = q_full + 8;
+  const uint32_t full0 = bars, empty0 = full0 + 8 * kLoads, q_full = empty0 + 8 * kLoads;
+  const uint32_t q_empty = q_full + 8;
   const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16;
   const uint32_t clean0 = o_full + 16, edge0 = clean0 + 8 * kEdges;
-  const uint32_t item_full = edge0 + 16 * kEdges, item_empty = item_full + 8 * kQueue;
+  const uint32_t item_full = edge0 + 8 * kEdges, item_empty = item_full + 8 * kQueue;
   const uint32_t drain = item_empty + 8 * kQueue;
-  uint8_t* words = smem + S::kBarOff + 16 * NC + 16 + 48 + 24 * kEdges + 16 * kQueue + 8;
+  uint8_t* words = smem + S::kBarOff + 16 * kLoads + 16 + 48 + 16 * kEdges + 16 * kQueue + 8;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(words);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 4);
   volatile int* bad_v = reinterpret_cast<volatile int*>(words + 8);           // [kQueue]
-  volatile uint32_t* landing = reinterpret_cast<volatile uint32_t*>(words + 8 + 4 * kQueue);  // [NC]
-  Piece* queue = reinterpret_cast<Piece*>(words + 8 + 4 * kQueue + 4 * 12);   // [kQueue]
+  volatile uint32_t* landing = reinterpret_cast<volatile uint32_t*>(words + 8 + 4 * kQueue);  // [kLoads]
+  Piece* queue = reinterpret_cast<Piece*>(words + 8 + 4 * kQueue + 4 * kLoads);   // [kQueue]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the broadcasts make the compiler's analysis see what is uniform in a warp: an MMA whose
+  // descriptors it keeps in uniform registers issues in its own time, otherwise in about 80
+  // cycles)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int cta_tok = 2 * p.tok_tile;
 
   if (warp == 8 && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
-    for (int i = 0; i < NC; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       mbar_init(full0 + 8 * i, 1);
       mbar_init(empty0 + 8 * i, 1);
     }
@@ -354,11 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full + 8 * s, 1);
-      mbar_init(p_full + 8 * s, 128);
+      mbar_init(p_full + 8 * s, 4);
       mbar_init(o_full + 8 * s, 1);
     }
     for (int i = 0; i < kEdges; ++i) mbar_init(clean0 + 8 * i, 32);
-    for (int i = 0; i < 2 * kEdges; ++i) mbar_init(edge0 + 8 * i, 1);
+    for (int i = 0; i < kEdges; ++i) mbar_init(edge0 + 8 * i, 1);
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(item_full + 8 * i, 1);
       mbar_init(item_empty + 8 * i, kConsumers);
@@ -374,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   // The it-th piece for a consumer warp: false at the span's end (or on abort).
   auto next_piece = [&](int it, Piece* w) -> bool {
@@ -451,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- TMA
       if (lane == 0) {
         const uint32_t box = static_cast<uint32_t>(p.tok_tile) * p.G * 128;
-        int i = 0, edges = 0, nq = 0;
+        int i = 0, n = 0, edges = 0, nq = 0;   // chunks, loads, edge tiles, Qs so far
         bool ok = true;
         for (int it = 0; ok; ++it) {
           if (!mbar_wait(item_full + 8 * (it % kQueue), (it / kQueue) & 1, abort_flag, p.err)) break;
@@ -460,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w.j0 < 0) break;
           const int e0 = first_edge(w);
           for (int j = w.j0; j < w.j1 && ok; ++j) {
-            const bool edge = j >= e0;
-            for (int c = 0; c < KC + VC; ++c, ++i) {
-              if (j == w.j0 && c == KC) {      // Q behind the first K tile
+            for (int v = 0; v < 2; ++v) {
+              const int chunks = v ? VC : KC;
+              if (j == w.j0 && v) {            // Q behind the first K tile
                 if (nq > 0 && !mbar_wait(q_empty, (nq - 1) & 1, abort_flag, p.err)) {
                   ok = false;
                   break;
@@ -475,30 +504,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                            w.row0 + s * p.tok_tile, q_full);
                 ++nq;
               }
-              const int slot = i % NC;
-              if (i >= NC && !mbar_wait(empty0 + 8 * slot, ((i / NC) - 1) & 1, abort_flag, p.err)) {
-                ok = false;
-                break;
+              const int reused = i + chunks - 1 - NC;   // the last chunk this load overwrites
+              if (reused >= 0) {
+                const int l = 2 * (reused / (KC + VC)) + (reused % (KC + VC) >= KC ? 1 : 0);
+                if (!mbar_wait(empty0 + 8 * (l % kLoads), (l / kLoads) & 1, abort_flag, p.err)) {
+                  ok = false;
+                  break;
+                }
               }
-              const bool is_k = c < KC;
-              uint32_t bar = full0 + 8 * slot, parity = (i / NC) & 1;
-              if (!is_k && edge) {
-                mbar_arrive(bar);              // keeps the slot's phases in step
-                bar = edge0 + 16 * (edges % kEdges) + 8 * (c - KC);
+              uint32_t bar = full0 + 8 * (n % kLoads), parity = (n / kLoads) & 1;
+              if (v && j >= e0) {
+                mbar_arrive(bar);              // keeps its phases in step
+                bar = edge0 + 8 * (edges % kEdges);
                 parity = (edges / kEdges) & 1;
+                ++edges;
               }
-              landing[slot] = bar | (parity << 31);
-              mbar_arrive_expect_tx(bar, kChunk);
-              tma_3d(ring + slot * kChunk, is_k ? &tm_k : &tm_v, 64 * (is_k ? c : c - KC), w.hk,
-                     w.kv0 + j * kKeys, bar);
+              landing[n % kLoads] = bar | (parity << 31);
+              mbar_arrive_expect_tx(bar, chunks * kChunk);
+              for (int c = 0; c < chunks; ++c, ++i)
+                tma_3d(ring + (i % NC) * kChunk, v ? &tm_v : &tm_k, 64 * c, w.hk, w.kv0 + j * kKeys, bar);
+              ++n;
             }
-            if (edge) ++edges;
           }
         }
         // no copy may be in flight when the CTA ends
         if (nq > 0) mbar_wait_drain(q_full, (nq - 1) & 1);
-        for (int s = 0; s < (i < NC ? i : NC); ++s)
-          mbar_wait_drain(landing[s] & 0x7FFFFFFFu, landing[s] >> 31);
+        for (int l = 0; l < (n < kLoads ? n : kLoads); ++l)
+          mbar_wait_drain(landing[l] & 0x7FFFFFFFu, landing[l] >> 31);
       }
       __syncwarp();
     } else if (warp == 9) {
@@ -510,25 +542,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && warp_bcast(mbar_wait(bar, parity, abort_flag, p.err));
         tc_fence_after();
       };
-      auto wait_chunk = [&](int i) { wait(full0 + 8 * (i % NC), (i / NC) & 1); };
-      auto free_chunks = [&](int i, int n) {
-        for (int c = 0; c < n; ++c) mma_commit_warp(empty0 + 8 * ((i + c) % NC));
+      // the barriers of tile t's K (v = 0) and V (v = 1), t counted over the whole span
+      auto wait_tile = [&](int t, int v) {
+        const int l = 2 * t + v;
+        wait(full0 + 8 * (l % kLoads), (l / kLoads) & 1);
       };
-      // S_s = Q_s K(j)^T, the chunks of K(j) from ring index i on
-      auto qk = [&](int s, int i, bool wait_k) {
+      auto free_tile = [&](int t, int v) { mma_commit_warp(empty0 + 8 * ((2 * t + v) % kLoads)); };
+      // S_s = Q_s K(t)^T
+      auto qk = [&](int s, int t) {
+        const int i = t * (KC + VC);
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          if (wait_k) wait_chunk(i + c);
-          if (!ok) return;
-          const uint64_t a = smem_desc(sbase + (s * KC + c) * kChunk, 16, 1024, kSw128);
-          const uint64_t bd = smem_desc(ring + ((i + c) % NC) * kChunk, 16, 1024, kSw128);
-          mma_ss4(tmem + 128 * s, a, bd, id_qk, c > 0 ? 1u : 0u);
-        }
+        for (int c = 0; c < KC; ++c)
+          mma_ss4(tmem + 128 * s, smem_desc(sbase + (s * KC + c) * kChunk, 16, 1024, kSw128),
+                  smem_desc(ring + ((i + c) % NC) * kChunk, 16, 1024, kSw128), id_qk, c > 0 ? 1u : 0u);
         mma_commit_warp(s_full + 8 * s);
       };
-      // O_s += P_s V(j): 16 positions (8 columns of P, 16 rows of V) an MMA
-      auto pv = [&](int s, int i, bool first) {
-        const int slot = i % NC;
+      // O_s += P_s V(t)
+      auto pv = [&](int s, int t, bool first) {
+        const int slot = (t * (KC + VC) + KC) % NC;
         const uint64_t v0 = smem_desc(ring + slot * kChunk, kChunk, 1024, kSw128);
         const uint32_t o = tmem + 256 + 128 * s, pt = tmem + 128 * s;
         const uint32_t acc = first ? 0u : 1u;
@@ -541,29 +572,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts8(o, pt, v0, id_pv, acc);
         }
       };
-      int i = 0, edges = 0, nq = 0;
+      int base = 0, edges = 0, nq = 0;         // tiles, edge tiles, Qs so far
       uint32_t done = 0;                       // parities of either row tile's tiles so far
       Piece w;
       for (int it = 0; ok && next_piece(it, &w); ++it) {
         piece_read(it);
-        const int n = w.j1 - w.j0;
+        const int n = __shfl_sync(0xffffffffu, w.j1 - w.j0, 0);
         if (n <= 0) continue;
         int c0 = tiles_of(w, 0, p.tok_tile), c1 = tiles_of(w, 1, p.tok_tile);
-        c0 = (c0 < w.j1 ? c0 : w.j1) - w.j0;   // K/V tiles of either row tile (may be negative)
-        c1 = (c1 < w.j1 ? c1 : w.j1) - w.j0;
-        const int e0 = first_edge(w) - w.j0;
+        // K/V tiles of either row tile (may be negative), the first one on the edge
+        c0 = __shfl_sync(0xffffffffu, (c0 < w.j1 ? c0 : w.j1) - w.j0, 0);
+        c1 = __shfl_sync(0xffffffffu, (c1 < w.j1 ? c1 : w.j1) - w.j0, 0);
+        const int e0 = __shfl_sync(0xffffffffu, first_edge(w) - w.j0, 0);
         wait(q_full, nq & 1);
         ++nq;
-        if (ok && c0 > 0) qk(0, i, true);
-        if (ok && c1 > 0) qk(1, i, c0 <= 0);
+        wait_tile(base, 0);
         if (!ok) break;
-        free_chunks(i, KC);
+        if (c0 > 0) qk(0, base);
+        if (c1 > 0) qk(1, base);
+        free_tile(base, 0);
         if (n == 1) mma_commit_warp(q_empty);
         for (int t = 0; t < n && ok; ++t) {
-          const int iv = i + t * (KC + VC) + KC, ik = iv + VC;
           const int s_first = t < c0 ? 0 : 1, s_last = t < c1 ? 1 : 0;
           const int k_first = t + 1 < c0 ? 0 : 1, k_last = t + 1 < c1 ? 1 : 0;
-          for (int s = s_first; s <= s_last && ok; ++s) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (s < s_first || s > s_last || !ok) continue;
             wait(p_full + 8 * s, (done >> s) & 1);
             done ^= 1u << s;
             if (s == s_first) {
@@ -571,17 +605,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(clean0 + 8 * (edges % kEdges), (edges / kEdges) & 1);
                 ++edges;
               } else {
-                for (int c = 0; c < VC; ++c) wait_chunk(iv + c);
+                wait_tile(base + t, 1);
               }
             }
-            if (!ok) break;
-            pv(s, iv, t == 0);
-            if (s == s_last) free_chunks(iv, VC);
+            if (!ok) continue;
+            pv(s, base + t, t == 0);
+            if (s == s_last) free_tile(base + t, 1);
             if (t + 1 < (s ? c1 : c0)) {
-              qk(s, ik, s == k_first);
-              if (!ok) break;
+              if (s == k_first) wait_tile(base + t + 1, 0);
+              if (!ok) continue;
+              qk(s, base + t + 1);
               if (s == k_last) {
-                free_chunks(ik, KC);
+                free_tile(base + t + 1, 0);
                 if (t + 2 == n) mma_commit_warp(q_empty);
               }
             } else {
@@ -589,23 +624,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        i += n * (KC + VC);
+        base += n;
       }
       mma_commit_warp(drain);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- V on the edge
-      int i = 0, edges = 0;
+      int base = 0, edges = 0;                 // tiles, edge tiles so far
       bool ok = true;
       Piece w;
       for (int it = 0; ok && next_piece(it, &w); ++it) {
         const int len = w.pos0 + w.toks;       // the request's keys
         for (int j = first_edge(w); j < w.j1 && ok; ++j, ++edges) {
-          const int iv = i + (j - w.j0) * (KC + VC) + KC;
+          const int iv = (base + j - w.j0) * (KC + VC) + KC;
           bool bad = false;
+          ok = mbar_wait(edge0 + 8 * (edges % kEdges), (edges / kEdges) & 1, abort_flag, p.err);
           for (int c = 0; c < VC && ok; ++c) {
-            ok = mbar_wait(edge0 + 16 * (edges % kEdges) + 8 * c, (edges / kEdges) & 1, abort_flag, p.err);
-            if (!ok) break;
             uint4* chunk = reinterpret_cast<uint4*>(smem + S::kQBytes + ((iv + c) % NC) * kChunk);
             // (the swizzle moves 16-byte words inside a 128-byte row only)
 #pragma unroll 4
@@ -638,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           if (ok) mbar_arrive(clean0 + 8 * (edges % kEdges));
         }
-        i += (w.j1 - w.j0) * (KC + VC);
+        base += w.j1 - w.j0;
         piece_read(it);
       }
     }
@@ -667,23 +701,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float x[128];
+        float mx[2];
+        const int last = lim - j * kKeys;
         tmem_ld32(t_s, x);
-        tmem_ld32(t_s + 32, x + 32);
-        tmem_ld32(t_s + 64, x + 64);
-        tmem_ld32(t_s + 96, x + 96);
-        tmem_wait_ld_regs(x, x + 16);
-        tmem_wait_ld_regs(x + 32, x + 48);
-        tmem_wait_ld_regs(x + 64, x + 80);
-        tmem_wait_ld_regs(x + 96, x + 112);
-        if (j >= e0) {
-          const int last = lim - j * kKeys;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
+        for (int c = 0; c < 4; ++c) {          // the maximum of 32 columns while the next 32 come
+          float* y = x + 32 * c;
+          tmem_wait_ld_regs(y, y + 16);
+          if (c < 3) tmem_ld32(t_s + 32 * (c + 1), y + 32);
+          if (j >= e0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = 32 * c + i <= last ? y[i] : -INFINITY;
+          }
+          if (c == 0) {
+            mx[0] = y[0];
+            mx[1] = y[1];
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mx[0] = max3(mx[0], y[i], y[i + 2]);
+            mx[1] = max3(mx[1], y[i + 1], y[i + 3]);
+          }
         }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float mt = fmaxf(mx[0], mx[1]);
         // raise the maximum where it grew by more than kRaise (always from -inf); each row by
         // itself, so that no row's result depends on its neighbours (or on idle rows)
         const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
@@ -705,24 +745,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), off2 = pair(off, off);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float pk[32];
+        for (int c = 0; c < 4; ++c) {          // 32 columns of weights
+          float pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = ex2_approx(fmaf(x[64 * half + 2 * i], p.scale_log2, off));
-            const float c = ex2_approx(fmaf(x[64 * half + 2 * i + 1], p.scale_log2, off));
-            sum[i & 1] += a;
-            sum[2 + (i & 1)] += c;
-            pk[i] = __uint_as_float(pack_bf16(a, c));
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t y = fma2(pair(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), scale2, off2);
+            float a, b;
+            unpair(y, &a, &b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            sum[i & 1] = add2(sum[i & 1], pair(a, b));
+            pk[i] = __uint_as_float(pack_bf16(a, b));
           }
-          tmem_st32(t_s + 32 * half, pk);
+          tmem_st16(t_s + 16 * c, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full + 8 * s);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * s);
+        float s0, s1, s2, s3;
+        unpair(sum[0], &s0, &s1);
+        unpair(sum[1], &s2, &s3);
+        l += (s0 + s1) + (s2 + s3);
       }
       // ---- the row's result
       const bool any = j1 > w.j0;
