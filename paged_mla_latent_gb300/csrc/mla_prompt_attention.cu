@@ -22,16 +22,18 @@
 //
 //   warps 0-3, 4-7 : softmax of tile 0 / 1, a thread a row: S from tensor memory, maximum,
 //                    exponentials, P as bf16 back over S's columns.
-//   warp 8         : TMA.  K and V tiles of 128 positions come in 16 KB chunks of 64 columns
-//                    (128-byte swizzle) through one ring; each has its own barriers.
+//   warp 8         : walks the span, queues its pieces for the others and loads them by TMA: K
+//                    and V tiles of 128 positions in 16 KB chunks of 64 columns (128-byte
+//                    swizzle) through one ring.
 //   warp 9         : tcgen05.mma issuer.  S = Q K^T from shared memory; O += P V with P (the A
 //                    operand) in tensor memory.  Order: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1),
-//                    so that one tile's MMAs run while the other's softmax does.
-//   warp 10        : for the tiles on the causal edge and at a request's end, zeroes the V rows
+//                    so that one tile's MMAs run while the other's softmax does.  (An issuer
+//                    for each tile: their MMAs interleave, both tiles' results come later,
+//                    16,384 tokens 1856 us instead of 1568.)
+//   warps 10-11    : for the tiles on the causal edge and at a request's end, zeroes the V rows
 //                    past the request (another request's, or stale memory) and takes
 //                    non-finite values out of V (0 * inf would reach rows that do not see
 //                    them); rows that do see one get it back at the end.
-//   warp 11        : walks the span and queues its pieces for the others.
 // Tensor memory: S_0 S_1 O_0 O_1, 128 columns each (all 512); P_s lies over S_s.
 //
 // The running maximum is only raised when it would grow by more than 8 (in log2): then the
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = sbase + S::kQBytes;
   // barriers: full[kLoads] and empty[kLoads] (K and V tiles in turn), q_full, q_empty, s_full[2],
   // p_full[2], o_full[2], clean[kEdges], edge[kEdges] (a V tile on the edge lands there, so that
-  // the warp that cleans it need not follow the ring), item_full[kQueue], item_empty[kQueue],
+  // the warps that clean it need not follow the ring), item_full[kQueue], item_empty[kQueue],
   // drain
   const uint32_t bars = sbase + S::kBarOff;
   const uint32_t full0 = bars, empty0 = full0 + 8 * kLoads, q_full = empty0 + 8 * kLoads;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t clean0 = o_full + 16, edge0 = clean0 + 8 * kEdges;
   const uint32_t item_full = edge0 + 8 * kEdges, item_empty = item_full + 8 * kQueue;
   const uint32_t drain = item_empty + 8 * kQueue;
-  uint8_t* words = smem + S::kBarOff + 16 * kLoads + 16 + 48 + 16 * kEdges + 16 * kQueue + 8;
+  uint8_t* words = smem + S::kBarOff + 16 * kLoads + 16 + 48 + 16 * kEdges + 16 * kQueue + 16;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(words);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 4);
   volatile int* bad_v = reinterpret_cast<volatile int*>(words + 8);           // [kQueue]
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full + 8 * s, 4);
       mbar_init(o_full + 8 * s, 1);
     }
-    for (int i = 0; i < kEdges; ++i) mbar_init(clean0 + 8 * i, 32);
+    for (int i = 0; i < kEdges; ++i) mbar_init(clean0 + 8 * i, 64);
     for (int i = 0; i < kEdges; ++i) mbar_init(edge0 + 8 * i, 1);
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(item_full + 8 * i, 1);
@@ -420,81 +422,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   // L1 of which shared memory leaves almost nothing.  2 x 200 + 104 = 3 x 168.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == 11) {
-      // ---------------------------------------------------------- the span's pieces
+    if (warp == 8) {
+      // ---------------------------------------------------------- the span's pieces, TMA
       const int64_t total = line_total(p, cta_tok, lane, blockIdx.x == 0);
       const int64_t span = (total + gridDim.x - 1) / gridDim.x;
       const int64_t x0 = blockIdx.x * span;
       const int64_t x1 = x0 + span < total ? x0 + span : total;
       const bool cuts = p.parts != nullptr;
-      int it = 0;
-      bool ok = true;
-      auto push = [&](const Piece& w) {
-        const int q = it % kQueue;
-        if (it >= kQueue && !mbar_wait(item_empty + 8 * q, ((it / kQueue) - 1) & 1, abort_flag, p.err)) {
-          ok = false;
-          return;
-        }
-        queue[q] = w;
-        bad_v[q] = 0;
-        mbar_arrive(item_full + 8 * q);
-        ++it;
-      };
-      if (x0 < x1) {
-        Unit u = find_unit(p, cta_tok, lane, x1 - 1);
-        if (lane == 0) {
-          while (ok) {
-            const int64_t weight = u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
-            Piece w = unit_piece(u, cta_tok, p.tok_tile);
-            const int n = w.j1;
-            if (n == 0) {                    // rows that see nothing: with the span of their start
-              if (x0 <= u.u0 && u.u0 < x1) push(w);
-            } else {
-              w.j0 = cut_at(u.u0, weight, n, x0, cuts);
-              w.j1 = cut_at(u.u0, weight, n, x1, cuts);
-              if (w.j0 < w.j1) {
-                if (w.j0 > 0 || w.j1 < n) w.part = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-                push(w);
-              }
-            }
-            if (u.u0 <= x0) break;
-            if (--u.i < 0) {                 // the unit before
-              if (--u.hk < 0) {
-                do u.r = load_request(p, --u.b, cta_tok, false);
-                while (u.r.units == 0);
-                u.hk = p.Hk - 1;
-              }
-              u.i = u.r.units - 1;
-            }
-            u.u0 -= u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
-          }
-        }
-      }
-      if (lane == 0 && ok) {
-        Piece end = {};
-        end.j0 = -1;
-        push(end);
-      }
-      __syncwarp();
-    } else if (warp == 8) {
-      // ---------------------------------------------------------- TMA
+      Unit u = {};
+      if (x0 < x1) u = find_unit(p, cta_tok, lane, x1 - 1);
       if (lane == 0) {
         const uint32_t box = static_cast<uint32_t>(p.tok_tile) * p.G * 128;
         int i = 0, n = 0, edges = 0, nq = 0;   // chunks, loads, edge tiles, Qs so far
+        int it = 0;
         bool ok = true;
-        for (int it = 0; ok; ++it) {
-          if (!mbar_wait(item_full + 8 * (it % kQueue), (it / kQueue) & 1, abort_flag, p.err)) break;
-          const Piece w = queue[it % kQueue];
-          mbar_arrive(item_empty + 8 * (it % kQueue));
-          if (w.j0 < 0) break;
+        auto push = [&](const Piece& w) {
+          const int q = it % kQueue;
+          if (it >= kQueue && !mbar_wait(item_empty + 8 * q, ((it / kQueue) - 1) & 1, abort_flag, p.err)) {
+            ok = false;
+            return;
+          }
+          queue[q] = w;
+          bad_v[q] = 0;
+          mbar_arrive(item_full + 8 * q);
+          ++it;
+        };
+        auto load = [&](const Piece& w) {
           const int e0 = first_edge(w);
-          for (int j = w.j0; j < w.j1 && ok; ++j) {
+          for (int j = w.j0; j < w.j1; ++j) {
             for (int v = 0; v < 2; ++v) {
               const int chunks = v ? VC : KC;
               if (j == w.j0 && v) {            // Q behind the first K tile
                 if (nq > 0 && !mbar_wait(q_empty, (nq - 1) & 1, abort_flag, p.err)) {
                   ok = false;
-                  break;
+                  return;
                 }
                 const int tiles = w.toks > p.tok_tile ? 2 : 1;
                 mbar_arrive_expect_tx(q_full, tiles * KC * box);
@@ -509,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int l = 2 * (reused / (KC + VC)) + (reused % (KC + VC) >= KC ? 1 : 0);
                 if (!mbar_wait(empty0 + 8 * (l % kLoads), (l / kLoads) & 1, abort_flag, p.err)) {
                   ok = false;
-                  break;
+                  return;
                 }
               }
               uint32_t bar = full0 + 8 * (n % kLoads), parity = (n / kLoads) & 1;
@@ -526,6 +487,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++n;
             }
           }
+        };
+        while (ok && x0 < x1) {
+          const int64_t weight = u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
+          Piece w = unit_piece(u, cta_tok, p.tok_tile);
+          const int tiles = w.j1;
+          bool mine = x0 <= u.u0 && u.u0 < x1;   // rows that see nothing: the span of their start
+          if (tiles > 0) {
+            w.j0 = cut_at(u.u0, weight, tiles, x0, cuts);
+            w.j1 = cut_at(u.u0, weight, tiles, x1, cuts);
+            mine = w.j0 < w.j1;
+            if (w.j0 > 0 || w.j1 < tiles) w.part = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+          }
+          if (mine) {
+            push(w);
+            if (ok) load(w);
+          }
+          if (u.u0 <= x0) break;
+          if (--u.i < 0) {                     // the unit before
+            if (--u.hk < 0) {
+              do u.r = load_request(p, --u.b, cta_tok, false);
+              while (u.r.units == 0);
+              u.hk = p.Hk - 1;
+            }
+            u.i = u.r.units - 1;
+          }
+          u.u0 -= u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
+        }
+        if (ok) {
+          Piece end = {};
+          end.j0 = -1;
+          push(end);
         }
         // no copy may be in flight when the CTA ends
         if (nq > 0) mbar_wait_drain(q_full, (nq - 1) & 1);
@@ -572,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts8(o, pt, v0, id_pv, acc);
         }
       };
-      int base = 0, edges = 0, nq = 0;         // tiles, edge tiles, Qs so far
+      int base = 0, edges = 0, nq = 0;         // K/V tiles, edge tiles, Qs so far
       uint32_t done = 0;                       // parities of either row tile's tiles so far
       Piece w;
       for (int it = 0; ok && next_piece(it, &w); ++it) {
@@ -592,36 +584,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c1 > 0) qk(1, base);
         free_tile(base, 0);
         if (n == 1) mma_commit_warp(q_empty);
-        for (int t = 0; t < n && ok; ++t) {
-          const int s_first = t < c0 ? 0 : 1, s_last = t < c1 ? 1 : 0;
-          const int k_first = t + 1 < c0 ? 0 : 1, k_last = t + 1 < c1 ? 1 : 0;
+        for (int t = 0; t < n; ++t) {
+          if (t >= e0) {
+            wait(clean0 + 8 * (edges % kEdges), (edges / kEdges) & 1);
+            ++edges;
+          } else {
+            wait_tile(base + t, 1);
+          }
+          bool k_here = false;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (s < s_first || s > s_last || !ok) continue;
-            wait(p_full + 8 * s, (done >> s) & 1);
-            done ^= 1u << s;
-            if (s == s_first) {
-              if (t >= e0) {
-                wait(clean0 + 8 * (edges % kEdges), (edges / kEdges) & 1);
-                ++edges;
-              } else {
-                wait_tile(base + t, 1);
-              }
+            const int c = s ? c1 : c0;
+            if (t < c) {
+              wait(p_full + 8 * s, (done >> s) & 1);
+              done ^= 1u << s;
+              if (!ok) break;
+              pv(s, base + t, t == 0);
+              if (t + 1 == c) mma_commit_warp(o_full + 8 * s);
             }
-            if (!ok) continue;
-            pv(s, base + t, t == 0);
-            if (s == s_last) free_tile(base + t, 1);
-            if (t + 1 < (s ? c1 : c0)) {
-              if (s == k_first) wait_tile(base + t + 1, 0);
-              if (!ok) continue;
+            if (s) free_tile(base + t, 1);
+            if (t + 1 < c) {
+              if (!k_here) wait_tile(base + t + 1, 0);   // behind PV, which hides the wait
+              k_here = true;
+              if (!ok) break;
               qk(s, base + t + 1);
-              if (s == k_last) {
-                free_tile(base + t + 1, 0);
-                if (t + 2 == n) mma_commit_warp(q_empty);
-              }
-            } else {
-              mma_commit_warp(o_full + 8 * s);
             }
+          }
+          if (!ok) break;
+          if (t + 1 < n) {
+            free_tile(base + t + 1, 0);
+            if (t + 2 == n) mma_commit_warp(q_empty);
           }
         }
         base += n;
@@ -643,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4* chunk = reinterpret_cast<uint4*>(smem + S::kQBytes + ((iv + c) % NC) * kChunk);
             // (the swizzle moves 16-byte words inside a 128-byte row only)
 #pragma unroll 4
-            for (int e = lane; e < 128 * 8; e += 32) {
+            for (int e = threadIdx.x - 320; e < 128 * 8; e += 64) {
               if (j * kKeys + (e >> 3) >= len) {
                 chunk[e] = make_uint4(0, 0, 0, 0);
                 continue;
@@ -701,67 +693,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float x[128];
-        float mx[2];
-        const int last = lim - j * kKeys;
         tmem_ld32(t_s, x);
+        tmem_ld32(t_s + 32, x + 32);
+        tmem_ld32(t_s + 64, x + 64);
+        tmem_ld32(t_s + 96, x + 96);
+        tmem_wait_ld_regs(x, x + 16);
+        tmem_wait_ld_regs(x + 32, x + 48);
+        tmem_wait_ld_regs(x + 64, x + 80);
+        tmem_wait_ld_regs(x + 96, x + 112);
+        if (j >= e0) {
+          const int last = lim - j * kKeys;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {          // the maximum of 32 columns while the next 32 come
-          float* y = x + 32 * c;
-          tmem_wait_ld_regs(y, y + 16);
-          if (c < 3) tmem_ld32(t_s + 32 * (c + 1), y + 32);
-          if (j >= e0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = 32 * c + i <= last ? y[i] : -INFINITY;
-          }
-          if (c == 0) {
-            mx[0] = y[0];
-            mx[1] = y[1];
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            mx[0] = max3(mx[0], y[i], y[i + 2]);
-            mx[1] = max3(mx[1], y[i + 1], y[i + 3]);
-          }
+          for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
         }
-        const float mt = fmaxf(mx[0], mx[1]);
-        // raise the maximum where it grew by more than kRaise (always from -inf); each row by
-        // itself, so that no row's result depends on its neighbours (or on idle rows)
-        const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float mn = raise ? mt : m;
-          const float f = m == mn ? 1.f : ex2_approx((m - mn) * p.scale_log2);   // 0 from -inf
-          m = mn;
-          l *= f;
-          if (j > w.j0) {
-#pragma unroll 1
-            for (int c = 0; c < DV; c += 16) {
-              float o[16];
-              tmem_ld16(t_o + c, o);
-              tmem_wait_ld();
+        // The first half's weights are taken with the old maximum while the tile's own is
+        // found, and taken again in the rare case that it has to be raised.
+        uint64_t sum[2];
+        uint32_t pk[32];
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+        auto weights = [&](int half) {
+          const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
+          const uint64_t off2 = pair(off, off);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= f;
-              tmem_st16(t_o + c, o);
-            }
-          }
-        }
-        const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
-        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), off2 = pair(off, off);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {          // 32 columns of weights
-          float pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t y = fma2(pair(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), scale2, off2);
+          for (int i = 0; i < 32; ++i) {
+            const uint64_t y = fma2(pair(x[64 * half + 2 * i], x[64 * half + 2 * i + 1]), scale2, off2);
             float a, b;
             unpair(y, &a, &b);
             a = ex2_approx(a);
             b = ex2_approx(b);
             sum[i & 1] = add2(sum[i & 1], pair(a, b));
-            pk[i] = __uint_as_float(pack_bf16(a, b));
+            pk[i] = pack_bf16(a, b);
           }
-          tmem_st16(t_s + 16 * c, pk);
+        };
+        bool raised = j == w.j0;
+        float mt = -INFINITY;
+        auto find_max = [&] {
+          float mx[2] = {x[0], x[1]};
+#pragma unroll
+          for (int i = 2; i < 126; i += 4) {
+            mx[0] = max3(mx[0], x[i], x[i + 2]);
+            mx[1] = max3(mx[1], x[i + 1], x[i + 3]);
+          }
+          mt = max3(fmaxf(mx[0], mx[1]), x[126], x[127]);
+        };
+        if (raised) {                            // a piece's first tile: O is empty
+          find_max();
+          if (live) m = mt;
         }
+        while (true) {
+          sum[0] = sum[1] = 0;
+          weights(0);
+          if (raised) break;
+          find_max();
+          // raise the maximum where it grew by more than kRaise (always from -inf); each row by
+          // itself, so that no row's result depends on its neighbours (or on idle rows)
+          const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
+          if (!__any_sync(0xffffffffu, raise)) break;
+          const float mn = raise ? mt : m;
+          const float f = m == mn ? 1.f : ex2_approx((m - mn) * p.scale_log2);   // 0 from -inf
+          m = mn;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < DV; c += 16) {
+            float o[16];
+            tmem_ld16(t_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= f;
+            tmem_st16(t_o + c, o);
+          }
+          raised = true;
+        }
+        tmem_st32(t_s, reinterpret_cast<float*>(pk));
+        weights(1);
+        tmem_st32(t_s + 32, reinterpret_cast<float*>(pk));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
