@@ -277,8 +277,8 @@ __device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 // The same with A in tensor memory (lane = row, each 32-bit column two bf16 of consecutive k)
-// over 128 of K: eight MMAs, 8 columns of A and 16 rows (2048 bytes) of B apart.
-__device__ __forceinline__ void mma_ts8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// over 64 of K: four MMAs, 8 columns of A and 16 rows (2048 bytes) of B apart.
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p, t, e;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -290,14 +290,6 @@ __device__ __forceinline__ void mma_ts8(uint32_t d, uint32_t a, uint64_t b, uint
       "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
       "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.s32 a, %1, 32;\n\tadd.s64 b, %2, 512;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.s32 a, %1, 40;\n\tadd.s64 b, %2, 640;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.s32 a, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.s32 a, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
       "}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
@@ -336,6 +328,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+// Four lanes hold four 16-byte words each, v[4 w + k]: lane i gets word i of all four, in lane
+// order.  A thread has a row of O; stored as it lies, an instruction writes 16 bytes into each
+// of 32 rows and a unit's result takes 6500 cycles; transposed, 64 bytes into each of eight.
+__device__ __forceinline__ void transpose4(uint32_t* v, int lane) {
+  const bool b = lane & 1, c = lane & 2;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t &x = v[8 * k + i], &y = v[8 * k + 4 + i];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, b ? x : y, 1);
+      x = b ? got : x;
+      y = b ? y : got;
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t &x = v[4 * r + i], &y = v[8 + 4 * r + i];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, c ? x : y, 2);
+      x = c ? got : x;
+      y = c ? y : got;
+    }
+}
 __device__ __forceinline__ bool half_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 template <class S>
@@ -350,17 +366,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw);
   const uint32_t ring = sbase + S::kQBytes;
   // barriers: full[kLoads] and empty[kLoads] (K and V tiles in turn), q_full, q_empty, s_full[2],
-  // p_full[2], o_full[2], clean[kEdges], edge[kEdges] (a V tile on the edge lands there, so that
+  // p_full[2][2] (the halves of a tile), o_full[2], clean[kEdges], edge[kEdges] (a V tile on the edge lands there, so that
   // the warps that clean it need not follow the ring), item_full[kQueue], item_empty[kQueue],
   // drain
   const uint32_t bars = sbase + S::kBarOff;
   const uint32_t full0 = bars, empty0 = full0 + 8 * kLoads, q_full = empty0 + 8 * kLoads;
   const uint32_t q_empty = q_full + 8;
-  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16;
+  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32;
   const uint32_t clean0 = o_full + 16, edge0 = clean0 + 8 * kEdges;
   const uint32_t item_full = edge0 + 8 * kEdges, item_empty = item_full + 8 * kQueue;
   const uint32_t drain = item_empty + 8 * kQueue;
-  uint8_t* words = smem + S::kBarOff + 16 * kLoads + 16 + 48 + 16 * kEdges + 16 * kQueue + 16;
+  uint8_t* words = smem + S::kBarOff + 16 * kLoads + 16 + 64 + 16 * kEdges + 16 * kQueue + 16;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(words);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 4);
   volatile int* bad_v = reinterpret_cast<volatile int*>(words + 8);           // [kQueue]
@@ -385,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full + 8 * s, 1);
-      mbar_init(p_full + 8 * s, 4);
+      mbar_init(p_full + 16 * s, 4);
+      mbar_init(p_full + 16 * s + 8, 4);
       mbar_init(o_full + 8 * s, 1);
     }
     for (int i = 0; i < kEdges; ++i) mbar_init(clean0 + 8 * i, 64);
@@ -549,19 +566,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                   smem_desc(ring + ((i + c) % NC) * kChunk, 16, 1024, kSw128), id_qk, c > 0 ? 1u : 0u);
         mma_commit_warp(s_full + 8 * s);
       };
-      // O_s += P_s V(t)
-      auto pv = [&](int s, int t, bool first) {
+      // O_s += P_s V(t) over half of the tile's positions
+      auto pv = [&](int s, int t, int half, bool first) {
         const int slot = (t * (KC + VC) + KC) % NC;
-        const uint64_t v0 = smem_desc(ring + slot * kChunk, kChunk, 1024, kSw128);
-        const uint32_t o = tmem + 256 + 128 * s, pt = tmem + 128 * s;
+        const uint64_t v0 = desc_at(smem_desc(ring + slot * kChunk, kChunk, 1024, kSw128), 8192 * half);
+        const uint32_t o = tmem + 256 + 128 * s, pt = tmem + 128 * s + 32 * half;
         const uint32_t acc = first ? 0u : 1u;
         // V's two chunks lie at the ring's two ends (with an even KC a V tile starts in an even
         // slot of the even ring: never)
         if (VC == 2 && KC % 2 == 1 && slot == NC - 1) {
-          mma_ts8(o, pt, v0, id_pv64, acc);
-          mma_ts8(o + 64, pt, smem_desc(ring, kChunk, 1024, kSw128), id_pv64, acc);
+          mma_ts4(o, pt, v0, id_pv64, acc);
+          mma_ts4(o + 64, pt, desc_at(smem_desc(ring, kChunk, 1024, kSw128), 8192 * half), id_pv64, acc);
         } else {
-          mma_ts8(o, pt, v0, id_pv, acc);
+          mma_ts4(o, pt, v0, id_pv, acc);
         }
       };
       int base = 0, edges = 0, nq = 0;         // K/V tiles, edge tiles, Qs so far
@@ -596,10 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s = 0; s < 2; ++s) {
             const int c = s ? c1 : c0;
             if (t < c) {
-              wait(p_full + 8 * s, (done >> s) & 1);
+              wait(p_full + 16 * s, (done >> s) & 1);
+              if (!ok) break;
+              pv(s, base + t, 0, t == 0);
+              wait(p_full + 16 * s + 8, (done >> s) & 1);
               done ^= 1u << s;
               if (!ok) break;
-              pv(s, base + t, t == 0);
+              pv(s, base + t, 1, false);
               if (t + 1 == c) mma_commit_warp(o_full + 8 * s);
             }
             if (s) free_tile(base + t, 1);
@@ -765,12 +785,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           raised = true;
         }
         tmem_st32(t_s, reinterpret_cast<float*>(pk));
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 16 * s);
         weights(1);
         tmem_st32(t_s + 32, reinterpret_cast<float*>(pk));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * s);
+        if (lane == 0) mbar_arrive(p_full + 16 * s + 8);
         float s0, s1, s2, s3;
         unpair(sum[0], &s0, &s1);
         unpair(sum[1], &s2, &s3);
@@ -796,8 +820,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool none = whole && l == 0.f;
       const int h = w.hk * p.G + hg;
       const int64_t row = static_cast<int64_t>(w.row0) + tok;
-      uint16_t* orow = p.o + row * p.o_tok + h * p.o_head;
-      float* part = whole ? nullptr : p.parts + static_cast<int64_t>(w.part) * S::kPartFloats;
+      // this lane's 16-byte word goes to the rows of its group of four lanes
+      const int64_t mine = !live ? -1
+                           : whole ? row * p.o_tok + h * p.o_head
+                                   : w.part * static_cast<int64_t>(S::kPartFloats) + 4 * kRows + (s * kRows + r) * DV;
+      int64_t dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
+      float* part = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats);
       const float m2 = m == -INFINITY ? m : m * p.scale_log2;
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
@@ -818,18 +848,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (half_nonfinite(vr[i])) o[i] += __uint_as_float(static_cast<uint32_t>(vr[i]) << 16);
           }
-        if (!live) continue;
+        __syncwarp();
+        uint32_t y[16];
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(orow + c + 8 * i) =
-                make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                           pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-        } else {
-          float* at = part + 4 * kRows + (s * kRows + r) * DV + c;
+          for (int i = 0; i < 16; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+          transpose4(y, lane);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(at + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i)
+            if (dst[i] >= 0)
+              *reinterpret_cast<uint4*>(p.o + dst[i] + c + 8 * (lane & 3)) =
+                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[16 * g + i]);
+            transpose4(y, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (dst[i] >= 0)
+                *reinterpret_cast<uint4*>(p.parts + dst[i] + c + 16 * g + 4 * (lane & 3)) =
+                    make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
         }
       }
       if (live && whole && p.lse)
