@@ -69,10 +69,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;              // log2 growth of the maximum that forces a rescale
 
-// Fixed cost of a unit on the line (its Q, the first tile's way, its result) in positions,
-// and the fewest K/V tiles a part of a cut unit may have: writing and joining a part moves
+// Fixed cost of a unit on the line (its Q, the first tile's way, its result: about 12,000 cycles
+// at 20 a position) in positions, and the fewest K/V tiles a part of a cut unit may have: writing and joining a part moves
 // 266 KB, about four tiles' time of an SM.
-constexpr int kUnitCost = 256;
+constexpr int kUnitCost = 640;
 constexpr int kMinCut = 8;                 // a power of two
 constexpr int kMaxParts = 512;             // parts of one unit: at most one a span
 
@@ -88,6 +88,8 @@ struct PromptShape {
   static_assert(kSmem <= 232448, "shared memory");
 };
 
+struct Cut;
+
 struct PromptParams {
   const int32_t *qo_indptr, *kv_indptr;
   int B, Hq, Hk, G;
@@ -100,6 +102,7 @@ struct PromptParams {
   const uint16_t* v;                       // for the rows that see a non-finite value
   int64_t v_tok, v_head;
   float* parts;                            // two a CTA; null: units are not cut
+  Cut* cuts;                               // one a CTA
   int* err;
 };
 
@@ -112,6 +115,13 @@ struct Piece {
   int hk;
   int j0, j1;
   int part;         // where a cut piece leaves its result; -1: the unit is whole
+};
+
+// What the join needs of the unit whose first part a CTA leaves (tiles = 0: none).
+struct Cut {
+  Piece unit;
+  int tiles;
+  int64_t u0, weight, span;                // on the line
 };
 
 // K/V tiles that tile s of a unit needs (its last token's).
@@ -167,32 +177,45 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
   }
   return x;
 }
-// Length of the whole line (a warp together).
-__device__ __forceinline__ int64_t line_total(const PromptParams& p, int cta_tok, int lane, bool flag) {
-  int64_t x = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const Request r = load_request(p, b, cta_tok, flag);
-    x += r.cum(r.units, cta_tok);
-  }
-#pragma unroll
-  for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-  return x * p.Hk;
-}
 // A unit and where it starts on the line.
 struct Unit {
   Request r;
   int b, hk, i;
   int64_t u0;
 };
-// The unit that holds point x of the line, 0 <= x < total (a warp together).
-__device__ __forceinline__ Unit find_unit(const PromptParams& p, int cta_tok, int lane, int64_t x) {
-  Unit u;
-  u.b = 0;
+// A CTA's span [x0, x1) of the line and the unit that holds x1 - 1 (a warp together).  The
+// first 32 requests stay in the lanes' registers, so that a batch of as many pays one round
+// trip to memory.
+struct Span {
+  int64_t x0, x1, length;
+  Unit last;
+};
+__device__ __forceinline__ Span find_span(const PromptParams& p, int cta_tok, int lane) {
+  Span sp;
+  Request mine = {0, 0, 0, 0, 0};
+  int64_t total = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const Request r = load_request(p, b, cta_tok, blockIdx.x == 0);
+    if (b < 32) mine = r;
+    total += r.cum(r.units, cta_tok);
+  }
+#pragma unroll
+  for (int i = 16; i; i >>= 1) total += __shfl_xor_sync(0xffffffffu, total, i);
+  total *= p.Hk;
+  sp.length = (total + gridDim.x - 1) / gridDim.x;
+  sp.x0 = blockIdx.x * sp.length;
+  sp.x1 = sp.x0 + sp.length < total ? sp.x0 + sp.length : total;
+  Unit& u = sp.last;
+  u = {};
+  if (sp.x0 >= sp.x1) return sp;
+  const int64_t x = sp.x1 - 1;
   int64_t done = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    Request r = {0, 0, 0, 0, 0};
-    if (b < p.B) r = load_request(p, b, cta_tok, false);
+    Request r = mine;
+    if (b0 > 0) {
+      r = {0, 0, 0, 0, 0};
+      if (b0 + lane < p.B) r = load_request(p, b0 + lane, cta_tok, false);
+    }
     const int64_t n = r.cum(r.units, cta_tok) * p.Hk;
     const int64_t end = done + warp_scan(n, lane);
     const uint32_t who = __ballot_sync(0xffffffffu, x < end && x >= end - n);
@@ -200,23 +223,29 @@ __device__ __forceinline__ Unit find_unit(const PromptParams& p, int cta_tok, in
       const int src = __ffs(who) - 1;
       u.b = b0 + src;
       done = __shfl_sync(0xffffffffu, end - n, src);
+      u.r.q0 = __shfl_sync(0xffffffffu, r.q0, src);
+      u.r.T = __shfl_sync(0xffffffffu, r.T, src);
+      u.r.kv0 = __shfl_sync(0xffffffffu, r.kv0, src);
+      u.r.L = __shfl_sync(0xffffffffu, r.L, src);
+      u.r.units = __shfl_sync(0xffffffffu, r.units, src);
       break;
     }
     done = __shfl_sync(0xffffffffu, end, 31);
   }
-  u.r = load_request(p, u.b, cta_tok, false);
   const int64_t head = u.r.cum(u.r.units, cta_tok);
-  u.hk = static_cast<int>((x - done) / head);
-  const int64_t y = x - done - u.hk * head;
+  while (x - done >= head) {               // (at most Hk times)
+    done += head;
+    ++u.hk;
+  }
   int lo = 0, hi = u.r.units - 1;
-  while (lo < hi) {                        // the last unit that starts at or before y
+  while (lo < hi) {                        // the last unit that starts at or before x
     const int mid = (lo + hi + 1) >> 1;
-    if (u.r.cum(mid, cta_tok) <= y) lo = mid;
+    if (u.r.cum(mid, cta_tok) <= x - done) lo = mid;
     else hi = mid - 1;
   }
   u.i = lo;
-  u.u0 = done + u.hk * head + u.r.cum(lo, cta_tok);
-  return u;
+  u.u0 = done + u.r.cum(lo, cta_tok);
+  return sp;
 }
 __device__ __forceinline__ Piece unit_piece(const Unit& u, int cta_tok, int tok_tile) {
   Piece w;
@@ -441,13 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8) {
       // ---------------------------------------------------------- the span's pieces, TMA
-      const int64_t total = line_total(p, cta_tok, lane, blockIdx.x == 0);
-      const int64_t span = (total + gridDim.x - 1) / gridDim.x;
-      const int64_t x0 = blockIdx.x * span;
-      const int64_t x1 = x0 + span < total ? x0 + span : total;
+      const Span sp = find_span(p, cta_tok, lane);
+      const int64_t x0 = sp.x0, x1 = sp.x1;
+      Unit u = sp.last;
       const bool cuts = p.parts != nullptr;
-      Unit u = {};
-      if (x0 < x1) u = find_unit(p, cta_tok, lane, x1 - 1);
+      if (cuts && lane == 0) p.cuts[blockIdx.x].tiles = 0;
       if (lane == 0) {
         const uint32_t box = static_cast<uint32_t>(p.tok_tile) * p.G * 128;
         int i = 0, n = 0, edges = 0, nq = 0;   // chunks, loads, edge tiles, Qs so far
@@ -514,7 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.j0 = cut_at(u.u0, weight, tiles, x0, cuts);
             w.j1 = cut_at(u.u0, weight, tiles, x1, cuts);
             mine = w.j0 < w.j1;
-            if (w.j0 > 0 || w.j1 < tiles) w.part = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+            if (mine && (w.j0 > 0 || w.j1 < tiles)) {
+              w.part = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+              if (w.j0 == 0) p.cuts[blockIdx.x] = {w, tiles, u.u0, weight, sp.length};
+            }
           }
           if (mine) {
             push(w);
@@ -892,43 +922,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the unit that starts in span blockIdx.x and is cut at its end; blockIdx.y
+// Joins the parts of the unit that span blockIdx.x cuts and has the first part of; blockIdx.y
 // takes 32 of its 256 rows, eight threads a row.  Bytes bound: the parts, from L2.
 template <int DV>
-__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, int spans) {
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
   constexpr int kPart = 2 * kRows * (DV + 2);
-  __shared__ Piece sh_piece;
   __shared__ int sh_n, sh_parts[kMaxParts];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta_tok = 2 * p.tok_tile;
   const int first = blockIdx.x;
-  if (warp == 0) {
-    const int64_t total = line_total(p, cta_tok, lane, false);
-    const int64_t span = (total + spans - 1) / spans;
-    const int64_t x = (first + 1) * span;
+  const Cut& cut = p.cuts[first];
+  const int tiles = cut.tiles;
+  if (tiles == 0) return;
+  const Piece w = cut.unit;
+  if (threadIdx.x == 0) {
     int parts = 0;
-    if (x < total) {
-      const Unit u = find_unit(p, cta_tok, lane, x);
-      const int64_t weight = u.r.cum(u.i + 1, cta_tok) - u.r.cum(u.i, cta_tok);
-      const Piece w = unit_piece(u, cta_tok, p.tok_tile);
-      const int n = w.j1;
-      int t = cut_at(u.u0, weight, n, x, true);
-      if (lane == 0 && n >= 2 * kMinCut && t > 0 && t < n && cut_at(u.u0, weight, n, first * span, true) == 0) {
-        sh_parts[parts++] = 2 * first + 1;
-        for (int i = first + 1; t < n; ++i) {            // spans between two cuts, some empty
-          const int e = cut_at(u.u0, weight, n, (i + 1) * span, true);
-          if (e > t) sh_parts[parts++] = 2 * i;
-          t = e;
-        }
-        sh_piece = w;
-      }
+    sh_parts[parts++] = 2 * first + 1;
+    int t = w.j1;
+    for (int i = first + 1; t < tiles; ++i) {            // spans between two cuts, some empty
+      const int e = cut_at(cut.u0, cut.weight, tiles, (i + 1) * cut.span, true);
+      if (e > t) sh_parts[parts++] = 2 * i;
+      t = e;
     }
-    if (lane == 0) sh_n = parts;
+    sh_n = parts;
   }
   __syncthreads();
   const int n_parts = sh_n;
-  if (n_parts == 0) return;
-  const Piece w = sh_piece;
   const int row = 32 * blockIdx.y + (threadIdx.x >> 3), q = threadIdx.x & 7;
   const int s = row / kRows, r = row - s * kRows;
   const int tt = r / p.G, tok = s * p.tok_tile + tt;
@@ -1011,7 +1028,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prompt_attention_kernel<S><<<sms, kThreads, S::kSmem, stream>>>(tq, tk, tv, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.parts) return e;
-  prompt_join_kernel<DV><<<dim3(sms - 1, 8), 256, 0, stream>>>(p, sms);
+  prompt_join_kernel<DV><<<dim3(sms - 1, 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1023,10 +1040,12 @@ int sms_of_device(int* out) {
   return MLA_OK;
 }
 
-// Bytes of the parts a call may leave: none where no request can be long enough to be cut.
+// Bytes of the parts and cuts a call may leave: none where no request can be long enough to be
+// cut.
+size_t cuts_for(int sms) { return (static_cast<size_t>(sms) * sizeof(Cut) + 255) / 256 * 256; }
 size_t parts_for(int sms, int64_t n_keys, int64_t DV) {
   if (n_keys <= (2 * kMinCut - 1) * kKeys || sms < 2 || sms > kMaxParts) return 0;
-  return 2 * static_cast<size_t>(sms) * 2 * kRows * static_cast<size_t>(DV + 2) * 4;
+  return cuts_for(sms) + 2 * static_cast<size_t>(sms) * 2 * kRows * static_cast<size_t>(DV + 2) * 4;
 }
 
 // Strides TMA can step: positive where the dim has more than one entry.
@@ -1106,7 +1125,8 @@ extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k
   p.v_tok = v->stride[0];
   p.v_head = v->stride[1];
   p.err = error_word;
-  p.parts = workspace && need > 0 ? static_cast<float*>(workspace) : nullptr;
+  p.cuts = static_cast<Cut*>(workspace);
+  p.parts = workspace && need > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + cuts_for(sms)) : nullptr;
 
   EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
   if (!enc) return MLA_ERR_CUDA;
