@@ -69,10 +69,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;              // log2 growth of the maximum that forces a rescale
 
-// Fixed cost of a unit on the line (its Q, the first tile's way, its result: about 12,000 cycles
-// at 20 a position) in positions, and the fewest K/V tiles a part of a cut unit may have: writing and joining a part moves
+// Fixed cost of a unit on the line (its Q, the first tile's way, its result: about 10,000 cycles
+// at 20 a position; 256 to 640 measure alike) in positions, and the fewest K/V tiles a part of a cut unit may have: writing and joining a part moves
 // 266 KB, about four tiles' time of an SM.
-constexpr int kUnitCost = 640;
+constexpr int kUnitCost = 512;
 constexpr int kMinCut = 8;                 // a power of two
 constexpr int kMaxParts = 512;             // parts of one unit: at most one a span
 
@@ -338,6 +338,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -357,28 +362,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-// Four lanes hold four 16-byte words each, v[4 w + k]: lane i gets word i of all four, in lane
-// order.  A thread has a row of O; stored as it lies, an instruction writes 16 bytes into each
-// of 32 rows and a unit's result takes 6500 cycles; transposed, 64 bytes into each of eight.
+// Four lanes hold four 16-byte words each, v[4 w + k].  Afterwards v[4 i + k] is word lane & 3
+// of lane ^ i.  A thread has a row of O: stored as it lies, an instruction would write 16 bytes
+// into each of 32 rows; so it writes 64 bytes into each of eight.
 __device__ __forceinline__ void transpose4(uint32_t* v, int lane) {
   const bool b = lane & 1, c = lane & 2;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t &x = v[8 * k + i], &y = v[8 * k + 4 + i];
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, b ? x : y, 1);
-      x = b ? got : x;
-      y = b ? y : got;
+      const uint32_t x = v[8 * k + i], y = v[8 * k + 4 + i];
+      v[8 * k + i] = b ? y : x;
+      v[8 * k + 4 + i] = __shfl_xor_sync(0xffffffffu, b ? x : y, 1);
     }
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t &x = v[4 * r + i], &y = v[8 + 4 * r + i];
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, c ? x : y, 2);
-      x = c ? got : x;
-      y = c ? y : got;
+      const uint32_t x = v[4 * r + i], y = v[8 + 4 * r + i];
+      v[4 * r + i] = c ? y : x;
+      v[8 + 4 * r + i] = __shfl_xor_sync(0xffffffffu, c ? x : y, 2);
     }
 }
 __device__ __forceinline__ bool half_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
@@ -848,6 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = w.part < 0;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       const bool none = whole && l == 0.f;
+      const bool any_none = __any_sync(0xffffffffu, none);
       const int h = w.hk * p.G + hg;
       const int64_t row = static_cast<int64_t>(w.row0) + tok;
       // this lane's 16-byte word goes to the rows of its group of four lanes
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    : w.part * static_cast<int64_t>(S::kPartFloats) + 4 * kRows + (s * kRows + r) * DV;
       int64_t dst[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
+      for (int i = 0; i < 4; ++i) dst[i] = __shfl_xor_sync(0xffffffffu, mine, i);
       float* part = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats);
       const float m2 = m == -INFINITY ? m : m * p.scale_log2;
 #pragma unroll 1
@@ -869,8 +873,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
+        const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
+        for (int i = 0; i < 16; ++i) unpair(mul2(pair(o[2 * i], o[2 * i + 1]), inv2), &o[2 * i], &o[2 * i + 1]);
+        if (any_none) {                          // (0 * inf among weightless values)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i];
+        }
         if (fix && live)
           for (int j = e0 * kKeys; j <= lim && j < w.j1 * kKeys; ++j) {
             const uint16_t* vr = p.v + static_cast<int64_t>(w.kv0 + j) * p.v_tok + w.hk * p.v_head + c;
