@@ -8,12 +8,14 @@
 //   pair i of a row: (x, y) -> (x cos_i - y sin_i, y cos_i + x sin_i), i < R/2, the pairs
 //   (2i, 2i+1) or (i, i + R/2); columns from R on pass through.
 //
-// Bytes bound (3 flops an element).  One item is 16 columns of one row: two 16-byte loads
-// whose results two 16-byte bf16 stores (or 16 bytes of codes) take, so that every access is
-// a whole 16-byte word; 8 pairs share the item's 8 cosines and sines, which come from L1 or
-// L2 for all but a token's first head.  Arithmetic is the definition's in fp32, every
-// product, sum and quotient rounded on its own, and one rounding to the stored type (a bf16
-// value is off by at most 2^-8 of itself, an e4m3 code by 2^-4), so the bytes are exact.
+// Bytes bound (3 flops an element).  An item is two 8-column words of a row, half a region's
+// width apart (the region of rotated columns or the rest), so that eight lanes read and write
+// whole 128-byte lines; with the pairs (i, i + R/2) the two words are each other's partners,
+// with (2i, 2i+1) each holds its own pairs.  In large calls a thread takes the item of kStrip
+// heads: the item's 8 cosines and sines are read once for them and their loads are in flight
+// together.  Arithmetic is the definition's in fp32, every product, sum and quotient rounded
+// on its own, and one rounding to the stored type (a bf16 value is off by at most 2^-8 of
+// itself, an e4m3 code by 2^-4), so the bytes are exact.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -27,6 +29,8 @@ namespace {
 using namespace pmla;
 
 constexpr int kThreads = 256;
+constexpr int kStripHeads = 2;
+constexpr int kResident = 2048;     // threads a SM
 
 struct RopeAppendParams {
   const uint16_t *q, *k, *v;        // bf16 bits
@@ -45,7 +49,6 @@ struct RopeAppendParams {
   int64_t n_tok;
   int Hq, Hk;
   int half_rot;                     // R / 2
-  int neox;
   int* err;
 };
 
@@ -57,112 +60,218 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Eight fp32 values divided by s, to eight e4m3 codes.
-__device__ __forceinline__ uint2 quantise8(const float* x, float s) {
+// Two fp32 values in a register pair and the packed operations on them, each half rounded on
+// its own as the scalar operation rounds it.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Quotients by one scale.  Markstein's theorem (1990): with r = 1/s correctly rounded, q = x r
+// and e = x - q s (exact in one fused operation), q + e r rounds to the correctly rounded
+// quotient, where nothing over- or underflows.  Scales between 2^-40 and 2^40 keep e normal
+// for every x whose code is not zero; beyond +-1024 the code is saturated whatever the
+// quotient, so q stops there.  Other scales divide.
+struct Divisor {
+  float s, r;
+  bool plain;
+  __device__ __forceinline__ void divide(float& x, float& y) const {
+    if (plain) {
+      x = __fdiv_rn(x, s);
+      y = __fdiv_rn(y, s);
+      return;
+    }
+    const uint64_t v = pair(x, y), rr = pair(r, r);
+    float a, b;
+    unpair(mul2(v, rr), &a, &b);
+    a = fminf(fmaxf(a, -1024.f), 1024.f);
+    b = fminf(fmaxf(b, -1024.f), 1024.f);
+    const uint64_t q = pair(a, b);
+    unpair(fma2(fma2(q, pair(-s, -s), v), rr, q), &x, &y);
+  }
+};
+__device__ __forceinline__ Divisor make_divisor(float scale) {
+  Divisor d;
+  d.s = scale;
+  d.r = __fdiv_rn(1.f, scale);
+  d.plain = !(fabsf(scale) >= 0x1p-40f && fabsf(scale) <= 0x1p40f);
+  return d;
+}
+// Eight fp32 values divided by the scale, to eight e4m3 codes.
+__device__ __forceinline__ uint2 quantise8(const float* x, const Divisor& d) {
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i + 1], s), __fdiv_rn(x[2 * i], s));
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+    d.divide(a, b);
+    c[i] = f32x2_to_e4m3x2(b, a);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 __device__ __forceinline__ uint4 round8(const float* x) {
   return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kNeox, int kStrip>
 __global__ void __launch_bounds__(kThreads) gqa_rope_append_kernel(const RopeAppendParams p) {
   constexpr int kPieces = D / 16;
-  const int rows = p.Hq + 2 * p.Hk;
-  const uint32_t per_tok = static_cast<uint32_t>(rows) * kPieces;
-  // the block's first item by one 64-bit division, the thread's by a 32-bit one
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads;
-  const int64_t t0 = base / per_tok;
-  const uint32_t local = static_cast<uint32_t>(base - t0 * per_tok) + threadIdx.x;
-  const int64_t t = t0 + local / per_tok;
-  if (t >= p.n_tok) return;
-  const uint32_t item = local % per_tok;
-  const int row = static_cast<int>(item / kPieces);
-  const int piece = static_cast<int>(item % kPieces);
-  const bool is_q = row < p.Hq;
-  const bool is_k = !is_q && row < p.Hq + p.Hk;
-  const int h = is_q ? row : (is_k ? row - p.Hq : row - p.Hq - p.Hk);
+  // strips of heads a token: q, then k, then v; a thread keeps its item from token to token
+  const int q_strips = (p.Hq + kStrip - 1) / kStrip, k_strips = (p.Hk + kStrip - 1) / kStrip;
+  const int item = blockIdx.y * blockDim.x + threadIdx.x;
+  const int strip = item / kPieces;
+  const int piece = item % kPieces;
+  if (strip >= q_strips + 2 * k_strips) return;
+  const bool is_q = strip < q_strips;
+  const bool is_k = !is_q && strip < q_strips + k_strips;
+  const int h0 = (is_q ? strip : (is_k ? strip - q_strips : strip - q_strips - k_strips)) * kStrip;
+  const int heads = is_q ? p.Hq : p.Hk;
 
-  // columns of the item's two 16-byte words
+  // columns of the item's words
   const bool rot = (is_q || is_k) && piece * 8 < p.half_rot;
-  const bool halves = rot && p.neox;
-  const int c0 = halves ? 8 * piece : 16 * piece;
-  const int c1 = halves ? p.half_rot + 8 * piece : 16 * piece + 8;
-  const uint16_t* src = is_q ? p.q + t * p.q_tok + h * p.q_head
-                             : (is_k ? p.k + t * p.k_tok + h * p.k_head
-                                     : p.v + t * p.v_tok + h * p.v_head);
-  // loads that depend on no other first
-  const uint4 a = *reinterpret_cast<const uint4*>(src + c0);
-  const uint4 b = *reinterpret_cast<const uint4*>(src + c1);
-  const int32_t slot = is_q ? -1 : __ldg(p.slot_mapping + t);
-  float scale = 1.f;
-  if (kFp8 && !is_q) scale = __ldg(is_k ? p.k_scale : p.v_scale);
+  const int first = rot || !(is_q || is_k) ? 0 : 2 * p.half_rot;     // the region's first column
+  const int half = rot ? p.half_rot : (D - first) / 2;
+  const int c0 = first + 8 * (piece - first / 16);                   // the other: half further on
+  const int64_t head = is_q ? p.q_head : (is_k ? p.k_head : p.v_head);
+  const int64_t tok = is_q ? p.q_tok : (is_k ? p.k_tok : p.v_tok);
+  const uint16_t* src0 = (is_q ? p.q : (is_k ? p.k : p.v)) + h0 * head + c0;
+  const int64_t dst_head = is_q ? p.qo_head : p.ko_head, dst_tok = is_q ? p.qo_tok : p.ko_tok;
+  uint16_t* dst0 = is_q ? p.q_out : (is_k ? p.k_out : nullptr);
+  if (dst0) dst0 += h0 * dst_head + c0;
+  uint8_t* cache = (is_k ? p.k_cache : p.v_cache) + h0 * p.head_pitch + c0 * (kFp8 ? 1 : 2);
+  Divisor div = {};
+  if (kFp8 && !is_q) div = make_divisor(__ldg(is_k ? p.k_scale : p.v_scale));
 
-  float x[8], y[8];   // the results for c0 .. c0+7 and c1 .. c1+7
-  {
-    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+  int64_t t = blockIdx.x;
+  int32_t pos = rot ? __ldg(p.positions + t) : 0, slot = is_q ? -1 : __ldg(p.slot_mapping + t);
+  while (true) {
+    // loads that depend on no other first: the item's words, its angles, and the next token's
+    // position and slot
+    uint4 a[kStrip], b[kStrip];
+    const uint16_t* src = src0 + t * tok;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = lo_f32(wa[i]);
-      x[2 * i + 1] = hi_f32(wa[i]);
-      y[2 * i] = lo_f32(wb[i]);
-      y[2 * i + 1] = hi_f32(wb[i]);
-    }
-  }
-  if (rot) {
-    const int32_t pos = __ldg(p.positions + t);
-    if (pos < 0 || pos >= p.max_pos) {
-      if (row == 0 && piece == 0) atomicOr(p.err, kErrBadIndex);
-      return;                       // the token's rotated columns stay unwritten
-    }
-    const float* cs = p.cos_sin + pos * p.cs_row + 8 * piece;
+    for (int i = 0; i < kStrip; ++i)
+      if (h0 + i < heads) {
+        a[i] = *reinterpret_cast<const uint4*>(src + i * head);
+        b[i] = *reinterpret_cast<const uint4*>(src + i * head + half);
+      }
     float c[8], s[8];
-    *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(cs));
-    *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(cs + 4));
-    *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(cs + p.half_rot));
-    *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(cs + p.half_rot + 4));
+    const bool known = pos >= 0 && pos < p.max_pos;
+    if (rot && known) {
+      // the angles of the first word's pairs and of the second's (halves: one set of eight)
+      const float* cs = p.cos_sin + pos * p.cs_row;
+      const int i0 = kNeox ? 8 * piece : 4 * piece, i1 = kNeox ? i0 + 4 : i0 + p.half_rot / 2;
+      *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(cs + i0));
+      *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(cs + i1));
+      *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(cs + p.half_rot + i0));
+      *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(cs + p.half_rot + i1));
+    }
+    const int64_t t_next = t + gridDim.x;
+    int32_t pos_next = 0, slot_next = -1;
+    if (t_next < p.n_tok) {
+      if (rot) pos_next = __ldg(p.positions + t_next);
+      if (!is_q) slot_next = __ldg(p.slot_mapping + t_next);
+    }
+    const bool bad_slot = slot >= p.n_slots;
+    if (bad_slot && is_k && h0 == 0 && piece == 0) atomicOr(p.err, kErrBadRowId);
+    if (!known && strip == 0 && piece == 0) atomicOr(p.err, kErrBadIndex);
+    uint8_t* entry = nullptr;
+    if (slot >= 0 && !bad_slot)
+      entry = cache + (slot >> p.log2_page) * p.page_pitch + (slot & ((1 << p.log2_page) - 1)) * p.slot_pitch;
+    uint16_t* dst = dst0 ? dst0 + t * dst_tok : nullptr;
+
+    if (known)                                     // else the token's rotated columns stay unwritten
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // halves: the pair is (x[i], y[i]); interleaved: neighbours of one word
-      float& u = halves ? x[i] : (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]);
-      float& w = halves ? y[i] : (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]);
-      const float u0 = u, w0 = w;
-      u = __fsub_rn(__fmul_rn(u0, c[i]), __fmul_rn(w0, s[i]));
-      w = __fadd_rn(__fmul_rn(w0, c[i]), __fmul_rn(u0, s[i]));
+    for (int i = 0; i < kStrip; ++i) {
+      if (h0 + i >= heads) break;
+      float x[8], y[8];   // the results for c0 .. c0+7 and c1 .. c1+7
+      {
+        const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[2 * k] = lo_f32(wa[k]);
+          x[2 * k + 1] = hi_f32(wa[k]);
+          y[2 * k] = lo_f32(wb[k]);
+          y[2 * k + 1] = hi_f32(wb[k]);
+        }
+      }
+      if (rot) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          // two pairs (u, w) at once; halves: u in x, w in y; interleaved: neighbours
+          float& u0 = kNeox ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]);
+          float& w0 = kNeox ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
+          float& u1 = kNeox ? x[k + 1] : (k < 4 ? x[2 * k + 2] : y[2 * k - 6]);
+          float& w1 = kNeox ? y[k + 1] : (k < 4 ? x[2 * k + 3] : y[2 * k - 5]);
+          const uint64_t u = pair(u0, u1), w = pair(w0, w1);
+          const uint64_t cc = pair(c[k], c[k + 1]), ss = pair(s[k], s[k + 1]), ms = pair(-s[k], -s[k + 1]);
+          unpair(add2(mul2(u, cc), mul2(w, ms)), &u0, &u1);
+          unpair(add2(mul2(w, cc), mul2(u, ss)), &w0, &w1);
+        }
+      }
+      // columns that pass through keep their bits in bf16
+      const uint4 out0 = rot ? round8(x) : a[i], out1 = rot ? round8(y) : b[i];
+      if (dst) {
+        *reinterpret_cast<uint4*>(dst + i * dst_head) = out0;
+        *reinterpret_cast<uint4*>(dst + i * dst_head + half) = out1;
+      }
+      if (!entry) continue;
+      uint8_t* at = entry + i * p.head_pitch;
+      if (!kFp8) {
+        *reinterpret_cast<uint4*>(at) = out0;
+        *reinterpret_cast<uint4*>(at + 2 * half) = out1;
+      } else {
+        *reinterpret_cast<uint2*>(at) = quantise8(x, div);
+        *reinterpret_cast<uint2*>(at + half) = quantise8(y, div);
+      }
     }
+    if (t_next >= p.n_tok) break;
+    t = t_next;
+    pos = pos_next;
+    slot = slot_next;
   }
-  // columns that pass through keep their bits in bf16
-  const uint4 out0 = rot ? round8(x) : a, out1 = rot ? round8(y) : b;
-  uint16_t* dst = nullptr;
-  if (is_q) dst = p.q_out + t * p.qo_tok + h * p.qo_head;
-  if (is_k && p.k_out) dst = p.k_out + t * p.ko_tok + h * p.ko_head;
-  if (dst) {
-    *reinterpret_cast<uint4*>(dst + c0) = out0;
-    *reinterpret_cast<uint4*>(dst + c1) = out1;
-  }
-  if (is_q || slot < 0) return;
-  if (slot >= p.n_slots) {
-    if (is_k && h == 0 && piece == 0) atomicOr(p.err, kErrBadRowId);
-    return;
-  }
-  uint8_t* entry = (is_k ? p.k_cache : p.v_cache) + (slot >> p.log2_page) * p.page_pitch +
-                   (slot & ((1 << p.log2_page) - 1)) * p.slot_pitch + h * p.head_pitch;
-  if (!kFp8) {
-    *reinterpret_cast<uint4*>(entry + 2 * c0) = out0;
-    *reinterpret_cast<uint4*>(entry + 2 * c1) = out1;
-  } else {
-    const uint2 e0 = quantise8(x, scale), e1 = quantise8(y, scale);
-    if (halves) {
-      *reinterpret_cast<uint2*>(entry + c0) = e0;
-      *reinterpret_cast<uint2*>(entry + c1) = e1;
-    } else {
-      *reinterpret_cast<uint4*>(entry + c0) = make_uint4(e0.x, e0.y, e1.x, e1.y);
-    }
-  }
+}
+
+template <int D, bool kFp8, bool kNeox>
+int launch(const RopeAppendParams& p, int sms, cudaStream_t s) {
+  const int64_t rows = p.n_tok * (p.Hq + 2 * p.Hk);
+  // strips pay once there are items for several full waves of threads
+  const bool strips = rows * (D / 16) >= static_cast<int64_t>(sms) * 2048 * 4;
+  const int n = strips ? kStripHeads : 1;
+  const int items = ((p.Hq + n - 1) / n + 2 * ((p.Hk + n - 1) / n)) * (D / 16);
+  const int threads = items < kThreads ? (items + 31) / 32 * 32 : kThreads;
+  const unsigned parts = (items + threads - 1) / threads;
+  // as many blocks as stay resident, each going from token to token
+  int64_t blocks = static_cast<int64_t>(sms) * kResident / (threads * parts);
+  if (blocks > p.n_tok || blocks < 1) blocks = blocks < 1 ? 1 : p.n_tok;
+  const dim3 grid(static_cast<unsigned>(blocks), parts);
+  if (strips) gqa_rope_append_kernel<D, kFp8, kNeox, kStripHeads><<<grid, threads, 0, s>>>(p);
+  else gqa_rope_append_kernel<D, kFp8, kNeox, 1><<<grid, threads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+template <int D>
+int launch(const RopeAppendParams& p, bool fp8, bool neox, int sms, cudaStream_t s) {
+  if (fp8) return neox ? launch<D, true, true>(p, sms, s) : launch<D, true, false>(p, sms, s);
+  return neox ? launch<D, false, true>(p, sms, s) : launch<D, false, false>(p, sms, s);
 }
 
 }  // namespace
@@ -230,20 +339,12 @@ extern "C" int mla_gqa_rope_and_cache(
   p.Hq = static_cast<int>(Hq);
   p.Hk = static_cast<int>(Hk);
   p.half_rot = static_cast<int>(R / 2);
-  p.neox = is_neox;
   p.err = error_word;
 
-  const int64_t items = T * (Hq + 2 * Hk) * (D / 16);
-  const int64_t blocks = (items + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(blocks);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  if (D == 64) {
-    if (c.fp8) gqa_rope_append_kernel<64, true><<<grid, kThreads, 0, s>>>(p);
-    else gqa_rope_append_kernel<64, false><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (c.fp8) gqa_rope_append_kernel<128, true><<<grid, kThreads, 0, s>>>(p);
-    else gqa_rope_append_kernel<128, false><<<grid, kThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return D == 64 ? launch<64>(p, c.fp8, is_neox, sms, s) : launch<128>(p, c.fp8, is_neox, sms, s);
 }
