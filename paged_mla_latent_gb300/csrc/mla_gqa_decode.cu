@@ -119,6 +119,7 @@ struct DecodeShape {
   static constexpr int kBuf = kWarps * kWarpBytes > kJoinBytes ? kWarps * kWarpBytes : kJoinBytes;
   static constexpr int kSmem = kBuf + 2 * kWarps * kHeads * 4;
   static constexpr int kSlotFloats = kHeads * (D + 2);
+  static constexpr int kAhead = NT < 4 ? 10 : 2;           // half of a join's loads in flight a thread
   // what a unit costs besides its tiles (page ids, the first tile's way from DRAM, the joins:
   // about 2.5 us), in tiles at a CTA's share of the bandwidth (22 bytes a ns)
   static constexpr int kUnitCost = 55000 / kTileBytes;
@@ -358,13 +359,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int t_load = t0 + warp;
-    int page = page_of(t_load);
-#pragma unroll 1
-    for (int s = 0; s < S::kStages - 1; ++s) {
-      const int next = page_of(t_load + kWarps);
-      issue(t_load, s, page);
-      page = next;
-      t_load += kWarps;
+    int page;
+    {
+      int ahead[S::kStages];               // the first tiles' page ids, read together
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i) ahead[i] = page_of(t_load + i * kWarps);
+#pragma unroll
+      for (int i = 0; i < S::kStages - 1; ++i) issue(t_load + i * kWarps, i, ahead[i]);
+      t_load += (S::kStages - 1) * kWarps;
+      page = ahead[S::kStages - 1];
     }
 
     // ---- q fragments: head 8 nt + g, columns as the K fragments hold them
@@ -575,31 +578,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
         }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == n_tiles;
+    // columns d .. d+3 of the chunk's head h, and its lse
+    auto finish = [&](int h, int d, const float* oo, float mm, float ll) {
+      const int hq = hk * p.G + h0 + h;
+      const bool none = ll == 0.f;
+      const float f = none ? 0.f : vscale / ll;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_o(p, b, hq, d + i, none ? 0.f : oo[i] * f);
+      if (d == 0 && p.lse)
+        p.lse[static_cast<int64_t>(b) * p.Hq + hq] =
+            none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - (kFp8 ? 14.f * kLn2 : 0.f);
+    };
     float* slot = p.slots + (2 * static_cast<int64_t>(cta) + (t0 == 0 ? 1 : 0)) * S::kSlotFloats;
-    for (int e = tid; e < nh * D; e += kThreads) {
+    for (int e = 4 * tid; e < nh * D; e += 4 * kThreads) {
       const int h = e / D, d = e - h * D;
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * kHeads + h]);
-      float ll = 0.f, oo = 0.f;
+      float ll = 0.f, oo[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = s_m[w * kHeads + h];
-        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mm);
-        // a warp with no position keeps m = -inf, l = 0; one whose scores are all -inf or
-        // NaN keeps its l
-        ll += mw == -INFINITY ? s_l[w * kHeads + h] : f * s_l[w * kHeads + h];
-        oo += mw == -INFINITY ? s_o[(w * kHeads + h) * D + d] : f * s_o[(w * kHeads + h) * D + d];
+        // a warp with no position keeps m = -inf, l = 0, o = 0; one whose scores are all -inf
+        // or NaN keeps its l and o
+        const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - mm);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * D + d);
+        ll += f * s_l[w * kHeads + h];
+        oo[0] += f * x.x;
+        oo[1] += f * x.y;
+        oo[2] += f * x.z;
+        oo[3] += f * x.w;
       }
       if (whole) {
-        const int hq = hk * p.G + h0 + h;
-        const bool none = ll == 0.f;
-        store_o(p, b, hq, d, none ? 0.f : oo / ll * vscale);
-        if (d == 0 && p.lse)
-          p.lse[static_cast<int64_t>(b) * p.Hq + hq] =
-              none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - (kFp8 ? 14.f * kLn2 : 0.f);
+        finish(h, d, oo, mm, ll);
       } else {
-        slot[2 * kHeads + e] = oo;
+        *reinterpret_cast<float4*>(slot + 2 * kHeads + e) = make_float4(oo[0], oo[1], oo[2], oo[3]);
         if (d == 0) {
           slot[h] = mm;
           slot[kHeads + h] = ll;
@@ -610,37 +623,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
       // ---- the last span to arrive joins the unit's pieces, in the spans' order
       const int64_t first = quotient(u0 + S::kUnitCost - 1, span);
       const int64_t last = quotient(u0 + n_tiles - S::kUnitCost, span);
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
         int* c = p.counters + first;
+        __threadfence();                   // the CTA's part before its arrival
         const int seen = atomicAdd(c, 1);
         sh_last = seen == last - first;
         if (sh_last) *c = 0;               // as it was found, for the next call
+        __threadfence();                   // the others' parts after theirs
       }
       __syncthreads();
       if (sh_last) {
-        __threadfence();
-        // a warp a head: the pieces' maxima and sums, lanes over pieces
         const int np = static_cast<int>(last - first) + 1;
         float* s_f = reinterpret_cast<float*>(smem);         // [piece][head], over the rings
-        auto slot_of = [&](int i) {
-          return p.slots + (2 * (first + i) + (i == 0 ? 1 : 0)) * S::kSlotFloats;
-        };
+        float* s_s = s_f + np * kHeads;
+        // parts lie two slots apart, the first one a slot further on
+        const float* parts = p.slots + 2 * first * S::kSlotFloats;
+        for (int e = tid; e < np * kHeads; e += kThreads) {
+          const int i = e / kHeads, h = e - i * kHeads;
+          const float* sl = parts + (2 * i + (i == 0 ? 1 : 0)) * S::kSlotFloats;
+          s_f[e] = h < nh ? __ldcg(sl + h) : 0.f;
+          s_s[e] = h < nh ? __ldcg(sl + kHeads + h) : 0.f;
+        }
+        __syncthreads();
+        // a warp a head, lanes over pieces
         for (int h = warp; h < nh; h += kWarps) {
           float mm = -INFINITY, ll = 0.f;
-          for (int i = lane; i < np; i += 32) {
-            const float mw = __ldcg(slot_of(i) + h);
-            s_f[i * kHeads + h] = mw;
-            mm = fmaxf(mm, mw);
-          }
+          for (int i = lane; i < np; i += 32) mm = fmaxf(mm, s_f[i * kHeads + h]);
 #pragma unroll
           for (int x16 = 16; x16; x16 >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x16));
           for (int i = lane; i < np; i += 32) {
             const float mw = s_f[i * kHeads + h];
             const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - mm);
             s_f[i * kHeads + h] = f;
-            ll += f * __ldcg(slot_of(i) + kHeads + h);
+            ll += f * s_s[i * kHeads + h];
           }
 #pragma unroll
           for (int x16 = 16; x16; x16 >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x16);
@@ -650,26 +666,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
           }
         }
         __syncthreads();
-        for (int e = 4 * tid; e < nh * D; e += 4 * kThreads) {
-          const int h = e / D, d = e - h * D;
-          float oo[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 16
-          for (int i = 0; i < np; ++i) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(slot_of(i) + 2 * kHeads + e));
-            const float f = s_f[i * kHeads + h];
-            oo[0] += f * x.x;
-            oo[1] += f * x.y;
-            oo[2] += f * x.z;
-            oo[3] += f * x.w;
-          }
-          const int hq = hk * p.G + h0 + h;
-          const float ll = s_l[h], mm = s_m[h];
-          const bool none = ll == 0.f;
+        constexpr int kEach = 4 * kThreads;  // columns the threads take at once
+        for (int e0 = 4 * tid; e0 < nh * D; e0 += 2 * kEach) {
+          const bool two = e0 + kEach < nh * D;
+          const int h = e0 / D, h2 = (e0 + kEach) / D;
+          float oo[8] = {};
+          for (int i0 = 0; i0 < np; i0 += S::kAhead) {       // 2 kAhead loads in flight a thread
+            float4 x[2 * S::kAhead];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) store_o(p, b, hq, d + i, none ? 0.f : oo[i] / ll * vscale);
-          if (d == 0 && p.lse)
-            p.lse[static_cast<int64_t>(b) * p.Hq + hq] =
-                none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - (kFp8 ? 14.f * kLn2 : 0.f);
+            for (int i = 0; i < S::kAhead; ++i)
+              if (i0 + i < np) {
+                const float* at = parts + (2 * (i0 + i) + (i0 + i == 0 ? 1 : 0)) * S::kSlotFloats + 2 * kHeads + e0;
+                x[2 * i] = __ldcg(reinterpret_cast<const float4*>(at));
+                if (two) x[2 * i + 1] = __ldcg(reinterpret_cast<const float4*>(at + kEach));
+              }
+#pragma unroll
+            for (int i = 0; i < S::kAhead; ++i) {
+              if (i0 + i >= np) break;
+              const float f = s_f[(i0 + i) * kHeads + h];
+              oo[0] += f * x[2 * i].x;
+              oo[1] += f * x[2 * i].y;
+              oo[2] += f * x[2 * i].z;
+              oo[3] += f * x[2 * i].w;
+              if (!two) continue;
+              const float f2 = s_f[(i0 + i) * kHeads + h2];
+              oo[4] += f2 * x[2 * i + 1].x;
+              oo[5] += f2 * x[2 * i + 1].y;
+              oo[6] += f2 * x[2 * i + 1].z;
+              oo[7] += f2 * x[2 * i + 1].w;
+            }
+          }
+          finish(h, e0 % D, oo, s_m[h], s_l[h]);
+          if (two) finish(h2, (e0 + kEach) % D, oo + 4, s_m[h2], s_l[h2]);
         }
       }
     }
