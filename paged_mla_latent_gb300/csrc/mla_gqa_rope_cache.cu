@@ -60,8 +60,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Two fp32 values in a register pair and the packed operations on them, each half rounded on
-// its own as the scalar operation rounds it.
+// Two fp32 values in a register pair and the packed operations on them.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -73,11 +72,6 @@ __device__ __forceinline__ void unpair(uint64_t x, float* lo, float* hi) {
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -223,8 +217,17 @@ __global__ void __launch_bounds__(kThreads) gqa_rope_append_kernel(const RopeApp
           float& w1 = kNeox ? y[k + 1] : (k < 4 ? x[2 * k + 3] : y[2 * k - 5]);
           const uint64_t u = pair(u0, u1), w = pair(w0, w1);
           const uint64_t cc = pair(c[k], c[k + 1]), ss = pair(s[k], s[k + 1]), ms = pair(-s[k], -s[k + 1]);
-          unpair(add2(mul2(u, cc), mul2(w, ms)), &u0, &u1);
-          unpair(add2(mul2(w, cc), mul2(u, ss)), &w0, &w1);
+          // (the sums are scalar: a packed sum of packed products comes out fused, its products
+          // unrounded)
+          float a0, a1, b0, b1;
+          unpair(mul2(u, cc), &a0, &a1);
+          unpair(mul2(w, ms), &b0, &b1);
+          u0 = __fadd_rn(a0, b0);
+          u1 = __fadd_rn(a1, b1);
+          unpair(mul2(w, cc), &a0, &a1);
+          unpair(mul2(u, ss), &b0, &b1);
+          w0 = __fadd_rn(a0, b0);
+          w1 = __fadd_rn(a1, b1);
         }
       }
       // columns that pass through keep their bits in bf16

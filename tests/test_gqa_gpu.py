@@ -112,6 +112,46 @@ def test_append(pm, T, Hq, Hk, D, R, neox, ps, fp8, layout):
         assert ((rest == 0x7F) if fp8 else rest.isnan()).all()
 
 
+@pytest.mark.parametrize("scale", [None, 1.0, 0.0237, 3e-13, 2.0 ** 41, 1e-20])
+@pytest.mark.parametrize("neox", [0, 1])
+def test_append_is_exact(pm, neox, scale):
+    """The definition's fp32 arithmetic, every operation rounded on its own, bit for bit (torch's
+    elementwise operations round so), for scales on both sides of the quotients' two ways."""
+    T, H, D, R = 5000, 2, 128, 96
+    g = _gen(11 + neox)
+    q, k, v = _randn(g, T, H, D), _randn(g, T, H, D), _randn(g, T, H, D, std=3.0)
+    if scale:
+        k, v = (x.float().mul(min(scale, 1e36) * 40).bfloat16() for x in (k, v))
+        v[0, 0, :6] = torch.tensor([math.inf, -math.inf, math.nan, 3e38, -3e38, 1e-38], device=DEV).bfloat16()
+    pos = torch.randint(0, 70000, (T,), generator=g, device=DEV, dtype=torch.int32)
+    cs = _table(70000, R)
+    kc, vc = _cache(T, 1, H, D, scale is not None, "nhd")
+    s = None if scale is None else torch.tensor(scale, device=DEV)
+    slots, err = torch.arange(T, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_out = torch.empty_like(q)
+    pm.mla_gqa_rope_and_cache(q, k, v, pos, cs, neox, slots, q_out, kc, vc, err, s, s)
+    row = cs[pos.long()][:, None]
+    c, sn = row[..., :R // 2], row[..., R // 2:]
+
+    def turned(x):
+        x = x.float()
+        a, b = (x[..., :R // 2], x[..., R // 2:R]) if neox else (x[..., 0:R:2], x[..., 1:R:2])
+        u, w = a * c - b * sn, b * c + a * sn
+        front = torch.cat([u, w], -1) if neox else torch.stack([u, w], -1).flatten(-2)
+        return torch.cat([front, x[..., R:]], -1)
+
+    def bits(x):
+        return x.view(torch.uint8 if x.dtype == torch.float8_e4m3fn else torch.int16)
+
+    assert torch.equal(bits(q_out), bits(turned(q).bfloat16()))
+    for cache, x in ((kc, turned(k)), (vc, v.float())):
+        want = x.bfloat16() if scale is None else (x / s).clamp(-448, 448).to(torch.float8_e4m3fn)
+        got = cache[:, 0]
+        nan = want.float().isnan()
+        assert torch.equal(got.float().isnan(), nan)
+        assert torch.equal(bits(got)[~nan], bits(want)[~nan])
+
+
 @pytest.mark.parametrize("neox", [0, 1])
 def test_append_in_place(pm, neox):
     g = _gen(3)
