@@ -362,11 +362,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-// Four lanes hold four 16-byte words each, v[4 w + k].  Afterwards v[4 i + k] is word lane & 3
-// of lane ^ i.  A thread has a row of O: stored as it lies, an instruction would write 16 bytes
-// into each of 32 rows; so it writes 64 bytes into each of eight.
-__device__ __forceinline__ void transpose4(uint32_t* v, int lane) {
-  const bool b = lane & 1, c = lane & 2;
+// Two lanes hold two 16-byte words each, v[4 w + k], twice.  Afterwards v[4 i + k] is word
+// lane & 1 of lane ^ i.  A thread has a row of O: stored as it lies, an instruction would write
+// 16 bytes into each of 32 rows; so it writes whole 32-byte sectors of 16.
+__device__ __forceinline__ void transpose2(uint32_t* v, int lane) {
+  const bool b = lane & 1;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -374,14 +374,6 @@ __device__ __forceinline__ void transpose4(uint32_t* v, int lane) {
       const uint32_t x = v[8 * k + i], y = v[8 * k + 4 + i];
       v[8 * k + i] = b ? y : x;
       v[8 * k + 4 + i] = __shfl_xor_sync(0xffffffffu, b ? x : y, 1);
-    }
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t x = v[4 * r + i], y = v[8 + 4 * r + i];
-      v[4 * r + i] = c ? y : x;
-      v[8 + 4 * r + i] = __shfl_xor_sync(0xffffffffu, c ? x : y, 2);
     }
 }
 __device__ __forceinline__ bool half_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
@@ -642,7 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_tile(base + t, 1);
           }
           bool k_here = false;
-#pragma unroll
+          // (rolled: the roles share the SM's instruction caches, and a tile's two copies here cost
+          // 24 packed prompts 323 us instead of 292)
+#pragma unroll 1
           for (int s = 0; s < 2; ++s) {
             const int c = s ? c1 : c0;
             if (t < c) {
@@ -757,7 +751,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j >= e0) {
           const int last = lim - j * kKeys;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
+          for (int c = 0; c < 128; c += 32) {
+            const int n = last - c + 1;          // columns of this group that the row sees
+            const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[c + i] = seen & (1u << i) ? x[c + i] : -INFINITY;
+          }
         }
         // The first half's weights are taken with the old maximum while the tile's own is
         // found, and taken again in the rare case that it has to be raised.
@@ -854,14 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_none = __any_sync(0xffffffffu, none);
       const int h = w.hk * p.G + hg;
       const int64_t row = static_cast<int64_t>(w.row0) + tok;
-      // this lane's 16-byte word goes to the rows of its group of four lanes
-      const int64_t mine = !live ? -1
-                           : whole ? row * p.o_tok + h * p.o_head
-                                   : w.part * static_cast<int64_t>(S::kPartFloats) + 4 * kRows + (s * kRows + r) * DV;
-      int64_t dst[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = __shfl_xor_sync(0xffffffffu, mine, i);
-      float* part = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats);
+      // this lane's words go to its row and its neighbour's
+      const int64_t mine = live ? row * p.o_tok + h * p.o_head : -1;
+      const int64_t dst[2] = {mine, __shfl_xor_sync(0xffffffffu, mine, 1)};
+      float* stats = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats) + s * kRows + r;
+      float* part = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats) + 4 * kRows + (s * kRows + r) * DV;
       const float m2 = m == -INFINITY ? m : m * p.scale_log2;
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
@@ -880,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i];
         }
-        if (fix && live)
+        if (__builtin_expect(fix && live, 0))
           for (int j = e0 * kKeys; j <= lim && j < w.j1 * kKeys; ++j) {
             const uint16_t* vr = p.v + static_cast<int64_t>(w.kv0 + j) * p.v_tok + w.hk * p.v_head + c;
 #pragma unroll
@@ -892,31 +888,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (whole) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
-          transpose4(y, lane);
+          transpose2(y, lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (dst[i] >= 0)
-              *reinterpret_cast<uint4*>(p.o + dst[i] + c + 8 * (lane & 3)) =
+            if (dst[i & 1] >= 0)
+              *reinterpret_cast<uint4*>(p.o + dst[i & 1] + c + 16 * (i >> 1) + 8 * (lane & 1)) =
                   make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-        } else {
+        } else if (live) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[16 * g + i]);
-            transpose4(y, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (dst[i] >= 0)
-                *reinterpret_cast<uint4*>(p.parts + dst[i] + c + 16 * g + 4 * (lane & 3)) =
-                    make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(part + c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (live && whole && p.lse)
         p.lse[row * p.Hq + h] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m2) * kLn2 + logf(l);
       if (live && !whole) {
-        part[s * kRows + r] = m2;
-        part[2 * kRows + s * kRows + r] = l;
+        stats[0] = m2;
+        stats[2 * kRows] = l;
       }
       tc_fence_before();                       // O is read before the next piece's P arrives
     }
