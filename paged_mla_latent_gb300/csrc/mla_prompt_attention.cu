@@ -459,10 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(item_empty + 8 * (it % kQueue));
   };
 
-  // A softmax thread holds a row of S: 128 registers.  At the launch's 168 it spills, into an
-  // L1 of which shared memory leaves almost nothing.  2 x 200 + 104 = 3 x 168.
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8) {
       // ---------------------------------------------------------- the span's pieces, TMA
       const Span sp = find_span(p, cta_tok, lane);
@@ -634,9 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_tile(base + t, 1);
           }
           bool k_here = false;
-          // (rolled: the roles share the SM's instruction caches, and a tile's two copies here cost
-          // 24 packed prompts 323 us instead of 292)
-#pragma unroll 1
+#pragma unroll
           for (int s = 0; s < 2; ++s) {
             const int c = s ? c1 : c0;
             if (t < c) {
@@ -717,7 +712,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax, one row a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int s = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -739,36 +733,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_bcast(mbar_wait(s_full + 8 * s, done & 1, abort_flag, p.err));
         if (!ok) break;
         tc_fence_after();
-        float x[128];
-        tmem_ld32(t_s, x);
-        tmem_ld32(t_s + 32, x + 32);
-        tmem_ld32(t_s + 64, x + 64);
-        tmem_ld32(t_s + 96, x + 96);
-        tmem_wait_ld_regs(x, x + 16);
-        tmem_wait_ld_regs(x + 32, x + 48);
-        tmem_wait_ld_regs(x + 64, x + 80);
-        tmem_wait_ld_regs(x + 96, x + 112);
-        if (j >= e0) {
-          const int last = lim - j * kKeys;
+        // two passes over S, 64 columns at a time, in loops: the roles share the SM's instruction
+        // caches, which a row of 128 registers and its unrolled code overran
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float x[64];
+          tmem_ld32(t_s + 64 * half, x);
+          tmem_ld32(t_s + 64 * half + 32, x + 32);
+          tmem_wait_ld_regs(x, x + 16);
+          tmem_wait_ld_regs(x + 32, x + 48);
+          if (j >= e0) {
+            const int last = lim - j * kKeys - 64 * half;
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            const int n = last - c + 1;          // columns of this group that the row sees
-            const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+            for (int c = 0; c < 64; c += 32) {
+              const int n = last - c + 1;          // columns of this group that the row sees
+              const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[c + i] = seen & (1u << i) ? x[c + i] : -INFINITY;
+              for (int i = 0; i < 32; ++i) x[c + i] = seen & (1u << i) ? x[c + i] : -INFINITY;
+            }
+            tmem_st32(t_s + 64 * half, x);
+            tmem_st32(t_s + 64 * half + 32, x + 32);
+          }
+          float mx[2] = {x[0], x[1]};
+#pragma unroll
+          for (int i = 2; i < 62; i += 4) {
+            mx[0] = max3(mx[0], x[i], x[i + 2]);
+            mx[1] = max3(mx[1], x[i + 1], x[i + 3]);
+          }
+          mt = fmaxf(mt, max3(fmaxf(mx[0], mx[1]), x[62], x[63]));
+        }
+        if (j >= e0) tmem_wait_st();
+        // raise the maximum where it grew by more than kRaise (always from -inf); each row by
+        // itself, so that no row's result depends on its neighbours (or on idle rows)
+        const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = raise ? mt : m;
+          const float f = m == mn ? 1.f : ex2_approx((m - mn) * p.scale_log2);   // 0 from -inf
+          m = mn;
+          l *= f;
+          if (j > w.j0) {
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 16) {
+              float o[16];
+              tmem_ld16(t_o + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(t_o + c, o);
+            }
           }
         }
-        // The first half's weights are taken with the old maximum while the tile's own is
-        // found, and taken again in the rare case that it has to be raised.
-        uint64_t sum[2];
-        uint32_t pk[32];
-        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
-        auto weights = [&](int half) {
-          const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
-          const uint64_t off2 = pair(off, off);
+        const float off = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), off2 = pair(off, off);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float x[64];
+          tmem_ld32(t_s + 64 * half, x);
+          tmem_ld32(t_s + 64 * half + 32, x + 32);
+          tmem_wait_ld_regs(x, x + 16);
+          tmem_wait_ld_regs(x + 32, x + 48);
+          uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const uint64_t y = fma2(pair(x[64 * half + 2 * i], x[64 * half + 2 * i + 1]), scale2, off2);
+            const uint64_t y = fma2(pair(x[2 * i], x[2 * i + 1]), scale2, off2);
             float a, b;
             unpair(y, &a, &b);
             a = ex2_approx(a);
@@ -776,57 +805,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[i & 1] = add2(sum[i & 1], pair(a, b));
             pk[i] = pack_bf16(a, b);
           }
-        };
-        bool raised = j == w.j0;
-        float mt = -INFINITY;
-        auto find_max = [&] {
-          float mx[2] = {x[0], x[1]};
-#pragma unroll
-          for (int i = 2; i < 126; i += 4) {
-            mx[0] = max3(mx[0], x[i], x[i + 2]);
-            mx[1] = max3(mx[1], x[i + 1], x[i + 3]);
-          }
-          mt = max3(fmaxf(mx[0], mx[1]), x[126], x[127]);
-        };
-        if (raised) {                            // a piece's first tile: O is empty
-          find_max();
-          if (live) m = mt;
+          tmem_st32(t_s + 32 * half, reinterpret_cast<float*>(pk));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 16 * s + 8 * half);
         }
-        while (true) {
-          sum[0] = sum[1] = 0;
-          weights(0);
-          if (raised) break;
-          find_max();
-          // raise the maximum where it grew by more than kRaise (always from -inf); each row by
-          // itself, so that no row's result depends on its neighbours (or on idle rows)
-          const bool raise = live && mt > m && !((mt - m) * p.scale_log2 <= kRaise);
-          if (!__any_sync(0xffffffffu, raise)) break;
-          const float mn = raise ? mt : m;
-          const float f = m == mn ? 1.f : ex2_approx((m - mn) * p.scale_log2);   // 0 from -inf
-          m = mn;
-          l *= f;
-#pragma unroll 1
-          for (int c = 0; c < DV; c += 16) {
-            float o[16];
-            tmem_ld16(t_o + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= f;
-            tmem_st16(t_o + c, o);
-          }
-          raised = true;
-        }
-        tmem_st32(t_s, reinterpret_cast<float*>(pk));
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 16 * s);
-        weights(1);
-        tmem_st32(t_s + 32, reinterpret_cast<float*>(pk));
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 16 * s + 8);
         float s0, s1, s2, s3;
         unpair(sum[0], &s0, &s1);
         unpair(sum[1], &s2, &s3);
