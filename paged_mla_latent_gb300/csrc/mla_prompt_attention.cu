@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  asm volatile("griddepcontrol.launch_dependents;");     // the join may be launched
 
   // The it-th piece for a consumer warp: false at the span's end (or on abort).
   auto next_piece = [&](int it, Piece* w) -> bool {
@@ -910,6 +911,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
   constexpr int kPart = 2 * kRows * (DV + 2);
   __shared__ int sh_n, sh_parts[kMaxParts];
   const int first = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the attention's results
   const Cut& cut = p.cuts[first];
   const int tiles = cut.tiles;
   if (tiles == 0) return;
@@ -1009,8 +1011,17 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prompt_attention_kernel<S><<<sms, kThreads, S::kSmem, stream>>>(tq, tk, tv, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.parts) return e;
-  prompt_join_kernel<DV><<<dim3(sms - 1, 8), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  // launched while this one runs (its blocks wait for the grid's end): the launch is hidden
+  cudaLaunchConfig_t join = {};
+  join.gridDim = dim3(sms - 1, 8);
+  join.blockDim = dim3(256);
+  join.stream = stream;
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  join.attrs = &early;
+  join.numAttrs = 1;
+  return cudaLaunchKernelEx(&join, prompt_join_kernel<DV>, p);
 }
 
 int sms_of_device(int* out) {
