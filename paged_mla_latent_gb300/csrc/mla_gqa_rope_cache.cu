@@ -15,7 +15,12 @@
 // heads: the item's 8 cosines and sines are read once for them and their loads are in flight
 // together.  Arithmetic is the definition's in fp32, every product, sum and quotient rounded
 // on its own, and one rounding to the stored type (a bf16 value is off by at most 2^-8 of
-// itself, an e4m3 code by 2^-4), so the bytes are exact.
+// itself, an e4m3 code by 2^-4), so the bytes are exact.  Blocks go from token to token, the
+// next token's position and slot read a token ahead.
+//
+// Measured (one GB300): 16,384 tokens, 32/8 heads of 128, e4m3 cache and rotated keys kept,
+// 411 MB: 86 us, 4.8 TB/s (0.71 of the copy rate; latency: 96 registers leave 14 warps a SM;
+// one head a thread 99 us, two 87, four 112); 64 tokens, 16/2 heads: 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
