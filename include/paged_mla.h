@@ -366,7 +366,8 @@ int mla_get_gqa_decode_workspace_size(int32_t batch_size, int32_t num_heads, int
  *   lse_out       (B, Hq) FP32 contiguous, or NULL
  *   workspace     mla_get_gqa_decode_workspace_size(...) bytes, 256-byte aligned, zeroed
  *                 before its first use; a call leaves its counters as it found them.  Calls
- *                 that share one must not overlap on the GPU.
+ *                 of any shape may share one that is large enough, if they do not overlap on
+ *                 the GPU; other entry points' calls may not (they leave partials there).
  * The result does not depend on the order in which the pieces of a split request finish.
  * Device-side errors go to the workspace's error word (mla_check_error): a page list that is
  * not monotone or leaves kv_indices makes that request empty, a page id outside the cache

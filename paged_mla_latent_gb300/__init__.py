@@ -491,11 +491,12 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
     """Causal attention of packed whole prompts (see include/paged_mla.h).  error_word: an
     int32 device tensor (>= 1 element).  workspace: a device tensor of
     mla_get_prompt_workspace_size bytes; without one the call takes it from torch's allocator
-    on the call's stream."""
+    on the call's stream (up to 40 MB; nothing where no request can be long enough to be cut
+    between SMs)."""
     d = _cuda_index(q)
     ew = _error_word(error_word, d)
     if workspace is None:
-        n = mla_get_prompt_workspace_size(k.shape[0], v.shape[2])
+        n = mla_get_prompt_workspace_size(k.shape[0], v.shape[-1])
         if n and stream is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
         elif n:

@@ -336,6 +336,29 @@ def test_decode_extreme_queries(pm):
         _check_decode(c, o, lse, f"queries of size {std}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_scales(pm, fp8):
+    """Softmax scales of zero (a plain mean), below zero and large."""
+    for sm in (0.0, -0.2, 2.0):
+        c = _decode_case([1, 400, 3000], 8, 2, 64, 16, fp8)
+        c["sm"] = sm
+        o, lse, _ = _run_decode(pm, c)
+        _check_decode(c, o, lse, f"sm_scale {sm}")
+
+
+def test_decode_shapes_share_a_workspace(pm):
+    shapes = [([5000, 17], 8, 1, 128, 16, False), ([3000] * 3, 40, 1, 128, 64, True),
+              ([7000], 16, 2, 64, 128, False), ([5000, 17], 8, 1, 128, 16, True)]
+    n = max(pm.mla_get_gqa_decode_workspace_size(len(s[0]), s[1], s[2], s[3]) for s in shapes)
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for lens, Hq, Hk, D, ps, fp8 in shapes:
+            c = _decode_case(lens, Hq, Hk, D, ps, fp8)
+            o, lse, _ = _run_decode(pm, c, ws=ws)
+            _check_decode(c, o, lse, f"{Hq}/{Hk} of {D}")
+    assert pm.mla_check_error(ws) == 0
+
+
 def test_decode_infinite_scores(pm):
     """A key of -inf scores drops out; NaN in an attended key or value reaches the row."""
     c = _decode_case([40], 4, 1, 64, 8, False)

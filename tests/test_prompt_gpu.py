@@ -194,16 +194,46 @@ def test_prompt_bad_ranges(pm):
     assert c["err"].item() == 0 and c["o"][80:].isnan().all() and not c["o"][:80].isnan().any()
 
 
-def test_prompt_in_a_graph(pm):
-    c = _case([300, 20], [300, 500], 8, 2, 128, 128)
+@pytest.mark.parametrize("keys", [[300, 500], [9000, 2500]])       # whole; cut and joined
+def test_prompt_in_a_graph(pm, keys):
+    c = _case([300, 20], keys, 8, 2, 128, 128)
     _run(pm, c)
     want = c["o"].clone()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         _run(pm, c)
-    c["o"].fill_(math.nan)
-    graph.replay()
-    assert torch.equal(c["o"], want)
+    for _ in range(3):
+        c["o"].fill_(math.nan)
+        graph.replay()
+        assert torch.equal(c["o"], want)
+
+
+def test_prompt_scales(pm):
+    for sm in (1e-30, 1e-3, 3.0):
+        c = _case([200, 70], [200, 1100], 4, 2, 128, 128)
+        c["sm"] = sm
+        _run(pm, c)
+        _check(c, f"sm_scale {sm}")
+
+
+def test_prompt_back_to_back(pm):
+    """Calls of different shapes on one workspace, one behind the other: a call's first kernel
+    does not run into the join before it."""
+    cases = [_case([40], [30000 + 700 * i], 8, 2, 128, 128, seed=i) for i in range(4)]
+    alone = []
+    for c in cases:
+        _run(pm, c)
+        alone.append(c["o"].clone())
+        torch.cuda.synchronize()
+    ws = torch.empty(pm.mla_get_prompt_workspace_size(40000, 128), dtype=torch.uint8, device=DEV)
+    for _ in range(5):
+        for c in cases:
+            c["o"].fill_(math.nan)
+        for c in cases:
+            pm.mla_prompt_attention(c["q"], c["k"], c["v"], c["o"], c["qo"], c["kv"], c["sm"], c["err"],
+                                    c["lse"], workspace=ws)
+        for c, want in zip(cases, alone):
+            assert torch.equal(c["o"], want)
 
 
 @pytest.mark.parametrize("D,DV", [(64, 64), (128, 128), (192, 128)])
