@@ -224,3 +224,20 @@ def test_prompt_workspace_size(pm):
     for bad in ((-1, 128), (100, 96)):
         with pytest.raises(pm.MlaError):
             f(*bad, 152)
+
+
+def test_packed_descriptors_are_the_structure(pm):
+    """The bytes a call passes are mla_tensor_t's (on CPU tensors: their device index is -1)."""
+    import torch
+    base = torch.zeros(5, 6, 7, 8, dtype=torch.bfloat16)
+    for t in (base, base[:, 1:3], base[0].transpose(0, 1), base[0, 0, ::2], torch.zeros(()),
+              torch.zeros(0, 3, dtype=torch.int32)):
+        assert pm._packed(t, -1) == bytes(pm._desc(t))
+    assert pm._packed(None, 0) is None
+    for bad, error in ((3, TypeError), (base, ValueError), ("x", TypeError)):
+        with pytest.raises(error):
+            pm._packed(bad, 0)
+    with pytest.raises(TypeError):
+        pm._packed(torch.zeros(2, dtype=torch.float64), -1)
+    with pytest.raises(ValueError):
+        pm._packed(torch.zeros(1, 1, 1, 1, 1), -1)
