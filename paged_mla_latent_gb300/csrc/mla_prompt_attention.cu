@@ -384,6 +384,10 @@ __device__ __forceinline__ void transpose2(uint32_t* v, int lane) {
     }
 }
 __device__ __forceinline__ bool half_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+// The word with zeros in place of its non-finite halves.
+__device__ __noinline__ uint32_t finite_halves(uint32_t w) {
+  return (half_nonfinite(w) ? 0u : w & 0xFFFFu) | (half_nonfinite(w >> 16) ? 0u : w & 0xFFFF0000u);
+}
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -679,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int len = w.pos0 + w.toks;       // the request's keys
         for (int j = first_edge(w); j < w.j1 && ok; ++j, ++edges) {
           const int iv = (base + j - w.j0) * (KC + VC) + KC;
+          const bool tail = (j + 1) * kKeys > len;
           bool bad = false;
           ok = mbar_wait(edge0 + 8 * (edges % kEdges), (edges / kEdges) & 1, abort_flag, p.err);
           for (int c = 0; c < VC && ok; ++c) {
@@ -686,26 +691,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the swizzle moves 16-byte words inside a 128-byte row only)
 #pragma unroll 4
             for (int e = threadIdx.x - 320; e < 128 * 8; e += 64) {
-              if (j * kKeys + (e >> 3) >= len) {
+              if (tail && j * kKeys + (e >> 3) >= len) {
                 chunk[e] = make_uint4(0, 0, 0, 0);
                 continue;
               }
-              const uint4 x = chunk[e];
-              uint32_t y[4] = {x.x, x.y, x.z, x.w};
-              bool any = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (half_nonfinite(y[k])) {
-                  y[k] &= 0xFFFF0000u;
-                  any = true;
-                }
-                if (half_nonfinite(y[k] >> 16)) {
-                  y[k] &= 0xFFFFu;
-                  any = true;
-                }
-              }
-              if (any) {
-                chunk[e] = make_uint4(y[0], y[1], y[2], y[3]);
+              uint4 x = chunk[e];
+              // a half whose exponent is all ones carries into its top bit
+              const uint32_t m = 0x7F807F80u, one = 0x00800080u;
+              const uint32_t top = ((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one);
+              if (__builtin_expect(top & 0x80008000u, 0)) {
+                x.x = finite_halves(x.x);
+                x.y = finite_halves(x.y);
+                x.z = finite_halves(x.z);
+                x.w = finite_halves(x.w);
+                chunk[e] = x;
                 bad = true;
               }
             }
@@ -751,8 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(t_s + 64 * half + 32, x + 32);
           tmem_wait_ld_regs(x, x + 16);
           tmem_wait_ld_regs(x + 32, x + 48);
-          if (j >= e0) {
-            const int last = lim - j * kKeys - 64 * half;
+          const int last = lim - j * kKeys - 64 * half;
+          if (j >= e0 && !__all_sync(0xffffffffu, last >= 63)) {
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
               const int n = last - c + 1;          // columns of this group that the row sees
