@@ -76,10 +76,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;              // log2 growth of the maximum that forces a rescale
 
-// Fixed cost of a unit on the line (its Q, the first tile's way, its result: about 10,000 cycles
-// at 20 a position; 256 to 640 measure alike) in positions, and the fewest K/V tiles a part of a cut unit may have: writing and joining a part moves
-// 266 KB, about four tiles' time of an SM.
-constexpr int kUnitCost = 512;
+// Fixed cost of a unit on the line (its Q, the first tile's way, its result: 7,400 cycles against
+// 2,700 a tile, fitted over the CTAs of packed prompts) in positions; with 512 the packed prompts
+// take 278 us instead of 266.  The fewest K/V tiles a part of a cut unit may have: writing and
+// joining a part moves 266 KB, about four tiles' time of an SM.
+constexpr int kUnitCost = 352;
 constexpr int kMinCut = 8;                 // a power of two
 constexpr int kMaxParts = 512;             // parts of one unit: at most one a span
 
@@ -369,11 +370,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-// Two lanes hold two 16-byte words each, v[4 w + k], twice.  Afterwards v[4 i + k] is word
-// lane & 1 of lane ^ i.  A thread has a row of O: stored as it lies, an instruction would write
-// 16 bytes into each of 32 rows; so it writes whole 32-byte sectors of 16.
-__device__ __forceinline__ void transpose2(uint32_t* v, int lane) {
-  const bool b = lane & 1;
+// Four lanes hold four 16-byte words each, v[4 w + k].  Afterwards v[4 i + k] is word lane & 3
+// of lane ^ i.  A thread has a row of O: stored as it lies, an instruction would write 16 bytes
+// into each of 32 rows; so it writes 64 bytes into each of eight.
+__device__ __forceinline__ void transpose4(uint32_t* v, int lane) {
+  const bool b = lane & 1, c = lane & 2;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -381,6 +382,14 @@ __device__ __forceinline__ void transpose2(uint32_t* v, int lane) {
       const uint32_t x = v[8 * k + i], y = v[8 * k + 4 + i];
       v[8 * k + i] = b ? y : x;
       v[8 * k + 4 + i] = __shfl_xor_sync(0xffffffffu, b ? x : y, 1);
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = v[4 * r + i], y = v[8 + 4 * r + i];
+      v[4 * r + i] = c ? y : x;
+      v[8 + 4 * r + i] = __shfl_xor_sync(0xffffffffu, c ? x : y, 2);
     }
 }
 __device__ __forceinline__ bool half_nonfinite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
@@ -844,9 +853,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_none = __any_sync(0xffffffffu, none);
       const int h = w.hk * p.G + hg;
       const int64_t row = static_cast<int64_t>(w.row0) + tok;
-      // this lane's words go to its row and its neighbour's
+      // this lane's words go to the rows of its group of four lanes
       const int64_t mine = live ? row * p.o_tok + h * p.o_head : -1;
-      const int64_t dst[2] = {mine, __shfl_xor_sync(0xffffffffu, mine, 1)};
+      const int64_t dst[4] = {mine, __shfl_xor_sync(0xffffffffu, mine, 1), __shfl_xor_sync(0xffffffffu, mine, 2),
+                              __shfl_xor_sync(0xffffffffu, mine, 3)};
       float* stats = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats) + s * kRows + r;
       float* part = whole ? nullptr : p.parts + w.part * static_cast<int64_t>(S::kPartFloats) + 4 * kRows + (s * kRows + r) * DV;
       const float m2 = m == -INFINITY ? m : m * p.scale_log2;
@@ -879,11 +889,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (whole) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
-          transpose2(y, lane);
+          transpose4(y, lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (dst[i & 1] >= 0)
-              *reinterpret_cast<uint4*>(p.o + dst[i & 1] + c + 16 * (i >> 1) + 8 * (lane & 1)) =
+            if (dst[i] >= 0)
+              *reinterpret_cast<uint4*>(p.o + dst[i] + c + 8 * (lane & 3)) =
                   make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         } else if (live) {
 #pragma unroll
