@@ -161,15 +161,15 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 
 // Positions of request b, 0 where its page list makes no sense.
 __device__ __forceinline__ int request_len(const GqaDecodeParams& p, int b, bool flag) {
-  const int64_t s = p.kv_indptr[b], e = p.kv_indptr[b + 1];
+  const int64_t s = __ldg(p.kv_indptr + b), e = __ldg(p.kv_indptr + b + 1);
+  const int last_len = p.last ? __ldg(p.last + b) : 1 << p.log2_page;
   if (s < 0 || e < s || e > p.n_idx) {
     if (flag) atomicOr(p.err, kErrBadIndptr);
     return 0;
   }
   if (e == s) return 0;
   const int ps = 1 << p.log2_page;
-  int last = p.last ? p.last[b] : ps;
-  last = last < 1 ? 1 : (last > ps ? ps : last);
+  const int last = last_len < 1 ? 1 : (last_len > ps ? ps : last_len);
   const int64_t len = ((e - s - 1) << p.log2_page) + last;
   if (len > 0x7FFFFF00) {
     if (flag) atomicOr(p.err, kErrBadIndptr);
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
   __syncthreads();
   int64_t mine = 0, inc = 0;
   int len0 = 0;
+#pragma unroll 4
   for (int b = tid; b < p.B; b += kThreads) {
     const int len = request_len(p, b, cta == 0);
     if (b < kThreads) len0 = len;

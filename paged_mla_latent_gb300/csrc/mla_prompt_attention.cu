@@ -161,7 +161,8 @@ struct Request {
 };
 __device__ __forceinline__ Request load_request(const PromptParams& p, int b, int cta_tok, bool flag) {
   Request r = {0, 0, 0, 0, 0};
-  const int64_t s = p.qo_indptr[b], e = p.qo_indptr[b + 1], ks = p.kv_indptr[b], ke = p.kv_indptr[b + 1];
+  const int64_t s = __ldg(p.qo_indptr + b), e = __ldg(p.qo_indptr + b + 1);
+  const int64_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
   if (s < 0 || e < s || e > p.n_tok) {     // the request is left out
     if (flag) atomicOr(p.err, kErrBadIndptr);
     return r;
@@ -202,6 +203,7 @@ __device__ __forceinline__ Span find_span(const PromptParams& p, int cta_tok, in
   Span sp;
   Request mine = {0, 0, 0, 0, 0};
   int64_t total = 0;
+#pragma unroll 4
   for (int b = lane; b < p.B; b += 32) {
     const Request r = load_request(p, b, cta_tok, blockIdx.x == 0);
     if (b < 32) mine = r;
