@@ -41,12 +41,12 @@
 // O is idle).  Weights stay below 2^8, sums in fp32.  P is rounded to bf16 (2^-8 of each
 // weight at most); l is summed from the unrounded weights.
 //
-// Measured (one GB300): 16,384 tokens, 32/8 heads of 128: 1.40 ms sustained, 1570 TFLOP/s (0.82
-// of cuBLAS's burst bf16 rate), 1.29 ms alone with the tensor pipe 74 % busy; 4,089 queries
-// behind 63,911 positions, 12 heads of 192/128: 1.29 ms, 1600 TFLOP/s; 24 packed prompts of 17 to
-// 4,089: 288 us, 995 TFLOP/s.  What bounds it: a tile's loop is its softmax (about 1500 cycles)
-// and then its PV and QK (1024), of which two tiles' overlap; in short units the ends (Q behind
-// the last S, the last PV, the result: about 8000 cycles).
+// Measured (one GB300): 16,384 tokens, 32/8 heads of 128: 1.38 ms call after call, 1590 TFLOP/s
+// (0.83 of cuBLAS's burst bf16 rate, 0.92 of its sustained one), 1.28 ms alone with the tensor
+// pipe 75 % busy; 4,089 queries behind 63,911 positions, 12 heads of 192/128: 1.28 ms, 1610
+// TFLOP/s; 24 packed prompts of 17 to 4,089: 275 us, 1040 TFLOP/s.  What bounds it: a tile's loop
+// is its softmax (about 1500 cycles) and then its PV and QK (1024), of which two tiles' overlap;
+// in short units the ends (Q behind the last S, the last PV, the result: 7400 cycles).
 //
 // Every wait is bounded (2 s): one that runs out sets the error word and ends the CTA.
 #include <cuda.h>
