@@ -720,12 +720,17 @@ int ctas_for(int* out) {
   return MLA_OK;
 }
 
-int head_tiles(int64_t G) { return G <= 8 ? 1 : (G <= 16 ? 2 : 4); }
+// n-tiles of 8 query heads a unit takes: the whole group up to 32 heads, so that the cache is
+// read once.  With 128-wide e4m3 rows at most 16: 32 heads' outputs and queries do not fit the
+// registers next to the conversions (64 requests of 8,192 positions, 32 heads a KV head: 159 us
+// in one unit, 114 in two; bf16 rows: 122 and 173).
+int head_tiles(int64_t G, bool narrow) { return G <= 8 ? 1 : (G <= 16 || narrow ? 2 : 4); }
+bool narrow_units(int64_t D, bool fp8) { return D == 128 && fp8; }
 
 size_t workspace_for(int ctas, int64_t G, int64_t D) {
   const size_t counters = (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256;
   return kHeaderBytes + counters +
-         2 * static_cast<size_t>(ctas) * 8 * head_tiles(G) * static_cast<size_t>(D + 2) * 4;
+         2 * static_cast<size_t>(ctas) * 8 * head_tiles(G, false) * static_cast<size_t>(D + 2) * 4;
 }
 
 template <int D, bool kFp8, int NT>
@@ -750,11 +755,12 @@ cudaError_t launch(const GqaDecodeParams& p, int ctas, cudaStream_t stream) {
 
 template <int D, bool kFp8>
 cudaError_t launch_nt(const GqaDecodeParams& p, int ctas, cudaStream_t s) {
-  switch (head_tiles(p.G)) {
-    case 1: return launch<D, kFp8, 1>(p, ctas, s);
-    case 2: return launch<D, kFp8, 2>(p, ctas, s);
-    default: return launch<D, kFp8, 4>(p, ctas, s);
-  }
+  constexpr bool kNarrow = D == 128 && kFp8;
+  const int nt = head_tiles(p.G, kNarrow);
+  if (nt == 1) return launch<D, kFp8, 1>(p, ctas, s);
+  if constexpr (!kNarrow)
+    if (nt == 4) return launch<D, kFp8, 4>(p, ctas, s);
+  return launch<D, kFp8, 2>(p, ctas, s);
 }
 
 }  // namespace
@@ -840,7 +846,8 @@ extern "C" int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache
   p.Hq = static_cast<int>(Hq);
   p.Hk = static_cast<int>(Hk);
   p.G = static_cast<int>(G);
-  p.chunks = static_cast<int>((G + 8 * head_tiles(G) - 1) / (8 * head_tiles(G)));
+  const int heads = 8 * head_tiles(G, narrow_units(D, c.fp8));
+  p.chunks = static_cast<int>((G + heads - 1) / heads);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.err = reinterpret_cast<int*>(ws);
   p.counters = reinterpret_cast<int*>(ws + kHeaderBytes);
