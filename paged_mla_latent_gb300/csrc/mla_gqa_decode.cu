@@ -9,11 +9,11 @@
 // Measured (one GB300, pages of 128 or 16): 64 requests of 2,048 to 65,536 positions, two KV
 // heads, bf16, 1.51 GB: 225 us, 6.72 TB/s (0.99 of the copy rate); one of 142,000 positions,
 // eight KV heads, e4m3, 291 MB: 60 us, of which 40 stream the cache, the rest are the plan, the
-// first tiles and the join of 38 pieces a unit; 37 ragged requests, 10.6 MB: 13.5 us; one of 137
+// first tiles and the join of 38 pieces a unit; 37 ragged requests, 10.6 MB: 12.2 us; one of 137
 // positions: 5.3 us.
 //
 // Work split.  A unit is (request, KV head, chunk of 8 NT query heads); its positions are cut
-// into tiles of 16.  All units' tiles form one line and every CTA takes an equal span of it,
+// into tiles of 16 or 32.  All units' tiles form one line and every CTA takes an equal span of it,
 // so ragged lengths, few long requests and many short ones all fill the GPU.  A unit that
 // crosses a span's end leaves partials (m, l, o in fp32) in workspace slots; the CTA that
 // arrives last at the unit's counter joins them in the order of the spans, so the result does
@@ -47,7 +47,6 @@ using namespace pmla;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;            // positions a warp takes at a time
 constexpr int kHeaderBytes = 256;    // error word
 constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -115,6 +114,11 @@ struct DecodeShape {
   static constexpr int D = D_, NT = NT_;
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kRow = D * (kFp8 ? 1 : 2);          // bytes of a K or V row
+  // positions a warp takes at a time, in groups of 16 (the MMA's M): rows of 128 bytes or less
+  // two groups, so that the softmax's shuffles and the loop are paid half as often (64 requests
+  // of 8,192 positions, e4m3, 64-wide rows: 42 us with one, 36 with two; 128-wide: 56 and 54)
+  static constexpr int MT = kRow <= 128 && NT <= 2 ? 2 : 1;
+  static constexpr int kTile = 16 * MT;
   static constexpr int kTileBytes = 2 * kTile * kRow;      // K then V
   static constexpr int kHeads = 8 * NT;
   // about 24 KB in flight a warp (eight warps a SM: 192 KB)
@@ -133,7 +137,7 @@ struct DecodeShape {
 // Weight of one unit of a request on the line of work.
 template <class S>
 __device__ __forceinline__ int64_t line_weight(int len) {
-  return len > 0 ? (len + kTile - 1) / kTile + S::kUnitCost : 0;
+  return len > 0 ? (len + S::kTile - 1) / S::kTile + S::kUnitCost : 0;
 }
 
 // Where a span's border, x tiles into a unit of n, cuts it: pieces shorter than their fixed
@@ -186,7 +190,7 @@ __device__ __forceinline__ void store_o(const GqaDecodeParams& p, int b, int h, 
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const GqaDecodeParams p) {
-  constexpr int D = S::D, NT = S::NT, kRow = S::kRow, kHeads = S::kHeads;
+  constexpr int D = S::D, NT = S::NT, MT = S::MT, kRow = S::kRow, kTile = S::kTile, kHeads = S::kHeads;
   constexpr bool kFp8 = S::kFp8;
   extern __shared__ __align__(128) uint8_t smem[];
   float* s_m = reinterpret_cast<float*>(smem + S::kBuf);       // [warp][head]
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
     const uint8_t* kh = p.k + hk * p.head_pitch;
     const uint8_t* vh = p.v + hk * p.head_pitch;
     const int ps_mask = (1 << p.log2_page) - 1;
-    const bool one_page = p.log2_page >= 4;    // a tile never crosses a page
+    const bool one_page = (1 << p.log2_page) >= kTile;    // a tile never crosses a page
     auto page_of = [&](int t) -> int {       // lane's page id for tile t (-1: no position)
       const int j = t * kTile + (one_page ? 0 : lane & (kTile - 1));
       return t < t1 && j < len ? __ldg(p.kv_indices + idx0 + (j >> p.log2_page)) : -1;
@@ -454,44 +458,51 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
       }
       const uint32_t kt = ring + stage * S::kTileBytes, vt = kt + kTile * kRow;
 
-      float sT[NT][4];
+      float sT[NT][MT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sT[nt][0] = sT[nt][1] = sT[nt][2] = sT[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) sT[nt][u][0] = sT[nt][u][1] = sT[nt][u][2] = sT[nt][u][3] = 0.f;
       if constexpr (!kFp8) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t a[4];
-          ldsm4(kt + chunk_at<kRow>(lane & 15, 2 * kk + (lane >> 4)), a);
+        for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<false>(sT[nt], a, qf[nt][kk][0], qf[nt][kk][1]);
-        }
+          for (int u = 0; u < MT; ++u) {
+            uint32_t a[4];
+            ldsm4(kt + chunk_at<kRow>(16 * u + (lane & 15), 2 * kk + (lane >> 4)), a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(sT[nt][u], a, qf[nt][kk][0], qf[nt][kk][1]);
+          }
       } else {
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) {
-          uint32_t r[4];                   // rows g / g+8, bytes 4cq..4cq+3 of two 16-column steps
-          ldsm4(kt + chunk_at<kRow>(lane & 15, 2 * kk + (lane >> 4)), r);
+        for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * i]), e4m3x2_to_f16x2(r[2 * i + 1]),
-                                   e4m3x2_to_f16x2(r[2 * i] >> 16), e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
+          for (int u = 0; u < MT; ++u) {
+            uint32_t r[4];                 // rows g / g+8, bytes 4cq..4cq+3 of two 16-column steps
+            ldsm4(kt + chunk_at<kRow>(16 * u + (lane & 15), 2 * kk + (lane >> 4)), r);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816<true>(sT[nt], a, qf[nt][2 * kk + i][0], qf[nt][2 * kk + i][1]);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * i]), e4m3x2_to_f16x2(r[2 * i + 1]),
+                                     e4m3x2_to_f16x2(r[2 * i] >> 16), e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(sT[nt][u], a, qf[nt][2 * kk + i][0], qf[nt][2 * kk + i][1]);
+            }
           }
-        }
       }
-      // ---- softmax over the tile's 16 positions (rows g, g + 8), per head (columns)
+      // ---- softmax over the tile's positions (rows g, g + 8 of each group), per head (columns)
       const int j0 = t * kTile + g;
-      uint32_t pf[NT][2];
+      uint32_t pf[NT][MT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float mt[2];
+        float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          sT[nt][i] = j0 < len ? sT[nt][i] * sc[nt][i] : -INFINITY;
-          sT[nt][2 + i] = j0 + 8 < len ? sT[nt][2 + i] * sc[nt][i] : -INFINITY;
-          mt[i] = fmaxf(sT[nt][i], sT[nt][2 + i]);
-        }
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sT[nt][u][i] = j0 + 16 * u + 8 * (i >> 1) < len ? sT[nt][u][i] * sc[nt][i & 1] : -INFINITY;
+            mt[i & 1] = fmaxf(mt[i & 1], sT[nt][u][i]);
+          }
 #pragma unroll
         for (int x16 = 4; x16 < 32; x16 <<= 1) {
           mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], x16));
@@ -517,42 +528,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
           }
         }
         // weights; with e4m3 they carry 2^14, in l too
-        float w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float mm = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
-          w[i] = ex2_approx(sT[nt][i] - mm + (kFp8 ? 14.f : 0.f));
-          l[nt][i & 1] += w[i];
+        for (int u = 0; u < MT; ++u) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mm = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
+            w[i] = ex2_approx(sT[nt][u][i] - mm + (kFp8 ? 14.f : 0.f));
+            l[nt][i & 1] += w[i];
+          }
+          pf[nt][u][0] = transpose8x8(kFp8 ? f32x2_to_f16x2(w[1], w[0]) : pack_bf16(w[0], w[1]));
+          pf[nt][u][1] = transpose8x8(kFp8 ? f32x2_to_f16x2(w[3], w[2]) : pack_bf16(w[2], w[3]));
         }
-        pf[nt][0] = transpose8x8(kFp8 ? f32x2_to_f16x2(w[1], w[0]) : pack_bf16(w[0], w[1]));
-        pf[nt][1] = transpose8x8(kFp8 ? f32x2_to_f16x2(w[3], w[2]) : pack_bf16(w[2], w[3]));
       }
       // ---- O^T += V^T . P^T
       const int vr = (lane & 7) + ((lane >> 4) << 3);      // position row of the transposed load
       const int vc = (lane >> 3) & 1;
       if constexpr (!kFp8) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t a[4];                   // columns 16 i + g / + 8, positions 2cq.. / + 8
-          ldsm4_t(vt + chunk_at<kRow>(vr, 2 * i + vc), a);
+        for (int u = 0; u < MT; ++u)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[nt][i], a, pf[nt][0], pf[nt][1]);
-        }
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];                 // columns 16 i + g / + 8, positions 2cq.. / + 8
+            ldsm4_t(vt + chunk_at<kRow>(16 * u + vr, 2 * i + vc), a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[nt][i], a, pf[nt][u][0], pf[nt][u][1]);
+          }
       } else {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          // each register: column pair (2g, 2g+1) of a 16-column group at positions 2cq, 2cq+1
-          uint32_t r[4];
-          ldsm4_t(vt + chunk_at<kRow>(vr, 2 * i + vc), r);
+        for (int u = 0; u < MT; ++u)
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const uint32_t lo = __byte_perm(r[k2], 0, 0x3120), hi = __byte_perm(r[k2 + 2], 0, 0x3120);
-            const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
-                                   e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
+          for (int i = 0; i < D / 32; ++i) {
+            // each register: column pair (2g, 2g+1) of a 16-column group at positions 2cq, 2cq+1
+            uint32_t r[4];
+            ldsm4_t(vt + chunk_at<kRow>(16 * u + vr, 2 * i + vc), r);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<true>(acc[nt][2 * i + k2], a, pf[nt][0], pf[nt][1]);
+            for (int k2 = 0; k2 < 2; ++k2) {
+              const uint32_t lo = __byte_perm(r[k2], 0, 0x3120), hi = __byte_perm(r[k2 + 2], 0, 0x3120);
+              const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
+                                     e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<true>(acc[nt][2 * i + k2], a, pf[nt][u][0], pf[nt][u][1]);
+            }
           }
-        }
       }
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
@@ -723,7 +741,7 @@ int ctas_for(int* out) {
 // n-tiles of 8 query heads a unit takes: the whole group up to 32 heads, so that the cache is
 // read once.  With 128-wide e4m3 rows at most 16: 32 heads' outputs and queries do not fit the
 // registers next to the conversions (64 requests of 8,192 positions, 32 heads a KV head: 159 us
-// in one unit, 114 in two; bf16 rows: 122 and 173).
+// in one unit, 99 in two; bf16 rows: 122 and 173).
 int head_tiles(int64_t G, bool narrow) { return G <= 8 ? 1 : (G <= 16 || narrow ? 2 : 4); }
 bool narrow_units(int64_t D, bool fp8) { return D == 128 && fp8; }
 
