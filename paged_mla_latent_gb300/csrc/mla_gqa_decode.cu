@@ -49,6 +49,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeaderBytes = 256;    // error word
 constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 320;        // spans of a line: 160 SMs; a unit has at most one piece a span
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -125,8 +126,11 @@ struct DecodeShape {
   static constexpr int kStages = 24576 / kTileBytes < 8 ? 24576 / kTileBytes : 8;
   static constexpr int kWarpBytes = kStages * kTileBytes;
   static constexpr int kJoinBytes = kWarps * kHeads * D * 4;   // per-warp outputs, over the rings
-  static constexpr int kBuf = kWarps * kWarpBytes > kJoinBytes ? kWarps * kWarpBytes : kJoinBytes;
+  static constexpr int kPieceBytes = 2 * kMaxCtas * kHeads * 4;   // m and l of a unit's pieces, over them too
+  static constexpr int kOverBytes = kJoinBytes > kPieceBytes ? kJoinBytes : kPieceBytes;
+  static constexpr int kBuf = kWarps * kWarpBytes > kOverBytes ? kWarps * kWarpBytes : kOverBytes;
   static constexpr int kSmem = kBuf + 2 * kWarps * kHeads * 4;
+  static_assert(kCtasPerSm * (kSmem + 1024 + 64) <= 233472, "shared memory of a SM");
   static constexpr int kSlotFloats = kHeads * (D + 2);
   static constexpr int kAhead = NT < 4 ? 10 : 2;           // half of a join's loads in flight a thread
   // what a unit costs besides its tiles (page ids, the first tile's way from DRAM, the joins:
@@ -734,7 +738,7 @@ int ctas_for(int* out) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
-  *out = sms * kCtasPerSm;
+  *out = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
   return MLA_OK;
 }
 

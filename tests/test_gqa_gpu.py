@@ -306,6 +306,22 @@ def test_decode_many_requests(pm, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,Hq,Hk,D", [
+    (33001, 32, 1, 64),        # one unit over every span: as many pieces as there are CTAs
+    (65001, 32, 1, 64),
+    (33001, 8, 1, 64),
+    (33001, 32, 1, 128),
+])
+def test_decode_one_unit_over_all_spans(pm, n, Hq, Hk, D, fp8):
+    c = _decode_case([n], Hq, Hk, D, 64, fp8)
+    o, lse, ws = _run_decode(pm, c)
+    assert pm.mla_check_error(ws) == 0
+    _check_decode(c, o, lse, f"{Hq}/{Hk} heads of {D}")
+    o2, lse2, _ = _run_decode(pm, c, ws=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_one_strong_key(pm, fp8):
     """One key takes nearly all of the weight, first, last or amid many; the rest is what
     the running maximum has to drop."""
