@@ -8,8 +8,8 @@
 // Bound by the cache's bytes: 2 D elements a position and KV head, each used by G heads.
 // Measured (one GB300, pages of 128 or 16): 64 requests of 2,048 to 65,536 positions, two KV
 // heads, bf16, 1.51 GB: 225 us, 6.72 TB/s (0.99 of the copy rate); one of 142,000 positions,
-// eight KV heads, e4m3, 291 MB: 60 us, of which 40 stream the cache, the rest are the plan, the
-// first tiles and the join of 38 pieces a unit; 37 ragged requests, 10.6 MB: 12.2 us; one of 137
+// eight KV heads, e4m3, 291 MB: 58 us, of which 40 stream the cache, the rest are the plan, the
+// first tiles and the join of 19 pieces a unit; 37 ragged requests, 10.6 MB: 11.5 us; one of 137
 // positions: 5.3 us.
 //
 // Work split.  A unit is (request, KV head, chunk of 8 NT query heads); its positions are cut
@@ -19,7 +19,7 @@
 // arrives last at the unit's counter joins them in the order of the spans, so the result does
 // not depend on the order of arrival.
 //
-// Inside a CTA four warps take tiles in turn, each with its own ring of cp.async stages, its
+// Inside a CTA four or eight warps take tiles in turn, each with its own ring of cp.async stages, its
 // own running maximum, sum and output, and no barrier until the span's piece ends.
 //   S^T (16 positions x 8 heads) = K (16 x D) . q^T by mma.sync m16n8k16 with K as the A
 //   operand, so that 8 heads fill the MMA's N exactly (a step has at most a few heads a KV
@@ -45,11 +45,9 @@ namespace {
 
 using namespace pmla;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kHeaderBytes = 256;    // error word
-constexpr int kCtasPerSm = 2;
-constexpr int kMaxCtas = 320;        // spans of a line: 160 SMs; a unit has at most one piece a span
+constexpr int kSmWarps = 8;          // warps a SM, in two CTAs or in one
+constexpr int kMaxSms = 160;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -109,10 +107,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// D columns, cache type, n-tiles of 8 query heads; kStages tiles in flight a warp.
-template <int D_, bool kFp8_, int NT_>
+// D columns, cache type, n-tiles of 8 query heads, warps a CTA; kStages tiles in flight a warp.
+template <int D_, bool kFp8_, int NT_, int W_>
 struct DecodeShape {
   static constexpr int D = D_, NT = NT_;
+  static constexpr int kWarps = W_, kThreads = 32 * W_;
+  static constexpr int kCtasPerSm = kSmWarps / W_;
+  static constexpr int kMaxCtas = kMaxSms * kCtasPerSm;    // a unit has at most one piece a CTA
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kRow = D * (kFp8 ? 1 : 2);          // bytes of a K or V row
   // positions a warp takes at a time, in groups of 16 (the MMA's M): rows of 128 bytes or less
@@ -132,9 +133,11 @@ struct DecodeShape {
   static constexpr int kSmem = kBuf + 2 * kWarps * kHeads * 4;
   static_assert(kCtasPerSm * (kSmem + 1024 + 64) <= 233472, "shared memory of a SM");
   static constexpr int kSlotFloats = kHeads * (D + 2);
-  static constexpr int kAhead = NT < 4 ? 10 : 2;           // half of a join's loads in flight a thread
+  static constexpr bool kTwo = kHeads * D > 4 * kThreads;  // a join's thread has two words of o
+  static constexpr int kAhead = NT == 4 ? 2 : (kTwo ? 10 : 20);   // pieces whose words are in flight
   // what a unit costs besides its tiles (page ids, the first tile's way from DRAM, the joins:
-  // about 2.5 us), in tiles at a CTA's share of the bandwidth (22 bytes a ns)
+  // about 2.5 us), in tiles at the bandwidth of four warps (22 bytes a ns); CTAs of eight take
+  // the same (one of 142,000 positions: 59 us; with 0.7 of it 63, with 1.5 times it 61)
   static constexpr int kUnitCost = 55000 / kTileBytes;
 };
 
@@ -193,8 +196,9 @@ __device__ __forceinline__ void store_o(const GqaDecodeParams& p, int b, int h, 
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const GqaDecodeParams p) {
+__global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_decode_kernel(const GqaDecodeParams p) {
   constexpr int D = S::D, NT = S::NT, MT = S::MT, kRow = S::kRow, kTile = S::kTile, kHeads = S::kHeads;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr bool kFp8 = S::kFp8;
   extern __shared__ __align__(128) uint8_t smem[];
   float* s_m = reinterpret_cast<float*>(smem + S::kBuf);       // [warp][head]
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-    // ---- the piece's four partial results meet in shared memory (over the idle rings)
+    // ---- the warps' partial results meet in shared memory (over the idle rings)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -696,11 +700,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
         __syncthreads();
         constexpr int kEach = 4 * kThreads;  // columns the threads take at once
         for (int e0 = 4 * tid; e0 < nh * D; e0 += 2 * kEach) {
-          const bool two = e0 + kEach < nh * D;
+          const bool two = S::kTwo && e0 + kEach < nh * D;
           const int h = e0 / D, h2 = (e0 + kEach) / D;
           float oo[8] = {};
-          for (int i0 = 0; i0 < np; i0 += S::kAhead) {       // 2 kAhead loads in flight a thread
-            float4 x[2 * S::kAhead];
+          for (int i0 = 0; i0 < np; i0 += S::kAhead) {       // all their loads in flight at once
+            float4 x[2 * S::kAhead];       // (the odd ones unused without a second word)
 #pragma unroll
             for (int i = 0; i < S::kAhead; ++i)
               if (i0 + i < np) {
@@ -733,12 +737,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const 
   }
 }
 
-int ctas_for(int* out) {
+// SMs that calls use: all of a GB300's 152.
+int sms_for(int* out) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
-  *out = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
+  *out = sms < kMaxSms ? sms : kMaxSms;
   return MLA_OK;
 }
 
@@ -749,15 +754,16 @@ int ctas_for(int* out) {
 int head_tiles(int64_t G, bool narrow) { return G <= 8 ? 1 : (G <= 16 || narrow ? 2 : 4); }
 bool narrow_units(int64_t D, bool fp8) { return D == 128 && fp8; }
 
-size_t workspace_for(int ctas, int64_t G, int64_t D) {
-  const size_t counters = (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256;
-  return kHeaderBytes + counters +
-         2 * static_cast<size_t>(ctas) * 8 * head_tiles(G, false) * static_cast<size_t>(D + 2) * 4;
+// Counters and slots for two CTAs a SM, which all calls of a shape fit.
+size_t counters_for(int sms) { return (static_cast<size_t>(sms) * 2 * 4 + 255) / 256 * 256; }
+size_t workspace_for(int sms, int64_t G, int64_t D) {
+  return kHeaderBytes + counters_for(sms) +
+         2 * 2 * static_cast<size_t>(sms) * 8 * head_tiles(G, false) * static_cast<size_t>(D + 2) * 4;
 }
 
-template <int D, bool kFp8, int NT>
-cudaError_t launch(const GqaDecodeParams& p, int ctas, cudaStream_t stream) {
-  using S = DecodeShape<D, kFp8, NT>;
+template <int D, bool kFp8, int NT, int W>
+cudaError_t launch_as(const GqaDecodeParams& p, int sms, cudaStream_t stream) {
+  using S = DecodeShape<D, kFp8, NT, W>;
   static std::mutex mu;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -771,18 +777,29 @@ cudaError_t launch(const GqaDecodeParams& p, int ctas, cudaStream_t stream) {
       attr_set[dev] = true;
     }
   }
-  gqa_decode_kernel<S><<<ctas, kThreads, S::kSmem, stream>>>(p);
+  gqa_decode_kernel<S><<<sms * S::kCtasPerSm, S::kThreads, S::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
+// Where the units are no more than the SMs, one CTA of eight warps a SM: half the pieces to
+// join, and a unit that one CTA has to itself gets a whole SM.  Otherwise two of four, one of
+// which streams while the other ends a piece.  With eight and with four, us: e4m3, eight heads a
+// KV head of 128, pages of 16: 2 units of 8,000 positions 12 and 19, 152 of 2,000 18 and 23, 304
+// of 500 16 and 12; bf16, 8,192 units of 16 positions 156 and 90.
+template <int D, bool kFp8, int NT>
+cudaError_t launch(const GqaDecodeParams& p, int sms, cudaStream_t stream) {
+  if (static_cast<int64_t>(p.B) * p.Hk * p.chunks <= sms) return launch_as<D, kFp8, NT, 8>(p, sms, stream);
+  return launch_as<D, kFp8, NT, 4>(p, sms, stream);
+}
+
 template <int D, bool kFp8>
-cudaError_t launch_nt(const GqaDecodeParams& p, int ctas, cudaStream_t s) {
+cudaError_t launch_nt(const GqaDecodeParams& p, int sms, cudaStream_t s) {
   constexpr bool kNarrow = D == 128 && kFp8;
   const int nt = head_tiles(p.G, kNarrow);
-  if (nt == 1) return launch<D, kFp8, 1>(p, ctas, s);
+  if (nt == 1) return launch<D, kFp8, 1>(p, sms, s);
   if constexpr (!kNarrow)
-    if (nt == 4) return launch<D, kFp8, 4>(p, ctas, s);
-  return launch<D, kFp8, 2>(p, ctas, s);
+    if (nt == 4) return launch<D, kFp8, 4>(p, sms, s);
+  return launch<D, kFp8, 2>(p, sms, s);
 }
 
 }  // namespace
@@ -794,12 +811,12 @@ extern "C" int mla_get_gqa_decode_workspace_size(int32_t batch_size, int32_t num
       num_heads % num_kv_heads != 0 || head_dim < 1 || num_sms > 65536)
     return MLA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return MLA_ERR_UNSUPPORTED;
-  int ctas = num_sms * kCtasPerSm;
+  int sms = num_sms;
   if (num_sms <= 0) {
-    const int st = ctas_for(&ctas);
+    const int st = sms_for(&sms);
     if (st != MLA_OK) return st;
   }
-  *bytes_out = workspace_for(ctas, num_heads / num_kv_heads, head_dim);
+  *bytes_out = workspace_for(sms, num_heads / num_kv_heads, head_dim);
   return MLA_OK;
 }
 
@@ -835,10 +852,10 @@ extern "C" int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache
   if (!workspace || !gqa_aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
   const int64_t G = Hq / Hk;
   if (workspace_bytes < workspace_for(1, G, D)) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  int ctas = 0;
-  const int cs = ctas_for(&ctas);
+  int sms = 0;
+  const int cs = sms_for(&sms);
   if (cs != MLA_OK) return cs;
-  if (workspace_bytes < workspace_for(ctas, G, D)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < workspace_for(sms, G, D)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (B == 0) return MLA_OK;
 
   GqaDecodeParams p;
@@ -873,10 +890,10 @@ extern "C" int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.err = reinterpret_cast<int*>(ws);
   p.counters = reinterpret_cast<int*>(ws + kHeaderBytes);
-  p.slots = reinterpret_cast<float*>(ws + kHeaderBytes + (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256);
+  p.slots = reinterpret_cast<float*>(ws + kHeaderBytes + counters_for(sms));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e;
-  if (D == 64) e = c.fp8 ? launch_nt<64, true>(p, ctas, s) : launch_nt<64, false>(p, ctas, s);
-  else e = c.fp8 ? launch_nt<128, true>(p, ctas, s) : launch_nt<128, false>(p, ctas, s);
+  if (D == 64) e = c.fp8 ? launch_nt<64, true>(p, sms, s) : launch_nt<64, false>(p, sms, s);
+  else e = c.fp8 ? launch_nt<128, true>(p, sms, s) : launch_nt<128, false>(p, sms, s);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -322,6 +322,21 @@ def test_decode_one_unit_over_all_spans(pm, n, Hq, Hk, D, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 1, 128), (5, 1, 64), (16, 1, 128), (12, 1, 64), (32, 1, 128), (32, 1, 64)])
+@pytest.mark.parametrize("lens", [
+    [40001] + [i % 5 for i in range(199)],         # one unit over nearly all spans
+    [(i * 131) % 1200 for i in range(170)],
+])
+def test_decode_more_units_than_sms(pm, lens, Hq, Hk, D, fp8):
+    c = _decode_case(lens, Hq, Hk, D, 32, fp8)
+    o, lse, ws = _run_decode(pm, c)
+    assert pm.mla_check_error(ws) == 0
+    _check_decode(c, o, lse, f"{Hq}/{Hk} heads of {D}")
+    o2, lse2, _ = _run_decode(pm, c, ws=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_one_strong_key(pm, fp8):
     """One key takes nearly all of the weight, first, last or amid many; the rest is what
     the running maximum has to drop."""
