@@ -7,8 +7,8 @@
 //
 // Bound by the cache's bytes: 2 D elements a position and KV head, each used by G heads.
 // Measured (one GB300, pages of 128 or 16): 64 requests of 2,048 to 65,536 positions, two KV
-// heads, bf16, 1.51 GB: 225 us, 6.72 TB/s (0.99 of the copy rate); one of 142,000 positions,
-// eight KV heads, e4m3, 291 MB: 58 us, of which 40 stream the cache, the rest are the plan, the
+// heads, bf16, 1.51 GB: 223 us, 6.77 TB/s (the copy rate); one of 142,000 positions,
+// eight KV heads, e4m3, 291 MB: 56 us, of which 40 stream the cache, the rest are the plan, the
 // first tiles and the join of 19 pieces a unit; 37 ragged requests, 10.6 MB: 11.5 us; one of 137
 // positions: 5.3 us.
 //
