@@ -16,11 +16,11 @@
 // together.  Arithmetic is the definition's in fp32, every product, sum and quotient rounded
 // on its own, and one rounding to the stored type (a bf16 value is off by at most 2^-8 of
 // itself, an e4m3 code by 2^-4), so the bytes are exact.  Blocks go from token to token, the
-// next token's position and slot read a token ahead.
+// next token's position and slot read a token ahead, its words sent for from DRAM.
 //
 // Measured (one GB300): 16,384 tokens, 32/8 heads of 128, e4m3 cache and rotated keys kept,
-// 411 MB: 86 us, 4.8 TB/s (0.71 of the copy rate; latency: 96 registers leave 14 warps a SM;
-// one head a thread 99 us, two 87, four 112); 64 tokens, 16/2 heads: 1.9 us.
+// 411 MB: 74 us, 5.5 TB/s (0.81 of the copy rate; latency: 96 registers leave 18 warps a SM;
+// one head a thread 117 us, two 74, four 80); 64 tokens, 16/2 heads: 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -33,7 +33,6 @@ namespace {
 
 using namespace pmla;
 
-constexpr int kThreads = 256;
 constexpr int kStripHeads = 2;
 constexpr int kResident = 2048;     // threads a SM
 
@@ -130,8 +129,12 @@ __device__ __forceinline__ uint4 round8(const float* x) {
   return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
 }
 
+// Threads of a block, of which three fit a SM at least: 80 registers a thread, but 96 for e4m3
+// strips (16,384 tokens, pairs (i, i + R/2): 72 us with 96, 77 with 80, 87 with the 106 that the
+// compiler would take, which leave four warps a quarter of the SM instead of five).
+constexpr int block_threads(bool fp8, int strip) { return fp8 && strip > 1 ? 192 : 256; }
 template <int D, bool kFp8, bool kNeox, int kStrip>
-__global__ void __launch_bounds__(kThreads) gqa_rope_append_kernel(const RopeAppendParams p) {
+__global__ void __launch_bounds__(block_threads(kFp8, kStrip), 3) gqa_rope_append_kernel(const RopeAppendParams p) {
   constexpr int kPieces = D / 16;
   // strips of heads a token: q, then k, then v; a thread keeps its item from token to token
   const int q_strips = (p.Hq + kStrip - 1) / kStrip, k_strips = (p.Hk + kStrip - 1) / kStrip;
@@ -188,6 +191,17 @@ __global__ void __launch_bounds__(kThreads) gqa_rope_append_kernel(const RopeApp
     if (t_next < p.n_tok) {
       if (rot) pos_next = __ldg(p.positions + t_next);
       if (!is_q) slot_next = __ldg(p.slot_mapping + t_next);
+    }
+    // the next token's words into L2 meanwhile: they cost no registers there (16,384 tokens,
+    // e4m3: 76 us with, 87 without; two tokens ahead 78, ahead of this token's loads 98)
+    if (t_next < p.n_tok) {
+      const uint16_t* next = src0 + t_next * tok;
+#pragma unroll
+      for (int i = 0; i < kStrip; ++i)
+        if (h0 + i < heads) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i * head));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i * head + half));
+        }
     }
     const bool bad_slot = slot >= p.n_slots;
     if (bad_slot && is_k && h0 == 0 && piece == 0) atomicOr(p.err, kErrBadRowId);
@@ -265,7 +279,8 @@ int launch(const RopeAppendParams& p, int sms, cudaStream_t s) {
   const bool strips = rows * (D / 16) >= static_cast<int64_t>(sms) * 2048 * 4;
   const int n = strips ? kStripHeads : 1;
   const int items = ((p.Hq + n - 1) / n + 2 * ((p.Hk + n - 1) / n)) * (D / 16);
-  const int threads = items < kThreads ? (items + 31) / 32 * 32 : kThreads;
+  const int most = block_threads(kFp8, n);
+  const int threads = items < most ? (items + 31) / 32 * 32 : most;
   const unsigned parts = (items + threads - 1) / threads;
   // as many blocks as stay resident, each going from token to token
   int64_t blocks = static_cast<int64_t>(sms) * kResident / (threads * parts);
