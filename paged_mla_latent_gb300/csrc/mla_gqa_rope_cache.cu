@@ -19,8 +19,8 @@
 // next token's position and slot read a token ahead, its words sent for from DRAM.
 //
 // Measured (one GB300): 16,384 tokens, 32/8 heads of 128, e4m3 cache and rotated keys kept,
-// 411 MB: 74 us, 5.5 TB/s (0.81 of the copy rate; latency: 96 registers leave 18 warps a SM;
-// one head a thread 117 us, two 74, four 80); 64 tokens, 16/2 heads: 1.9 us.
+// 411 MB: 70 us, 5.9 TB/s (0.86 of the copy rate; latency: 96 registers leave 18 warps a SM;
+// four heads a thread 80); 64 tokens, 16/2 heads: 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,7 +34,6 @@ namespace {
 using namespace pmla;
 
 constexpr int kStripHeads = 2;
-constexpr int kResident = 2048;     // threads a SM
 
 struct RopeAppendParams {
   const uint16_t *q, *k, *v;        // bf16 bits
@@ -282,8 +281,12 @@ int launch(const RopeAppendParams& p, int sms, cudaStream_t s) {
   const int most = block_threads(kFp8, n);
   const int threads = items < most ? (items + 31) / 32 * 32 : most;
   const unsigned parts = (items + threads - 1) / threads;
-  // as many blocks as stay resident, each going from token to token
-  int64_t blocks = static_cast<int64_t>(sms) * kResident / (threads * parts);
+  // whole waves of the blocks that are resident at a time, each going from token to token: one in
+  // small calls (4,089 tokens, 25/5 heads of 64, e4m3: 11 us, two 12, broken waves 14); three of
+  // strips, whose ends come at different times (16,384 tokens, 64/8 heads, e4m3: 121 us, two 126,
+  // one 145; bf16 117, two 117, one 130)
+  const int resident = (kFp8 && strips ? 20 : 24) / (threads / 32);      // warps a SM by registers
+  int64_t blocks = static_cast<int64_t>(sms) * resident * (strips ? 3 : 1) / parts;
   if (blocks > p.n_tok || blocks < 1) blocks = blocks < 1 ? 1 : p.n_tok;
   const dim3 grid(static_cast<unsigned>(blocks), parts);
   if (strips) gqa_rope_append_kernel<D, kFp8, kNeox, kStripHeads><<<grid, threads, 0, s>>>(p);
