@@ -407,6 +407,19 @@ def _cuda_index(t):
     return t.get_device()
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()        # (torch.cuda's own asks for its set-up each time)
+
+
+def _call(device, fn, *args):
+    """A library call with CUDA device `device` (an index) as the current one: the library
+    launches there and asks it for its SMs."""
+    if _current_device() == device:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _raw_stream(stream, device):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
@@ -429,7 +442,8 @@ def mla_gqa_rope_and_cache(q, k, v, positions, cos_sin, is_neox, slot_mapping, q
     device tensor (>= 1 element)."""
     d = _cuda_index(q)
     ew = _error_word(error_word, d)
-    rc = _lib.mla_gqa_rope_and_cache(
+    rc = _call(
+        d, _lib.mla_gqa_rope_and_cache,
         _packed(q, d), _packed(k, d), _packed(v, d), _packed(positions, d), _packed(cos_sin, d),
         int(is_neox), _packed(slot_mapping, d), _packed(k_scale, d), _packed(v_scale, d),
         _packed(q_out, d), _packed(k_out, d), _packed(k_cache, d), _packed(v_cache, d), ew,
@@ -466,7 +480,8 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
                                                   q.shape[2], q.device)
     elif workspace.get_device() != d:
         raise ValueError(f"the workspace must be on CUDA device {d}")
-    rc = _lib.mla_gqa_decode(
+    rc = _call(
+        d, _lib.mla_gqa_decode,
         _packed(q, d), _packed(k_cache, d), _packed(v_cache, d), _packed(o, d),
         _packed(kv_indptr, d), _packed(kv_indices, d), _packed(kv_last_page_lens, d),
         float(sm_scale), _packed(k_scale, d), _packed(v_scale, d), _packed(lse_out, d),
@@ -500,7 +515,7 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
     d = _cuda_index(q)
     ew = _error_word(error_word, d)
     if workspace is None:
-        n = mla_get_prompt_workspace_size(k.shape[0], v.shape[-1])
+        n = _call(d, mla_get_prompt_workspace_size, k.shape[0], v.shape[-1])
         if n and stream is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
         elif n:
@@ -510,7 +525,8 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
         raise ValueError(f"the workspace must be on CUDA device {d}")
     ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
-    rc = _lib.mla_prompt_attention(
+    rc = _call(
+        d, _lib.mla_prompt_attention,
         _packed(q, d), _packed(k, d), _packed(v, d), _packed(o, d), _packed(qo_indptr, d),
         _packed(kv_indptr, d), float(sm_scale), _packed(lse_out, d), ew, ws, n,
         _raw_stream(stream, d))
