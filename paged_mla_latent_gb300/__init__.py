@@ -153,6 +153,19 @@ def _stream(stream, device):
     return ctypes.c_void_p(int(stream))
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()        # (torch.cuda's own asks for its set-up each time)
+
+
+def _call(device, fn, *args):
+    """A library call with CUDA device `device` (an index) as the current one: the library
+    launches there and asks it for its SMs."""
+    if device < 0 or _current_device() == device:      # (CPU tensors: the library refuses them)
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _check(rc: int, where: str):
     if rc != 0:
         raise MlaError(rc, where)
@@ -204,10 +217,12 @@ def mla_decode(q, kv_buffer, o, qo_indptr, kv_indptr, kv_indices, kv_last_page_l
     descs = [_desc(t) for t in (q, kv_buffer, o, qo_indptr, kv_indptr, kv_indices,
                                 kv_last_page_lens, q_scale, kv_scale, lse_out)]
     dq, dkv, do, dqo, dkvp, didx, dlast, dqs, dks, dlse = descs
-    rc = _lib.mla_decode(_ref(dq), _ref(dkv), _ref(do), _ref(dqo), _ref(dkvp), _ref(didx),
-                         _ref(dlast), int(max_seqlen_q), float(sm_scale), _ref(dqs), _ref(dks),
-                         int(num_kv_splits), _ref(dlse), ctypes.c_void_p(workspace.data_ptr()),
-                         workspace.numel() * workspace.element_size(), _stream(stream, q.device))
+    rc = _call(
+        q.get_device(), _lib.mla_decode,
+        _ref(dq), _ref(dkv), _ref(do), _ref(dqo), _ref(dkvp), _ref(didx), _ref(dlast),
+        int(max_seqlen_q), float(sm_scale), _ref(dqs), _ref(dks), int(num_kv_splits), _ref(dlse),
+        ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(),
+        _stream(stream, q.device))
     _check(rc, "mla_decode")
     return workspace
 
@@ -223,7 +238,8 @@ def mla_decode_shared_prefix(q, kv_buffer, o, qo_indptr, kv_indptr, kv_indices,
     descs = [_desc(t) for t in (q, kv_buffer, o, qo_indptr, kv_indptr, kv_indices,
                                 kv_last_page_lens, q_scale, kv_scale, lse_out)]
     dq, dkv, do, dqo, dkvp, didx, dlast, dqs, dks, dlse = descs
-    rc = _lib.mla_decode_shared_prefix(
+    rc = _call(
+        q.get_device(), _lib.mla_decode_shared_prefix,
         _ref(dq), _ref(dkv), _ref(do), _ref(dqo), _ref(dkvp), _ref(didx), _ref(dlast),
         int(max_seqlen_q), float(sm_scale), _ref(dqs), _ref(dks), int(shared_prefix_len),
         _ref(dlse), ctypes.c_void_p(workspace.data_ptr()),
@@ -270,7 +286,7 @@ class PreparedDecode:
             self._fn, self._where = _lib.mla_decode, "mla_decode"
             self._args = (r[0], r[1], r[2], r[3], r[4], r[5], r[6], int(max_seqlen_q),
                           float(sm_scale), r[7], r[8], int(num_kv_splits), r[9]) + tail
-        self._device = q.device
+        self._device, self._index = q.device, q.get_device()
         self._stream = None if stream is None else _stream(stream, q.device)
         self._expand = None
         if compact_page_table is not None:
@@ -286,10 +302,10 @@ class PreparedDecode:
         st = _stream(stream, self._device) if stream is not None else (
             self._stream if self._stream is not None else _stream(None, self._device))
         if self._expand is not None:
-            rc = _lib.mla_expand_shared_prefix_indices(*self._expand, st)
+            rc = _call(self._index, _lib.mla_expand_shared_prefix_indices, *self._expand, st)
             if rc != 0:
                 raise MlaError(rc, "mla_expand_shared_prefix_indices")
-        rc = self._fn(*self._args, st)
+        rc = _call(self._index, self._fn, *self._args, st)
         if rc != 0:
             raise MlaError(rc, self._where)
         return self.workspace
@@ -315,10 +331,11 @@ def mla_decode_noalloc(q, kv_buffer, o, qo_indptr, kv_indptr, kv_indices, kv_las
             raise ValueError("error_out must be an int32 tensor of at least one element on "
                              f"{q.device}")
     ew = ctypes.c_void_p(error_out.data_ptr()) if error_out is not None else None
-    rc = _lib.mla_decode_noalloc(_ref(dq), _ref(dkv), _ref(do), _ref(dqo), _ref(dkvp), _ref(didx),
-                                 _ref(dlast), int(max_seqlen_q), float(sm_scale), _ref(dqs),
-                                 _ref(dks), int(num_kv_splits), _ref(dlse), ew,
-                                 _stream(stream, q.device))
+    rc = _call(
+        q.get_device(), _lib.mla_decode_noalloc,
+        _ref(dq), _ref(dkv), _ref(do), _ref(dqo), _ref(dkvp), _ref(didx), _ref(dlast),
+        int(max_seqlen_q), float(sm_scale), _ref(dqs), _ref(dks), int(num_kv_splits), _ref(dlse),
+        ew, _stream(stream, q.device))
     _check(rc, "mla_decode_noalloc")
 
 
@@ -332,8 +349,8 @@ def mla_expand_shared_prefix_indices(shared_indices, own_indptr, own_indices, kv
                                    error_word.device != kv_indices.device):
         raise ValueError("error_word must be an int32 tensor on the page table's device")
     ew = ctypes.c_void_p(error_word.data_ptr()) if error_word is not None else None
-    rc = _lib.mla_expand_shared_prefix_indices(*[_ref(d) for d in descs], ew,
-                                               _stream(stream, kv_indices.device))
+    rc = _call(kv_indices.get_device(), _lib.mla_expand_shared_prefix_indices,
+               *[_ref(d) for d in descs], ew, _stream(stream, kv_indices.device))
     _check(rc, "mla_expand_shared_prefix_indices")
 
 
@@ -342,7 +359,8 @@ def mla_merge_partials(o_parts, lse_parts, reduce_indptr, reduce_idx, o, lse_out
     """Softmax-weighted merge of partials with a CSR reduce map (see include/paged_mla.h)."""
     descs = [_desc(t) for t in (o_parts, lse_parts, reduce_indptr, reduce_idx, o, lse_out)]
     ew = ctypes.c_void_p(error_word.data_ptr()) if error_word is not None else None
-    rc = _lib.mla_merge_partials(*[_ref(d) for d in descs], ew, _stream(stream, o.device))
+    rc = _call(o.get_device(), _lib.mla_merge_partials, *[_ref(d) for d in descs], ew,
+               _stream(stream, o.device))
     _check(rc, "mla_merge_partials")
 
 
@@ -350,7 +368,8 @@ def mla_latent_to_v(o, w_uv, v, stream=None):
     """v[t, h, :] = o[t, h, :] @ w_uv[h]: the latent o mapped to v_head_dim (see
     include/paged_mla.h)."""
     descs = [_desc(t) for t in (o, w_uv, v)]
-    rc = _lib.mla_latent_to_v(*[_ref(d) for d in descs], _stream(stream, v.device))
+    rc = _call(v.get_device(), _lib.mla_latent_to_v, *[_ref(d) for d in descs],
+               _stream(stream, v.device))
     _check(rc, "mla_latent_to_v")
 
 
@@ -365,10 +384,9 @@ def mla_qk_rope_concat_and_cache(q_nope, q_pe, kv_c, k_pe, positions, cos_sin, i
         raise ValueError(f"error_word must be an int32 tensor on {q_out.device}")
     descs = [_desc(t) for t in (q_nope, q_pe, kv_c, k_pe, positions, cos_sin)]
     tail = [_desc(t) for t in (slot_mapping, q_scale, kv_scale, q_out, kv_buffer)]
-    rc = _lib.mla_qk_rope_concat_and_cache(*[_ref(d) for d in descs], int(is_neox),
-                                           *[_ref(d) for d in tail],
-                                           ctypes.c_void_p(error_word.data_ptr()),
-                                           _stream(stream, q_out.device))
+    rc = _call(q_out.get_device(), _lib.mla_qk_rope_concat_and_cache,
+               *[_ref(d) for d in descs], int(is_neox), *[_ref(d) for d in tail],
+               ctypes.c_void_p(error_word.data_ptr()), _stream(stream, q_out.device))
     _check(rc, "mla_qk_rope_concat_and_cache")
 
 
@@ -405,19 +423,6 @@ def _cuda_index(t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
     return t.get_device()
-
-
-def _current_device():
-    return torch._C._cuda_getDevice()        # (torch.cuda's own asks for its set-up each time)
-
-
-def _call(device, fn, *args):
-    """A library call with CUDA device `device` (an index) as the current one: the library
-    launches there and asks it for its SMs."""
-    if _current_device() == device:
-        return fn(*args)
-    with torch.cuda.device(device):
-        return fn(*args)
 
 
 def _raw_stream(stream, device):
@@ -540,9 +545,9 @@ def mla_selftest_bounded_wait(error_word, result, limit_ns, stream=None):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.numel() < n or \
                 not t.is_cuda:
             raise ValueError(f"expected an int32 CUDA tensor of at least {n} element(s)")
-    rc = _lib.mla_selftest_bounded_wait(ctypes.c_void_p(error_word.data_ptr()),
-                                        ctypes.c_void_p(result.data_ptr()), int(limit_ns),
-                                        _stream(stream, result.device))
+    rc = _call(result.get_device(), _lib.mla_selftest_bounded_wait,
+               ctypes.c_void_p(error_word.data_ptr()), ctypes.c_void_p(result.data_ptr()),
+               int(limit_ns), _stream(stream, result.device))
     _check(rc, "mla_selftest_bounded_wait")
 
 
@@ -550,11 +555,13 @@ def mla_validate(q, kv_buffer, qo_indptr, kv_indptr, kv_indices, kv_last_page_le
                  workspace, stream=None) -> int:
     """Device-side check of the index inputs; returns the status code (synchronises)."""
     descs = [_desc(t) for t in (q, kv_buffer, qo_indptr, kv_indptr, kv_indices, kv_last_page_lens)]
-    return int(_lib.mla_validate(*[_ref(d) for d in descs], ctypes.c_void_p(workspace.data_ptr()),
-                                 workspace.numel(), _stream(stream, q.device)))
+    return int(_call(q.get_device(), _lib.mla_validate, *[_ref(d) for d in descs],
+                     ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                     _stream(stream, q.device)))
 
 
 def mla_check_error(workspace, stream=None) -> int:
     """First device-side error recorded in the workspace since the last check (clears it)."""
-    return int(_lib.mla_check_error(ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                    _stream(stream, workspace.device)))
+    return int(_call(workspace.get_device(), _lib.mla_check_error,
+                     ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                     _stream(stream, workspace.device)))

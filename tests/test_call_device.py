@@ -106,3 +106,32 @@ def test_prompt_makes_its_workspace_for_the_tensors_device(world, monkeypatch):
     pm.mla_prompt_attention(q, k, k, q, _i32(2), _i32(2), 0.1, _i32(1))
     _check(lib, "mla_get_prompt_workspace_size", "mla_prompt_attention")
     assert made == [(256, torch.device("cuda", 1))]
+
+
+def test_latent_decode(world):
+    """The latent entry points, the prepared call and the checks of a workspace."""
+    pm, lib, _ = world
+    q, kv = OnDevice.make(2, 4, 576), OnDevice.make(8, 576)
+    ws, f = OnDevice.make(256, dtype=torch.uint8), OnDevice.make(1, dtype=torch.float32)
+    args = (q, kv, q, _i32(3), _i32(3), _i32(8), _i32(2), 1, 0.1, f, f)
+    pm.mla_decode(*args, workspace=ws, stream=7)
+    pm.mla_decode_shared_prefix(*args, 2, workspace=ws, stream=7)
+    pm.mla_decode_noalloc(*args, stream=7)
+    pm.PreparedDecode(*args, workspace=ws, stream=7).run()
+    pm.PreparedDecode(*args, workspace=ws, stream=7, compact_page_table=(_i32(1), _i32(3), _i32(2))).run()
+    pm.mla_validate(*args[:2], *args[3:7], ws, stream=7)
+    pm.mla_check_error(ws, stream=7)
+    _check(lib, "mla_decode", "mla_decode_shared_prefix", "mla_decode_noalloc", "mla_decode",
+           "mla_expand_shared_prefix_indices", "mla_decode", "mla_validate", "mla_check_error")
+
+
+def test_latent_steps_around_the_decode(world):
+    pm, lib, _ = world
+    x, i = OnDevice.make(2, 4, 64), _i32(2)
+    pm.mla_qk_rope_concat_and_cache(x, x, x, x, i, x, 0, i, x, x, x, x, _i32(1), stream=7)
+    pm.mla_latent_to_v(x, x, x, stream=7)
+    pm.mla_merge_partials(x, x, i, i, x, stream=7)
+    pm.mla_expand_shared_prefix_indices(i, i, i, i, i, stream=7)
+    pm.mla_selftest_bounded_wait(_i32(1), _i32(3), 1000, stream=7)
+    _check(lib, "mla_qk_rope_concat_and_cache", "mla_latent_to_v", "mla_merge_partials",
+           "mla_expand_shared_prefix_indices", "mla_selftest_bounded_wait")
