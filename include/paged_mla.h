@@ -323,7 +323,8 @@ int mla_qk_rope_concat_and_cache(const mla_tensor_t* q_nope, const mla_tensor_t*
  *   cos_sin       (max_pos, R) FP32, R <= D a multiple of 16, last dim contiguous, row
  *                 stride a multiple of 4, 16-byte aligned
  *   k_scale, v_scale  0-dim (or 1-element) FP32 with E4M3FN caches; NULL with BF16
- *   q_out, k_out  as q and k (written); may be q and k themselves (same pointer and strides).
+ *   q_out, k_out  as q and k, no two rows overlapping (written); may be q and k themselves
+ *                 (same pointer and strides).
  *                 k_out may be NULL (a decode step needs no copy of the new keys).
  *   k_cache, v_cache  (N_pages, PS, Hk, D) BF16 or E4M3FN, both of one type and one set of
  *                 strides, PS a power of two <= 1024, last dim contiguous, the other strides
@@ -361,7 +362,8 @@ int mla_get_gqa_decode_workspace_size(int32_t batch_size, int32_t num_heads, int
  *   q             (B, Hq, D) BF16, D 64 or 128, as above
  *   k_cache, v_cache, k_scale, v_scale  as above; bytes past a request's positions (a last
  *                 page's tail, other pages) are never read
- *   o             (B, Hq, D) BF16 or FP32, last dim contiguous (written)
+ *   o             (B, Hq, D) BF16 or FP32, last dim contiguous, no two rows overlapping
+ *                 (written)
  *   kv_indptr, kv_indices, kv_last_page_lens  the page table as mla_decode takes it
  *   lse_out       (B, Hq) FP32 contiguous, or NULL
  *   workspace     mla_get_gqa_decode_workspace_size(...) bytes, 256-byte aligned, zeroed
@@ -393,8 +395,8 @@ int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla
  *   q         (n_tok, Hq, D) BF16, k (n_keys, Hk, D) BF16, v (n_keys, Hk, Dv) BF16 with
  *             (D, Dv) = (64, 64), (128, 128) or (192, 128), Hq / Hk <= 128; each: last dim
  *             contiguous, 16-byte aligned, other strides positive multiples of 8 elements
- *   o         (n_tok, Hq, Dv) BF16, strides non-negative multiples of 8, 16-byte aligned
- *             (written); rows of no request are not
+ *   o         (n_tok, Hq, Dv) BF16, strides multiples of 8, no two rows overlapping, 16-byte
+ *             aligned (written); rows of no request are not
  *   qo_indptr, kv_indptr  (B+1,) INT32
  *   sm_scale  positive and finite
  *   lse_out   (n_tok, Hq) FP32 contiguous, or NULL

@@ -21,6 +21,21 @@ inline bool gqa_check_bf16(const mla_tensor_t* t, int64_t n, int64_t heads, int6
   return t->stride[2] == 1 && gqa_aligned(t->ptr, 2 * static_cast<uintptr_t>(unit));
 }
 
+// No two rows of a (n, heads, width) output share an element: the inner of its two outer dims
+// steps at least a row, the other at least the inner one's extent.  (Rows in one place would be
+// written by several threads at once, the last of which differs from call to call.)
+inline bool gqa_rows_apart(const mla_tensor_t* t) {
+  const bool heads_inner = t->stride[1] <= t->stride[0];
+  int64_t extent = t->shape[2];
+  for (int i = 0; i < 2; ++i) {
+    const int dim = (i == 0) == heads_inner ? 1 : 0;
+    if (t->shape[dim] <= 1) continue;        // never stepped
+    if (t->stride[dim] < extent) return false;
+    extent += (t->shape[dim] - 1) * t->stride[dim];
+  }
+  return true;
+}
+
 inline bool gqa_check_i32(const mla_tensor_t* t, int64_t n) {
   return t && (t->ptr || n == 0) && t->dtype == MLA_DTYPE_INT32 && t->ndim == 1 &&
          t->shape[0] == n && (n <= 1 || t->stride[0] == 1) && gqa_aligned(t->ptr, 4);

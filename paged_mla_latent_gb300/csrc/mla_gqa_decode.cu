@@ -836,7 +836,8 @@ extern "C" int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache
   if (st != MLA_OK) return st;
   if (!o || (!o->ptr && B > 0) || o->ndim != 3 || (o->dtype != MLA_DTYPE_BF16 && o->dtype != MLA_DTYPE_FP32) ||
       o->shape[0] != B || o->shape[1] != Hq || o->shape[2] != D || o->stride[2] != 1 ||
-      o->stride[0] < 0 || o->stride[1] < 0 || !gqa_aligned(o->ptr, o->dtype == MLA_DTYPE_FP32 ? 4 : 2))
+      o->stride[0] < 0 || o->stride[1] < 0 || !gqa_rows_apart(o) ||
+      !gqa_aligned(o->ptr, o->dtype == MLA_DTYPE_FP32 ? 4 : 2))
     return MLA_ERR_INVALID_ARG;
   if (!gqa_check_i32(kv_indptr, B + 1)) return MLA_ERR_INVALID_ARG;
   if (!kv_indices || kv_indices->ndim != 1 || !gqa_check_i32(kv_indices, kv_indices->shape[0]))

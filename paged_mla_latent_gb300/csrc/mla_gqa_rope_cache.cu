@@ -315,6 +315,7 @@ extern "C" int mla_gqa_rope_and_cache(
       !gqa_check_bf16(v, T, Hk, D, 8) || !gqa_check_bf16(q_out, T, Hq, D, 8) ||
       (k_out && !gqa_check_bf16(k_out, T, Hk, D, 8)))
     return MLA_ERR_INVALID_ARG;
+  if (!gqa_rows_apart(q_out) || (k_out && !gqa_rows_apart(k_out))) return MLA_ERR_INVALID_ARG;
   if (!gqa_check_i32(positions, T) || !gqa_check_i32(slot_mapping, T)) return MLA_ERR_INVALID_ARG;
   if (is_neox != 0 && is_neox != 1) return MLA_ERR_INVALID_ARG;
   if (!cos_sin || !cos_sin->ptr || cos_sin->dtype != MLA_DTYPE_FP32 || cos_sin->ndim != 2 ||

@@ -1093,7 +1093,8 @@ extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k
   if (n_tok < 0 || n_keys < 0 || n_tok >= 0x7FFFFF00 || n_keys >= 0x7FFFFF00) return MLA_ERR_INVALID_ARG;
   if (Hq < 1 || Hk < 1 || Hq > 1024 || Hq % Hk != 0) return MLA_ERR_INVALID_ARG;
   if (!gqa_check_bf16(q, n_tok, Hq, D, 8) || !gqa_check_bf16(k, n_keys, Hk, D, 8) ||
-      !gqa_check_bf16(v, n_keys, Hk, DV, 8) || !gqa_check_bf16(o, n_tok, Hq, DV, 8))
+      !gqa_check_bf16(v, n_keys, Hk, DV, 8) || !gqa_check_bf16(o, n_tok, Hq, DV, 8) ||
+      !gqa_rows_apart(o))
     return MLA_ERR_INVALID_ARG;
   if (!steppable(q) || !steppable(k) || !steppable(v)) return MLA_ERR_INVALID_ARG;
   if (!qo_indptr || qo_indptr->ndim != 1 || qo_indptr->shape[0] < 1) return MLA_ERR_INVALID_ARG;
