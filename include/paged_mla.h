@@ -390,8 +390,10 @@ int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla
  *   J = { j : 0 <= j <= L_b - T_b + t },  s_j = sm_scale * sum_d q[r, h, d] * k[i_j, h/G, d]
  *   lse = ln sum_{j in J} exp(s_j),  o[r, h] = sum_{j in J} exp(s_j - lse) * v[i_j, h/G]
  * with r = qo_indptr[b] + t, i_j = kv_indptr[b] + j.  An empty J gives o = 0, lse = -inf.
- * Values outside J (later positions, other requests, anything past the last row) do not
- * reach a row, infinities and NaN among them.
+ * So does a row all of whose scores are -inf.  Values outside J (later positions, other
+ * requests, anything past the last row) do not reach a row, infinities and NaN among them;
+ * inside J an infinite value has its weight's part, NaN where that weight is zero (a score of
+ * -inf, or too small for fp32).
  *   q         (n_tok, Hq, D) BF16, k (n_keys, Hk, D) BF16, v (n_keys, Hk, Dv) BF16 with
  *             (D, Dv) = (64, 64), (128, 128) or (192, 128), Hq / Hk <= 128; each: last dim
  *             contiguous, 16-byte aligned, other strides positive multiples of 8 elements

@@ -33,7 +33,7 @@
 //   warps 10-11    : for the tiles on the causal edge and at a request's end, zeroes the V rows
 //                    past the request (another request's, or stale memory) and takes
 //                    non-finite values out of V (0 * inf would reach rows that do not see
-//                    them); rows that do see one get it back at the end.
+//                    them); rows that do see one get it back at the end, times its weight.
 // Tensor memory: S_0 S_1 O_0 O_1, 128 columns each (all 512); P_s lies over S_s.
 //
 // The running maximum is only raised when it would grow by more than 8 (in log2): then the
@@ -107,8 +107,8 @@ struct PromptParams {
   uint16_t* o;
   int64_t o_tok, o_head;
   float* lse;
-  const uint16_t* v;                       // for the rows that see a non-finite value
-  int64_t v_tok, v_head;
+  const uint16_t *q, *k, *v;               // for the rows that see a non-finite value
+  int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
   float* parts;                            // two a CTA; null: units are not cut
   Cut* cuts;                               // one a CTA
   int* err;
@@ -398,6 +398,18 @@ __device__ __forceinline__ bool half_nonfinite(uint32_t h) { return (h & 0x7F80u
 // The word with zeros in place of its non-finite halves.
 __device__ __noinline__ uint32_t finite_halves(uint32_t w) {
   return (half_nonfinite(w) ? 0u : w & 0xFFFFu) | (half_nonfinite(w >> 16) ? 0u : w & 0xFFFF0000u);
+}
+
+// The weight 2^(scale2 q . k + off) of one key in a row of n columns.
+__device__ __forceinline__ float key_weight(const uint16_t* q, const uint16_t* k, int n, float scale2, float off) {
+  float dot = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < n; i += 2) {
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(q + i), b = *reinterpret_cast<const uint32_t*>(k + i);
+    dot = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), dot);
+    dot = fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), dot);
+  }
+  return ex2_approx(fmaf(dot, scale2, off));
 }
 
 template <class S>
@@ -875,18 +887,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
         for (int i = 0; i < 16; ++i) unpair(mul2(pair(o[2 * i], o[2 * i + 1]), inv2), &o[2 * i], &o[2 * i + 1]);
-        if (any_none) {                          // (0 * inf among weightless values)
+        if (__builtin_expect(fix && live, 0))
+          for (int j = e0 * kKeys; j <= lim && j < w.j1 * kKeys; ++j) {
+            const int64_t key = static_cast<int64_t>(w.kv0) + j;
+            const uint32_t* vr = reinterpret_cast<const uint32_t*>(p.v + key * p.v_tok + w.hk * p.v_head + c);
+            bool bad = false;
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) bad |= half_nonfinite(vr[i]) || half_nonfinite(vr[i] >> 16);
+            if (!bad) continue;
+            // a weight of zero makes inf NaN, as where PV has the value itself
+            const float weight = key_weight(p.q + row * p.q_tok + h * p.q_head, p.k + key * p.k_tok + w.hk * p.k_head,
+                                            S::D, p.scale_log2, m == -INFINITY ? 0.f : -m2);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t x = vr[i];
+              if (half_nonfinite(x)) o[2 * i] += weight * __uint_as_float(x << 16);
+              if (half_nonfinite(x >> 16)) o[2 * i + 1] += weight * __uint_as_float(x & 0xFFFF0000u);
+            }
+          }
+        __syncwarp();
+        if (any_none) {                          // a row without any weight is zero
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i];
         }
-        if (__builtin_expect(fix && live, 0))
-          for (int j = e0 * kKeys; j <= lim && j < w.j1 * kKeys; ++j) {
-            const uint16_t* vr = p.v + static_cast<int64_t>(w.kv0 + j) * p.v_tok + w.hk * p.v_head + c;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (half_nonfinite(vr[i])) o[i] += __uint_as_float(static_cast<uint32_t>(vr[i]) << 16);
-          }
-        __syncwarp();
         uint32_t y[16];
         if (whole) {
 #pragma unroll
@@ -1132,6 +1155,12 @@ extern "C" int mla_prompt_attention(const mla_tensor_t* q, const mla_tensor_t* k
   p.o_tok = o->stride[0];
   p.o_head = o->stride[1];
   p.lse = lse_out ? static_cast<float*>(lse_out->ptr) : nullptr;
+  p.q = static_cast<const uint16_t*>(q->ptr);
+  p.q_tok = q->stride[0];
+  p.q_head = q->stride[1];
+  p.k = static_cast<const uint16_t*>(k->ptr);
+  p.k_tok = k->stride[0];
+  p.k_head = k->stride[1];
   p.v = static_cast<const uint16_t*>(v->ptr);
   p.v_tok = v->stride[0];
   p.v_head = v->stride[1];
