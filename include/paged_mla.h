@@ -404,7 +404,8 @@ int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla
  *   lse_out   (n_tok, Hq) FP32 contiguous, or NULL
  *   error_word  device int32 (required): a request whose query range is not one inside
  *             n_tok is left out, one whose key range is not inside n_keys has no keys; both
- *             set bit 2.  Bit 4: a wait inside the kernel ran out (outputs not written).
+ *             set bit 2.  Bit 4: a wait inside the kernel ran out; some rows of o and lse are then
+ *             not written (those that are hold their results).
  *   workspace   NULL, or mla_get_prompt_workspace_size(...) bytes, 16-byte aligned (its
  *             contents do not matter): with it, long stretches of keys are cut between the
  *             SMs and joined by a second kernel, so that few or unequal requests fill the

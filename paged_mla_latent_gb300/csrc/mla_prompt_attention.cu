@@ -125,10 +125,12 @@ struct Piece {
   int part;         // where a cut piece leaves its result; -1: the unit is whole
 };
 
-// What the join needs of the unit whose first part a CTA leaves (tiles = 0: none).
+// What the join needs of the unit whose first part a CTA leaves (tiles = 0: none), and whether
+// a wait of the CTA ran out, so that parts of its may be missing (written as it ends).
 struct Cut {
   Piece unit;
   int tiles;
+  int gave_up;
   int64_t u0, weight, span;                // on the line
 };
 
@@ -274,7 +276,7 @@ __device__ __forceinline__ Piece unit_piece(const Unit& u, int cta_tok, int tok_
 // The K/V tile at which a border at point x of the line cuts a unit of n tiles that starts at
 // u0 and is `weight` long.  Short units stay whole, with the span that holds their middle;
 // long ones are cut at multiples of kMinCut tiles.
-__device__ __forceinline__ int cut_at(int64_t u0, int64_t weight, int n, int64_t x, bool cuts) {
+__host__ __device__ __forceinline__ int cut_at(int64_t u0, int64_t weight, int n, int64_t x, bool cuts) {
   if (x <= u0) return 0;
   if (x >= u0 + weight) return n;
   if (!cuts || n < 2 * kMinCut) return x > u0 + weight / 2 ? n : 0;
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mine = w.j0 < w.j1;
             if (mine && (w.j0 > 0 || w.j1 < tiles)) {
               w.part = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-              if (w.j0 == 0) p.cuts[blockIdx.x] = {w, tiles, u.u0, weight, sp.length};
+              if (w.j0 == 0) p.cuts[blockIdx.x] = {w, tiles, 0, u.u0, weight, sp.length};
             }
           }
           if (mine) {
@@ -937,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (p.parts && threadIdx.x == 0) p.cuts[blockIdx.x].gave_up = *abort_flag;
   if (warp == 9) {
     if (lane == 0) mbar_wait_drain(drain, 0);   // all issued MMAs complete (bounded)
     __syncwarp();
@@ -946,7 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the unit that span blockIdx.x cuts and has the first part of; blockIdx.y
-// takes 32 of its 256 rows, eight threads a row.  Bytes bound: the parts, from L2.
+// takes 32 of its 256 rows, eight threads a row.  Bytes bound: the parts, from L2.  Where a CTA
+// gave up, cut units stay unwritten: a missing part's place holds whatever was there.
 template <int DV>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
   constexpr int kPart = 2 * kRows * (DV + 2);
@@ -968,7 +972,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
     }
     sh_n = parts;
   }
-  __syncthreads();
+  int gave_up = 0;
+  for (int i = threadIdx.x; i <= gridDim.x; i += blockDim.x) gave_up |= p.cuts[i].gave_up;
+  if (__syncthreads_or(gave_up)) return;
   const int n_parts = sh_n;
   const int row = 32 * blockIdx.y + (threadIdx.x >> 3), q = threadIdx.x & 7;
   const int s = row / kRows, r = row - s * kRows;
