@@ -153,13 +153,13 @@ def _stream(stream, device):
     return ctypes.c_void_p(int(stream))
 
 
-def _current_device():
-    return torch._C._cuda_getDevice()        # (torch.cuda's own asks for its set-up each time)
+# the index of the current CUDA device, where the library launches and whose SMs it counts (a
+# call's tensors may be on another; torch.cuda's own function checks its set-up each time)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(device, fn, *args):
-    """A library call with CUDA device `device` (an index) as the current one: the library
-    launches there and asks it for its SMs."""
+    """A library call with CUDA device `device` (an index) as the current one."""
     if device < 0 or _current_device() == device:      # (CPU tensors: the library refuses them)
         return fn(*args)
     with torch.cuda.device(device):
@@ -446,9 +446,13 @@ def mla_gqa_rope_and_cache(q, k, v, positions, cos_sin, is_neox, slot_mapping, q
     k_out may be q and k; k_scale and v_scale belong to e4m3 caches.  error_word: an int32
     device tensor (>= 1 element)."""
     d = _cuda_index(q)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_gqa_rope_and_cache(q, k, v, positions, cos_sin, is_neox, slot_mapping, q_out,
+                                          k_cache, v_cache, error_word, k_scale, v_scale, k_out,
+                                          stream)
     ew = _error_word(error_word, d)
-    rc = _call(
-        d, _lib.mla_gqa_rope_and_cache,
+    rc = _lib.mla_gqa_rope_and_cache(
         _packed(q, d), _packed(k, d), _packed(v, d), _packed(positions, d), _packed(cos_sin, d),
         int(is_neox), _packed(slot_mapping, d), _packed(k_scale, d), _packed(v_scale, d),
         _packed(q_out, d), _packed(k_out, d), _packed(k_cache, d), _packed(v_cache, d), ew,
@@ -479,14 +483,17 @@ def mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_l
     """Attention of one new token a request over paged per-head caches (see
     include/paged_mla.h).  Returns the workspace used."""
     d = _cuda_index(q)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_gqa_decode(q, k_cache, v_cache, o, kv_indptr, kv_indices, kv_last_page_lens,
+                                  sm_scale, k_scale, v_scale, lse_out, workspace, stream)
     if workspace is None:
         with _on_stream(stream, q.device):      # made and zeroed on the stream that uses it
             workspace = make_gqa_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[2],
                                                   q.shape[2], q.device)
     elif workspace.get_device() != d:
         raise ValueError(f"the workspace must be on CUDA device {d}")
-    rc = _call(
-        d, _lib.mla_gqa_decode,
+    rc = _lib.mla_gqa_decode(
         _packed(q, d), _packed(k_cache, d), _packed(v_cache, d), _packed(o, d),
         _packed(kv_indptr, d), _packed(kv_indices, d), _packed(kv_last_page_lens, d),
         float(sm_scale), _packed(k_scale, d), _packed(v_scale, d), _packed(lse_out, d),
@@ -518,9 +525,13 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
     on the call's stream (up to 40 MB; nothing where no request can be long enough to be cut
     between SMs)."""
     d = _cuda_index(q)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word, lse_out,
+                                        workspace, stream)
     ew = _error_word(error_word, d)
     if workspace is None:
-        n = _call(d, mla_get_prompt_workspace_size, k.shape[0], v.shape[-1])
+        n = mla_get_prompt_workspace_size(k.shape[0], v.shape[-1])
         if n and stream is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
         elif n:
@@ -530,8 +541,7 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
         raise ValueError(f"the workspace must be on CUDA device {d}")
     ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
-    rc = _call(
-        d, _lib.mla_prompt_attention,
+    rc = _lib.mla_prompt_attention(
         _packed(q, d), _packed(k, d), _packed(v, d), _packed(o, d), _packed(qo_indptr, d),
         _packed(kv_indptr, d), float(sm_scale), _packed(lse_out, d), ew, ws, n,
         _raw_stream(stream, d))
