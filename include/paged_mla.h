@@ -358,7 +358,9 @@ int mla_get_gqa_decode_workspace_size(int32_t batch_size, int32_t num_heads, int
  * mla_decode: (pages - 1) * PS + kv_last_page_lens[b], 0 without pages):
  *   s_j = sm_scale * k_scale * sum_d q[b, h, d] * k_j[d]
  *   lse = ln sum_j exp(s_j),   o[b, h] = v_scale * sum_j exp(s_j - lse) * v_j
- * No position (or no finite maximum: every score -inf) gives o = 0 and lse = -inf.
+ * No position (or no finite maximum: every score -inf) gives o = 0 and lse = -inf.  Sums and
+ * maxima are fp32; the weights are rounded to bf16 for the product with a BF16 cache's values
+ * (2^-8 of a weight at most) and to 11 bits for that with an E4M3FN cache's.
  *   q             (B, Hq, D) BF16, D 64 or 128, as above
  *   k_cache, v_cache, k_scale, v_scale  as above; bytes past a request's positions (a last
  *                 page's tail, other pages) are never read
@@ -393,7 +395,8 @@ int mla_gqa_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache, const mla
  * So does a row all of whose scores are -inf.  Values outside J (later positions, other
  * requests, anything past the last row) do not reach a row, infinities and NaN among them;
  * inside J an infinite value has its weight's part, NaN where that weight is zero (a score of
- * -inf, or too small for fp32).
+ * -inf, or too small for fp32).  Sums and maxima are fp32; the weights are rounded to bf16 for
+ * the product with v (2^-8 of a weight at most).
  *   q         (n_tok, Hq, D) BF16, k (n_keys, Hk, D) BF16, v (n_keys, Hk, Dv) BF16 with
  *             (D, Dv) = (64, 64), (128, 128) or (192, 128), Hq / Hk <= 128; each: last dim
  *             contiguous, 16-byte aligned, other strides positive multiples of 8 elements

@@ -6,11 +6,13 @@
 //   heads of a KV head.
 //
 // Bound by the cache's bytes: 2 D elements a position and KV head, each used by G heads.
-// Measured (one GB300, pages of 128 or 16): 64 requests of 2,048 to 65,536 positions, two KV
+// Measured (GB300, pages of 128 or 16, calls in a CUDA graph; on its own a call takes at least the
+// 10 us of its host side): 64 requests of 2,048 to 65,536 positions, two KV
 // heads, bf16, 1.51 GB: 223 us, 6.77 TB/s (the copy rate); one of 142,000 positions,
-// eight KV heads, e4m3, 291 MB: 56 us, of which 40 stream the cache, the rest are the plan, the
+// eight KV heads, e4m3, 291 MB: 57 us, of which 40 stream the cache, the rest are the plan, the
 // first tiles and the join of 19 pieces a unit; 37 ragged requests, 10.6 MB: 11.5 us; one of 137
-// positions: 5.3 us.
+// positions: 5.4 us.  64 requests of 8,192 positions, two KV heads of 64, eight query heads each:
+// 48 us in bf16 (5.5 TB/s), 37 in e4m3 (3.6).
 //
 // Work split.  A unit is (request, KV head, chunk of 8 NT query heads); its positions are cut
 // into tiles of 16 or 32.  All units' tiles form one line and every CTA takes an equal span of it,

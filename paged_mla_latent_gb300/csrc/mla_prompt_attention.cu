@@ -34,19 +34,22 @@
 //                    past the request (another request's, or stale memory) and takes
 //                    non-finite values out of V (0 * inf would reach rows that do not see
 //                    them); rows that do see one get it back at the end, times its weight.
-// Tensor memory: S_0 S_1 O_0 O_1, 128 columns each (all 512); P_s lies over S_s.
+// Tensor memory: S_0 S_1 O_0 O_1, 128 columns each (all 512; 64-wide values leave half of an O's
+// unused); P_s lies over S_s, rounded to V's bf16 (by 2^-8 of a weight at most).
 //
 // The running maximum is only raised when it would grow by more than 8 (in log2): then the
 // thread rescales its row of O itself (the MMA that wrote S(j) was issued after PV(j-1), so
 // O is idle).  Weights stay below 2^8, sums in fp32.  P is rounded to bf16 (2^-8 of each
 // weight at most); l is summed from the unrounded weights.
 //
-// Measured (one GB300): 16,384 tokens, 32/8 heads of 128: 1.38 ms call after call, 1590 TFLOP/s
-// (0.83 of cuBLAS's burst bf16 rate, 0.92 of its sustained one), 1.28 ms alone with the tensor
-// pipe 75 % busy; 4,089 queries behind 63,911 positions, 12 heads of 192/128: 1.28 ms, 1610
-// TFLOP/s; 24 packed prompts of 17 to 4,089: 275 us, 1040 TFLOP/s.  What bounds it: a tile's loop
-// is its softmax (about 1500 cycles) and then its PV and QK (1024), of which two tiles' overlap;
-// in short units the ends (Q behind the last S, the last PV, the result: 7400 cycles).
+// Measured (GB300, one call after another, inputs in turn): 16,384 tokens, 32/8 heads of 128:
+// 1.40 to 1.42 ms, 1555 to 1575 TFLOP/s (0.82 of cuBLAS's burst bf16 rate, 0.91 of its sustained
+// one), of which 1.28 ms in the kernel alone, the tensor pipe 75 % busy; 4,089 queries behind
+// 63,911 positions, 12 heads of 192/128: 1.30 to 1.31 ms, 1575 to 1590 TFLOP/s; 24 packed prompts
+// of 17 to 4,089: 277 us, 1030 TFLOP/s.  64-wide heads (in a graph): 16,384 tokens 1.20 ms, 915
+// TFLOP/s; the packed prompts 245 us.  What bounds it: a tile's loop is its softmax (about 1500
+// cycles) and then its PV and QK (1024; 512 with 64-wide heads), of which two tiles' overlap; in
+// short units the ends (Q behind the last S, the last PV, the result: 7400 cycles).
 //
 // Every wait is bounded (2 s): one that runs out sets the error word and ends the CTA.
 #include <cuda.h>
@@ -77,8 +80,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;              // log2 growth of the maximum that forces a rescale
 
 // Fixed cost of a unit on the line (its Q, the first tile's way, its result: 7,400 cycles against
-// 2,700 a tile, fitted over the CTAs of packed prompts) in positions; with 512 the packed prompts
-// take 278 us instead of 266.  The fewest K/V tiles a part of a cut unit may have: writing and
+// 2,700 a tile, fitted over the CTAs of packed prompts of 128-wide heads, and taken for the other
+// widths without a fit of their own) in positions; with 512 those prompts take 278 us instead of
+// 266.  The fewest K/V tiles a part of a cut unit may have: writing and
 // joining a part moves 266 KB, about four tiles' time of an SM.
 constexpr int kUnitCost = 352;
 constexpr int kMinCut = 8;                 // a power of two
