@@ -2,8 +2,9 @@
 
 Every function here has the name of the C entry point it calls in
 ``include/paged_mla.h``; each converts torch tensors to ``mla_tensor_t`` descriptors
-(pointer, dtype, shape, strides) and passes the current CUDA stream.  All arithmetic runs
-in the library's CUDA kernels; there is no Python or CPU fallback: if the library cannot
+(pointer, dtype, shape, strides) and passes the current CUDA stream.  Calls run on the
+device of their tensors, whichever one is current.  All arithmetic runs in the library's
+CUDA kernels; there is no Python or CPU fallback: if the library cannot
 be loaded, importing this package raises.
 
 The operation ("[Kimi-K3 MLA TP8] MLA performance", §2-§5; "Scaling Kimi K3 on AMD
