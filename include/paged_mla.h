@@ -431,6 +431,152 @@ int mla_get_prompt_workspace_size(int64_t n_keys, int32_t v_head_dim, int32_t nu
                                   size_t* bytes_out);
 
 /*
+ * The four entry points below serve per-head caches held in 8 bits with a scale of its own for
+ * each block of positions and head (k_cache, v_cache, k_scale, v_scale):
+ *   k_cache, v_cache  (N_pages, PS, Hk, D) E4M3FN codes, D 64 or 128, as above
+ *   k_scale, v_scale  (N_pages, NB, Hk) FP32, both of one set of strides, no two elements in one
+ *                     place, NB a power of two; a block is BS = PS / NB <= 128 slots of one page
+ *                     and head, and slot s of page p holds code * scale[p][s / BS][h]
+ * They run in this order: the page table, the append, then the gather and mla_prompt_attention
+ * for prompts behind a cached prefix, or the decode of a request's newest tokens.  The page
+ * lists (kv_indptr, kv_indices, kv_last_page_lens) are those of mla_decode, after the step:
+ * request b holds L_b positions, of which the last T_b = qo_indptr[b+1] - qo_indptr[b] are the
+ * step's.
+ *
+ * mla_build_page_table: the lists of a step from the requests' lengths, on the device, with pages
+ * for the new tokens taken from a stack of free ones (any cache: the latent one's, too).  With
+ * P_b = ceil(L_b / PS) and O_b = ceil((L_b - T_b) / PS):
+ *   block_table[b][j] = free_pages[n - 1 - (sum_{c<b} (P_c - O_c) + j - O_b)]    (O_b <= j < P_b)
+ *   *free_count_out   = n - sum_b (P_b - O_b),   n = *free_count
+ *   qo_indptr, key_indptr, kv_indptr = running sums of T, L and P, each from 0
+ *   kv_indices[kv_indptr[b] + j] = block_table[b][j]                             (j < P_b)
+ *   kv_last_page_lens[b] = L_b - (P_b - 1) PS  (1 where L_b = 0)
+ *   positions[qo_indptr[b] + i]    = L_b - T_b + i                               (i < T_b)
+ *   slot_mapping[qo_indptr[b] + i] = its page * PS + its place in it
+ *   seq_lens, new_lens  (B,) INT32: L_b and T_b, 0 <= T_b <= L_b; B <= 16384
+ *   block_table   (B, W) INT32 page ids, last dim contiguous, P_b <= W, W * PS < 2^31 (its
+ *                 entries [O_b, P_b) are written where there is a pool, nothing else is)
+ *   page_size     PS, a power of two <= 1024
+ *   free_pages, free_count, free_count_out  (F,) INT32 and two INT32 of one element on the device,
+ *                 which may be one; all three or none (NULL): without, the table has every page
+ *                 already.  Freed pages are pushed by writing them at free_pages[*free_count ..].
+ *   qo_indptr, key_indptr, kv_indptr (B+1,), kv_last_page_lens (B,) INT32 (written)
+ *   kv_indices    INT32 (written up to sum P; entries behind are left as they were)
+ *   positions, slot_mapping  INT32 of one length, both or none (NULL); entries behind the last
+ *                 request's tokens become 0 and -1, so that a padded step appends nothing there
+ *   error_word    two INT32 on the device (required): [0] error bits, [1] is the call's own, zero
+ *                 before first use and left so; calls that share it must not overlap on the GPU.
+ * Device-side errors: a request whose lengths make no sense (negative, T_b > L_b, P_b > W) counts
+ * as empty and sets bit 2; a list longer than its buffer (or sums past 2^31) is cut and sets bit
+ * 8; a pool that runs out gives pages of -1 (which readers flag) and slots of -1, *free_count_out
+ * is then 0, bit 1 (a *free_count outside [0, F] counts as 0 and stays).  The rest of the outputs
+ * must not overlap one another or the inputs.
+ */
+int mla_build_page_table(const mla_tensor_t* seq_lens, const mla_tensor_t* new_lens,
+                         const mla_tensor_t* block_table, int32_t page_size,
+                         const mla_tensor_t* free_pages, const mla_tensor_t* free_count,
+                         const mla_tensor_t* free_count_out, const mla_tensor_t* qo_indptr,
+                         const mla_tensor_t* key_indptr, const mla_tensor_t* kv_indptr,
+                         const mla_tensor_t* kv_indices, const mla_tensor_t* kv_last_page_lens,
+                         const mla_tensor_t* positions, const mla_tensor_t* slot_mapping,
+                         int32_t* error_word, mla_stream_t stream);
+
+/*
+ * mla_gqa_rope_and_cache for caches with a scale for each block and head: rot, q, k, v, positions,
+ * cos_sin, is_neox, q_out and k_out as there.  Token qo_indptr[b] + i goes to position
+ * L_b - T_b + i of request b.  For a block and head with new values x (rot(k), or v, in fp32):
+ *   a = max |x| over the block's new values that are finite,
+ *   s(a) = the smallest power of two with a <= 448 s(a), from 2^-60 to 2^120
+ *   scale' = s(a)               where the block's first position is among the new ones
+ *          = max(scale, s(a))   where it is not (the block continues)
+ *   code = e(x, scale') for the new positions
+ *   code = e(fp32(code * fp32(scale / scale')), 1) for the block's earlier ones, where scale' > scale
+ * so that appending token by token or at once differs by the roundings of grown blocks only:
+ * scales are powers of two, under which codes change exactly but for those that become subnormal
+ * (2^-9 of the new scale).  Infinite values saturate at 448 scale', NaN stays NaN.
+ * Blocks that hold no new position keep codes and scale; so do slots behind the new positions.
+ * A block that several requests' lists share must hold no new position of any of them (whole
+ * shared pages); two requests that append to one page race.  Tokens behind qo_indptr[B] are left
+ * out, their rows of q_out and k_out as they were.
+ *   error_word    device int32 (required).  A request whose lists make no sense (token range not
+ *                 inside T, page list not monotone or not inside kv_indices, T_b > L_b) appends
+ *                 nothing (no k_out either) and sets bit 2; a page outside the cache is skipped
+ *                 and sets bit 64; a rotary position outside [0, max_pos) sets bit 1 and leaves
+ *                 that token's rotated columns (of q_out, k_out and its key entry) unwritten.
+ */
+int mla_gqa_block_append(const mla_tensor_t* q, const mla_tensor_t* k, const mla_tensor_t* v,
+                         const mla_tensor_t* positions, const mla_tensor_t* cos_sin,
+                         int32_t is_neox, const mla_tensor_t* qo_indptr,
+                         const mla_tensor_t* kv_indptr, const mla_tensor_t* kv_indices,
+                         const mla_tensor_t* kv_last_page_lens, const mla_tensor_t* q_out,
+                         const mla_tensor_t* k_out, const mla_tensor_t* k_cache,
+                         const mla_tensor_t* v_cache, const mla_tensor_t* k_scale,
+                         const mla_tensor_t* v_scale, int32_t* error_word, mla_stream_t stream);
+
+/*
+ * Requests' keys and values as packed rows, as mla_prompt_attention reads them (its kv_indptr is
+ * row_indptr): for position j < L_b of request b
+ *   k_rows[row_indptr[b] + j] = bf16(fp32(code * scale))          (j < L_b - T_b)
+ *                             = k_new[qo_indptr[b] + j - (L_b - T_b)]     otherwise
+ * and v_rows likewise.
+ *   row_indptr    (B+1,) INT32, row_indptr[b+1] - row_indptr[b] = L_b (key_indptr of
+ *                 mla_build_page_table)
+ *   qo_indptr, k_new, v_new  (B+1,) INT32 and (T, Hk, D) BF16, the step's rotated keys and its
+ *                 values; all or none (NULL: every position comes from the cache)
+ *   k_rows, v_rows  (n, Hk, D) BF16 (written; rows behind row_indptr[B] are left as they were)
+ *                 (BF16 tensors: last dim contiguous, 16-byte aligned, other strides non-negative
+ *                 multiples of 8 elements, outputs' rows not overlapping)
+ *   error_word    device int32 (required).  A request whose lists make no sense (page list, token
+ *                 range or row range, or a row range that is not L_b long) is left out and sets
+ *                 bit 2; a page outside the cache gives zeros and sets bit 64.
+ */
+int mla_gqa_block_gather(const mla_tensor_t* k_cache, const mla_tensor_t* v_cache,
+                         const mla_tensor_t* k_scale, const mla_tensor_t* v_scale,
+                         const mla_tensor_t* kv_indptr, const mla_tensor_t* kv_indices,
+                         const mla_tensor_t* kv_last_page_lens, const mla_tensor_t* row_indptr,
+                         const mla_tensor_t* qo_indptr, const mla_tensor_t* k_new,
+                         const mla_tensor_t* v_new, const mla_tensor_t* k_rows,
+                         const mla_tensor_t* v_rows, int32_t* error_word, mla_stream_t stream);
+
+/*
+ * Bytes of workspace mla_gqa_block_decode needs for calls of this shape on a GPU with num_sms SMs
+ * (<= 0: the current device's).  It does not grow with the batch or the lengths.
+ */
+int mla_get_gqa_block_decode_workspace_size(int32_t num_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_seqlen_q,
+                                            int32_t num_sms, size_t* bytes_out);
+
+/*
+ * Attention of each request's newest T_b tokens over the cache mla_gqa_block_append writes (one
+ * token a decode step; a few where drafts are verified).  Query t < T_b of request b, head h, KV
+ * head h / G, over positions j <= L_b - T_b + t (as mla_decode: causal among the new tokens):
+ *   s_j = sm_scale * kscale(j) * sum_d q[r, h, d] * kcode_j[d],   r = qo_indptr[b] + t
+ *   lse = ln sum_j exp(s_j),   o[r, h] = sum_j exp(s_j - lse) * vscale(j) * vcode_j
+ * No position (or no finite maximum) gives o = 0 and lse = -inf.  Sums and maxima are fp32; the
+ * weights times their v scale are rounded to 11 bits for the product with the codes, those below
+ * 2^-38 of the largest are lost.  Scales of v are finite and not negative; one below 2^-60 (zero
+ * among them) counts as 2^-60.
+ *   q             (sum_T, Hq, D) BF16, D 64 or 128, as above
+ *   o             (sum_T, Hq, D) BF16 or FP32, last dim contiguous, no two rows overlapping
+ *                 (written; rows of no request are not)
+ *   qo_indptr     (B+1,) INT32;  max_seqlen_q >= every T_b, 1..64
+ *   lse_out       (sum_T, Hq) FP32 contiguous, or NULL
+ *   workspace     mla_get_gqa_block_decode_workspace_size(...) bytes, as mla_gqa_decode's (calls of
+ *                 both may share one that is large enough, if they do not overlap on the GPU)
+ * The result does not depend on the order in which the pieces of a split request finish.
+ * Device-side errors go to the workspace's error word (mla_check_error): a page list that makes
+ * no sense makes that request empty, a token range outside sum_T or of more than max_seqlen_q
+ * leaves it out, a page id outside the cache reads as zeros; all give MLA_ERR_BAD_INDEX.
+ */
+int mla_gqa_block_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache,
+                         const mla_tensor_t* v_cache, const mla_tensor_t* k_scale,
+                         const mla_tensor_t* v_scale, const mla_tensor_t* o,
+                         const mla_tensor_t* qo_indptr, const mla_tensor_t* kv_indptr,
+                         const mla_tensor_t* kv_indices, const mla_tensor_t* kv_last_page_lens,
+                         int32_t max_seqlen_q, float sm_scale, const mla_tensor_t* lse_out,
+                         void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
  * Debug check of a decode call's index inputs on the device, then a host status:
  * MLA_OK, MLA_ERR_BAD_INPUT (indptr not monotone or not starting at 0 for qo, kv_len <
  * q_len, kv_last_page_lens outside [1, PS] (!= 1 when PS = 1), qo_indptr[B] != sum_T) or

@@ -31,7 +31,9 @@ __all__ = [
     "mla_status_string", "make_workspace", "library_path", "PreparedDecode", "mla_latent_to_v",
     "mla_selftest_bounded_wait", "mla_qk_rope_concat_and_cache", "mla_gqa_rope_and_cache",
     "mla_gqa_decode", "mla_get_gqa_decode_workspace_size", "make_gqa_decode_workspace",
-    "mla_prompt_attention", "mla_get_prompt_workspace_size",
+    "mla_prompt_attention", "mla_get_prompt_workspace_size", "mla_build_page_table",
+    "mla_gqa_block_append", "mla_gqa_block_gather", "mla_gqa_block_decode",
+    "mla_get_gqa_block_decode_workspace_size", "make_gqa_block_decode_workspace",
 ]
 
 MLA_DTYPE_FP8_E4M3FN = 1
@@ -98,6 +100,16 @@ def _load() -> ctypes.CDLL:
     lib.mla_prompt_attention.argtypes = [vp] * 6 + [ctypes.c_float] + [vp] * 3 + [c_sz, vp]
     lib.mla_get_prompt_workspace_size.restype = ctypes.c_int
     lib.mla_get_prompt_workspace_size.argtypes = [ctypes.c_int64, c_i32, c_i32, ctypes.POINTER(c_sz)]
+    lib.mla_build_page_table.restype = ctypes.c_int
+    lib.mla_build_page_table.argtypes = [vp] * 3 + [c_i32] + [vp] * 12
+    lib.mla_gqa_block_append.restype = ctypes.c_int
+    lib.mla_gqa_block_append.argtypes = [vp] * 5 + [c_i32] + [vp] * 12
+    lib.mla_gqa_block_gather.restype = ctypes.c_int
+    lib.mla_gqa_block_gather.argtypes = [vp] * 15
+    lib.mla_get_gqa_block_decode_workspace_size.restype = ctypes.c_int
+    lib.mla_get_gqa_block_decode_workspace_size.argtypes = [c_i32] * 5 + [ctypes.POINTER(c_sz)]
+    lib.mla_gqa_block_decode.restype = ctypes.c_int
+    lib.mla_gqa_block_decode.argtypes = [vp] * 10 + [c_i32, ctypes.c_float] + [vp] * 2 + [c_sz, vp]
     lib.mla_selftest_bounded_wait.restype = ctypes.c_int
     lib.mla_selftest_bounded_wait.argtypes = [vp, vp, ctypes.c_int64, vp]
     return lib
@@ -432,10 +444,12 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _error_word(error_word, device):
+def _error_word(error_word, device, words=1):
     if not isinstance(error_word, torch.Tensor) or error_word.dtype is not torch.int32 or \
-            error_word.get_device() != device or error_word.numel() < 1:
-        raise ValueError(f"error_word must be an int32 tensor on CUDA device {device}")
+            error_word.get_device() != device or error_word.numel() < words or \
+            (words > 1 and not error_word.is_contiguous()):
+        raise ValueError(f"error_word must be an int32 tensor on CUDA device {device}" +
+                         (f" of at least {words} contiguous elements" if words > 1 else ""))
     return error_word.data_ptr()
 
 
@@ -547,6 +561,118 @@ def mla_prompt_attention(q, k, v, o, qo_indptr, kv_indptr, sm_scale, error_word,
         _packed(kv_indptr, d), float(sm_scale), _packed(lse_out, d), ew, ws, n,
         _raw_stream(stream, d))
     _check(rc, "mla_prompt_attention")
+
+
+def mla_build_page_table(seq_lens, new_lens, block_table, page_size, qo_indptr, key_indptr, kv_indptr,
+                         kv_indices, kv_last_page_lens, error_word, positions=None, slot_mapping=None,
+                         free_pages=None, free_count=None, free_count_out=None, stream=None):
+    """Build a step's page lists, positions and cache slots on the device from the requests'
+    lengths, taking pages for the new tokens from a stack of free ones (see
+    include/paged_mla.h).  error_word: an int32 device tensor of two elements, zero before its
+    first use.  free_count_out may be free_count."""
+    d = _cuda_index(seq_lens)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_build_page_table(seq_lens, new_lens, block_table, page_size, qo_indptr,
+                                        key_indptr, kv_indptr, kv_indices, kv_last_page_lens,
+                                        error_word, positions, slot_mapping, free_pages, free_count,
+                                        free_count_out, stream)
+    ew = _error_word(error_word, d, 2)
+    rc = _lib.mla_build_page_table(
+        _packed(seq_lens, d), _packed(new_lens, d), _packed(block_table, d), int(page_size),
+        _packed(free_pages, d), _packed(free_count, d), _packed(free_count_out, d),
+        _packed(qo_indptr, d), _packed(key_indptr, d), _packed(kv_indptr, d),
+        _packed(kv_indices, d), _packed(kv_last_page_lens, d), _packed(positions, d),
+        _packed(slot_mapping, d), ew, _raw_stream(stream, d))
+    _check(rc, "mla_build_page_table")
+
+
+def mla_gqa_block_append(q, k, v, positions, cos_sin, is_neox, qo_indptr, kv_indptr, kv_indices,
+                         kv_last_page_lens, q_out, k_cache, v_cache, k_scale, v_scale, error_word,
+                         k_out=None, stream=None):
+    """Rotate q's and the new keys' first cos_sin.shape[1] columns and write each request's new
+    keys and values behind its cached ones, into e4m3 caches with a scale for each block and
+    head (see include/paged_mla.h).  q_out and k_out may be q and k.  error_word: an int32
+    device tensor (>= 1 element)."""
+    d = _cuda_index(q)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_gqa_block_append(q, k, v, positions, cos_sin, is_neox, qo_indptr, kv_indptr,
+                                        kv_indices, kv_last_page_lens, q_out, k_cache, v_cache,
+                                        k_scale, v_scale, error_word, k_out, stream)
+    ew = _error_word(error_word, d)
+    rc = _lib.mla_gqa_block_append(
+        _packed(q, d), _packed(k, d), _packed(v, d), _packed(positions, d), _packed(cos_sin, d),
+        int(is_neox), _packed(qo_indptr, d), _packed(kv_indptr, d), _packed(kv_indices, d),
+        _packed(kv_last_page_lens, d), _packed(q_out, d), _packed(k_out, d), _packed(k_cache, d),
+        _packed(v_cache, d), _packed(k_scale, d), _packed(v_scale, d), ew, _raw_stream(stream, d))
+    _check(rc, "mla_gqa_block_append")
+
+
+def mla_gqa_block_gather(k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_last_page_lens,
+                         row_indptr, k_rows, v_rows, error_word, qo_indptr=None, k_new=None,
+                         v_new=None, stream=None):
+    """Requests' cached keys and values (and the step's own behind them) as packed bf16 rows for
+    mla_prompt_attention (see include/paged_mla.h).  error_word: an int32 device tensor (>= 1
+    element)."""
+    d = _cuda_index(k_cache)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_gqa_block_gather(k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                                        kv_last_page_lens, row_indptr, k_rows, v_rows, error_word,
+                                        qo_indptr, k_new, v_new, stream)
+    ew = _error_word(error_word, d)
+    rc = _lib.mla_gqa_block_gather(
+        _packed(k_cache, d), _packed(v_cache, d), _packed(k_scale, d), _packed(v_scale, d),
+        _packed(kv_indptr, d), _packed(kv_indices, d), _packed(kv_last_page_lens, d),
+        _packed(row_indptr, d), _packed(qo_indptr, d), _packed(k_new, d), _packed(v_new, d),
+        _packed(k_rows, d), _packed(v_rows, d), ew, _raw_stream(stream, d))
+    _check(rc, "mla_gqa_block_gather")
+
+
+def mla_get_gqa_block_decode_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int,
+                                            max_seqlen_q: int = 1, num_sms: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.mla_get_gqa_block_decode_workspace_size(num_heads, num_kv_heads, head_dim, max_seqlen_q,
+                                                        num_sms, ctypes.byref(out)),
+           "mla_get_gqa_block_decode_workspace_size")
+    return int(out.value)
+
+
+def make_gqa_block_decode_workspace(num_heads: int, num_kv_heads: int, head_dim: int,
+                                    max_seqlen_q: int = 1, device=None) -> torch.Tensor:
+    """A zero-initialised device workspace for mla_gqa_block_decode calls of this shape."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = mla_get_gqa_block_decode_workspace_size(num_heads, num_kv_heads, head_dim, max_seqlen_q)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def mla_gqa_block_decode(q, k_cache, v_cache, k_scale, v_scale, o, qo_indptr, kv_indptr, kv_indices,
+                         kv_last_page_lens, max_seqlen_q, sm_scale, lse_out=None, workspace=None,
+                         stream=None):
+    """Attention of each request's newest tokens over paged e4m3 caches with a scale for each
+    block and head (see include/paged_mla.h).  Returns the workspace used."""
+    d = _cuda_index(q)
+    if d != _current_device():
+        with torch.cuda.device(d):
+            return mla_gqa_block_decode(q, k_cache, v_cache, k_scale, v_scale, o, qo_indptr, kv_indptr,
+                                        kv_indices, kv_last_page_lens, max_seqlen_q, sm_scale, lse_out,
+                                        workspace, stream)
+    if workspace is None:
+        with _on_stream(stream, q.device):      # made and zeroed on the stream that uses it
+            workspace = make_gqa_block_decode_workspace(q.shape[1], k_cache.shape[2], q.shape[2],
+                                                        max_seqlen_q, q.device)
+    elif workspace.get_device() != d:
+        raise ValueError(f"the workspace must be on CUDA device {d}")
+    rc = _lib.mla_gqa_block_decode(
+        _packed(q, d), _packed(k_cache, d), _packed(v_cache, d), _packed(k_scale, d),
+        _packed(v_scale, d), _packed(o, d), _packed(qo_indptr, d), _packed(kv_indptr, d),
+        _packed(kv_indices, d), _packed(kv_last_page_lens, d), int(max_seqlen_q), float(sm_scale),
+        _packed(lse_out, d), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _raw_stream(stream, d))
+    _check(rc, "mla_gqa_block_decode")
+    return workspace
 
 
 def mla_selftest_bounded_wait(error_word, result, limit_ns, stream=None):

@@ -1,0 +1,41 @@
+// Page lists on the device, for kernels that walk requests' positions.
+#pragma once
+
+#include <stdint.h>
+
+namespace pmla {
+
+struct PageList {
+  const int32_t *indptr, *indices, *last;   // last: null for one-token pages
+  int64_t n_idx;
+  int log2_page;
+
+  // Positions of request b; -1 where its list makes no sense.
+  __device__ __forceinline__ int positions(int b) const {
+    const int64_t s = __ldg(indptr + b), e = __ldg(indptr + b + 1);
+    const int ps = 1 << log2_page;
+    const int fill = last ? __ldg(last + b) : ps;
+    if (s < 0 || e < s || e > n_idx) return -1;
+    if (e == s) return 0;
+    const int64_t n = ((e - s - 1) << log2_page) + (fill < 1 ? 1 : (fill > ps ? ps : fill));
+    return n > 0x7FFFFF00 ? -1 : static_cast<int>(n);
+  }
+};
+
+// The last b in [0, n) with start(b) <= x, by a whole warp (start(0) <= x, start rising): 31
+// probes at a time, so that lists of up to 32 take one round trip to memory, of 1,024 two.
+template <class Start>
+__device__ __forceinline__ int warp_owner(int n, int lane, int64_t x, Start start) {
+  int lo = 0, width = n;                    // the answer lies in [lo, lo + width)
+  while (width > 1) {
+    const int step = (width + 31) / 32;
+    const int at = (lane + 1) * step;       // lane 31's probe is never inside
+    const bool before = at < width && start(lo + at) <= x;
+    const int passed = __popc(__ballot_sync(0xffffffffu, before));
+    lo += passed * step;
+    width = width - passed * step < step ? width - passed * step : step;
+  }
+  return lo;
+}
+
+}  // namespace pmla
