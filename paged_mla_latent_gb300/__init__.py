@@ -2,7 +2,8 @@
 
 Every function here has the name of the C entry point it calls in
 ``include/paged_mla.h``; each converts torch tensors to ``mla_tensor_t`` descriptors
-(pointer, dtype, shape, strides) and passes the current CUDA stream.  Calls run on the
+(pointer, dtype, shape, strides), through ctypes or, where calls take a few microseconds, in
+a compiled module, and passes the current CUDA stream.  Calls run on the
 device of their tensors, whichever one is current.  All arithmetic runs in the library's
 CUDA kernels; there is no Python or CPU fallback: if the library cannot
 be loaded, importing this package raises.
@@ -18,6 +19,7 @@ softmax-weighted merge of split-KV or context-shard partials.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 
@@ -115,7 +117,16 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+def _load_native():
+    """The module whose calls take torch tensors (built next to the library, which it links)."""
+    spec = importlib.util.spec_from_file_location("pmla_native", _build.NATIVE_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 _lib = _load()
+_native = _load_native()
 
 
 def library_path() -> str:
@@ -444,12 +455,10 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _error_word(error_word, device, words=1):
+def _error_word(error_word, device):
     if not isinstance(error_word, torch.Tensor) or error_word.dtype is not torch.int32 or \
-            error_word.get_device() != device or error_word.numel() < words or \
-            (words > 1 and not error_word.is_contiguous()):
-        raise ValueError(f"error_word must be an int32 tensor on CUDA device {device}" +
-                         (f" of at least {words} contiguous elements" if words > 1 else ""))
+            error_word.get_device() != device or error_word.numel() < 1:
+        raise ValueError(f"error_word must be an int32 tensor on CUDA device {device}")
     return error_word.data_ptr()
 
 
@@ -577,13 +586,12 @@ def mla_build_page_table(seq_lens, new_lens, block_table, page_size, qo_indptr, 
                                         key_indptr, kv_indptr, kv_indices, kv_last_page_lens,
                                         error_word, positions, slot_mapping, free_pages, free_count,
                                         free_count_out, stream)
-    ew = _error_word(error_word, d, 2)
-    rc = _lib.mla_build_page_table(
-        _packed(seq_lens, d), _packed(new_lens, d), _packed(block_table, d), int(page_size),
-        _packed(free_pages, d), _packed(free_count, d), _packed(free_count_out, d),
-        _packed(qo_indptr, d), _packed(key_indptr, d), _packed(kv_indptr, d),
-        _packed(kv_indices, d), _packed(kv_last_page_lens, d), _packed(positions, d),
-        _packed(slot_mapping, d), ew, _raw_stream(stream, d))
+    if not isinstance(error_word, torch.Tensor) or error_word.numel() < 2:
+        raise ValueError("error_word must be an int32 tensor of two elements")
+    rc = _native.mla_build_page_table(
+        d, seq_lens, new_lens, block_table, page_size, free_pages, free_count, free_count_out, qo_indptr,
+        key_indptr, kv_indptr, kv_indices, kv_last_page_lens, positions, slot_mapping, error_word,
+        _raw_stream(stream, d))
     _check(rc, "mla_build_page_table")
 
 
@@ -600,12 +608,9 @@ def mla_gqa_block_append(q, k, v, positions, cos_sin, is_neox, qo_indptr, kv_ind
             return mla_gqa_block_append(q, k, v, positions, cos_sin, is_neox, qo_indptr, kv_indptr,
                                         kv_indices, kv_last_page_lens, q_out, k_cache, v_cache,
                                         k_scale, v_scale, error_word, k_out, stream)
-    ew = _error_word(error_word, d)
-    rc = _lib.mla_gqa_block_append(
-        _packed(q, d), _packed(k, d), _packed(v, d), _packed(positions, d), _packed(cos_sin, d),
-        int(is_neox), _packed(qo_indptr, d), _packed(kv_indptr, d), _packed(kv_indices, d),
-        _packed(kv_last_page_lens, d), _packed(q_out, d), _packed(k_out, d), _packed(k_cache, d),
-        _packed(v_cache, d), _packed(k_scale, d), _packed(v_scale, d), ew, _raw_stream(stream, d))
+    rc = _native.mla_gqa_block_append(
+        d, q, k, v, positions, cos_sin, is_neox, qo_indptr, kv_indptr, kv_indices, kv_last_page_lens,
+        q_out, k_out, k_cache, v_cache, k_scale, v_scale, error_word, _raw_stream(stream, d))
     _check(rc, "mla_gqa_block_append")
 
 
@@ -621,12 +626,9 @@ def mla_gqa_block_gather(k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indic
             return mla_gqa_block_gather(k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
                                         kv_last_page_lens, row_indptr, k_rows, v_rows, error_word,
                                         qo_indptr, k_new, v_new, stream)
-    ew = _error_word(error_word, d)
-    rc = _lib.mla_gqa_block_gather(
-        _packed(k_cache, d), _packed(v_cache, d), _packed(k_scale, d), _packed(v_scale, d),
-        _packed(kv_indptr, d), _packed(kv_indices, d), _packed(kv_last_page_lens, d),
-        _packed(row_indptr, d), _packed(qo_indptr, d), _packed(k_new, d), _packed(v_new, d),
-        _packed(k_rows, d), _packed(v_rows, d), ew, _raw_stream(stream, d))
+    rc = _native.mla_gqa_block_gather(
+        d, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_last_page_lens, row_indptr,
+        qo_indptr, k_new, v_new, k_rows, v_rows, error_word, _raw_stream(stream, d))
     _check(rc, "mla_gqa_block_gather")
 
 
@@ -665,12 +667,9 @@ def mla_gqa_block_decode(q, k_cache, v_cache, k_scale, v_scale, o, qo_indptr, kv
                                                         max_seqlen_q, q.device)
     elif workspace.get_device() != d:
         raise ValueError(f"the workspace must be on CUDA device {d}")
-    rc = _lib.mla_gqa_block_decode(
-        _packed(q, d), _packed(k_cache, d), _packed(v_cache, d), _packed(k_scale, d),
-        _packed(v_scale, d), _packed(o, d), _packed(qo_indptr, d), _packed(kv_indptr, d),
-        _packed(kv_indices, d), _packed(kv_last_page_lens, d), int(max_seqlen_q), float(sm_scale),
-        _packed(lse_out, d), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _raw_stream(stream, d))
+    rc = _native.mla_gqa_block_decode(
+        d, q, k_cache, v_cache, k_scale, v_scale, o, qo_indptr, kv_indptr, kv_indices, kv_last_page_lens,
+        max_seqlen_q, sm_scale, lse_out, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, d))
     _check(rc, "mla_gqa_block_decode")
     return workspace
 

@@ -1,9 +1,11 @@
-"""Build libpagedmla.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc.
+"""Build libpagedmla.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc, and the Python
+module whose calls turn torch tensors into its descriptors with g++.
 
-Four translation units (host API + merge kernels, and one per decode instantiation)
-compile in parallel, then link into ``paged_mla_latent_gb300/_build/libpagedmla.so``.
+The translation units (host API + merge kernels, and one per decode instantiation or
+operator) compile in parallel, then link into ``paged_mla_latent_gb300/_build/libpagedmla.so``.
 The CUDA runtime is linked statically, so the library loads on a machine without a GPU
-(the symbol checks of the CPU test-suite rely on that).
+(the symbol checks of the CPU test-suite rely on that).  The module is built against the
+installed torch, whose version its file name carries.
 """
 from __future__ import annotations
 
@@ -11,12 +13,17 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libpagedmla.so")
+NATIVE_PATH = os.path.join(BUILD_DIR, f"pmla_native.torch{torch.__version__}.so")
+NATIVE_SOURCE = os.path.join(CSRC, "native_calls.cpp")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "paged_mla.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -35,13 +42,13 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, os.path.abspath(__file__)]
+        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, NATIVE_SOURCE, os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(NATIVE_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(NATIVE_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -64,8 +71,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(_sources())) as ex:
+    def compile_native():
+        obj = os.path.join(BUILD_DIR, f"native_calls.{os.getpid()}.o")
+        root = os.path.dirname(torch.__file__)
+        include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+                   os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                   os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *(f"-I{d}" for d in include), "-c", NATIVE_SOURCE, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {NATIVE_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    with ThreadPoolExecutor(max_workers=len(_sources()) + 1) as ex:
+        native = ex.submit(compile_native)
         objs = list(ex.map(compile_one, _sources()))
+        native = native.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -77,6 +98,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-shared", "-o", tmp, native, f"-L{BUILD_DIR}", "-l:libpagedmla.so", "-Wl,-rpath,$ORIGIN",
+           f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    os.remove(native)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
     return LIB_PATH
 
 
