@@ -199,14 +199,49 @@ def values(pages, b, cache, scale, n=None):
     return take(cache, (page, slot)).float() * scale[page, slot // pages.bs][..., None]
 
 
+# A weight (with its v scale) is rounded to f16 where the largest counts 2^14; below f16's normal
+# range it loses half of 2^-24, 2^-39 of the largest.
+WEIGHT = ref.F16
+LOST = 2.0 ** -39
+
+
 def attend(pages, b, q, k_cache, v_cache, ks, vs, sm):
-    """o, lse, mass and largest score of the newest q.shape[0] tokens of request b, fp64."""
+    """o, lse, mass and largest score of the newest q.shape[0] tokens of request b, fp64, and what
+    their smallest weights can lose."""
     t, hq, d = q.shape
     hk = k_cache.shape[2]
     group, n = hq // hk, pages.held[b]
     k, v = values(pages, b, k_cache, ks).double(), values(pages, b, v_cache, vs).double()
+    page, slot = pages.where(b, 0, n)
+    scale = vs[page, slot // pages.bs].double().clamp_min(2.0 ** -60)       # (n, hk)
+    codes = take(v_cache, (page, slot)).float().double().abs().sum(0)       # (hk, d)
     limit = (n - t + 1 + torch.arange(t, device=q.device)).repeat_interleave(group)
-    out = [ref.attend(q[:, h * group:(h + 1) * group].double().reshape(t * group, d), k[:, h], v[:, h], sm, limit)
-           for h in range(hk)]
+    out = []
+    for h in range(hk):
+        qq = q[:, h * group:(h + 1) * group].double().reshape(t * group, d)
+        o, lse, mass, big = ref.attend(qq, k[:, h], v[:, h], sm, limit)
+        if n:
+            s = torch.where(torch.arange(n, device=q.device) < limit[:, None], qq @ k[:, h].T * sm, -math.inf)
+            w = torch.exp(s - lse.clamp_min(-1e300)[:, None]) * scale[:, h]
+            lost = LOST * w.amax(1, keepdim=True) * codes[h]
+        else:
+            lost = torch.zeros_like(o)
+        out.append((o, lse, mass, big, lost))
     back = lambda x: x.view(t, group, *x.shape[1:])
     return [torch.cat([back(x) for x in y], dim=1) for y in zip(*out)]
+
+
+def check(got_o, got_lse, want, n_keys, d, out_eps, what):
+    """As ref.check, with what the smallest weights lose."""
+    o, lse, mass, big, lost = want
+    empty = torch.isneginf(lse)
+    ob, lb = ref.bounds(o, torch.where(empty, torch.zeros_like(lse), lse), mass, big, n_keys, d, WEIGHT, out_eps)
+    g = got_o.double()
+    assert torch.isfinite(g).all(), f"{what}: non-finite output"
+    worst = ((g - o).abs() / (ob + lost)).max().item()
+    assert worst <= 1.0, f"{what}: o error {worst:.3f} of its bound"
+    assert (g[empty] == 0).all(), f"{what}: an empty row is not zero"
+    gl = got_lse.double()
+    assert torch.equal(torch.isneginf(gl), empty), f"{what}: lse of empty rows"
+    worst = (torch.where(empty, torch.zeros_like(gl), (gl - lse).abs()) / lb).max().item()
+    assert worst <= 1.0, f"{what}: lse error {worst:.3f} of its bound"
