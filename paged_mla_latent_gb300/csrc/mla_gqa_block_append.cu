@@ -8,14 +8,20 @@
 //   scale grew.  Powers of two cost no precision (e4m3 has three bits whatever the scale) and
 //   make quotients and the earlier codes' growth exact but for e4m3's subnormals.
 //
-// Bytes bound.  A warp takes tiles of 16 positions of one head: eight (or four) lanes a row, a
-// lane two 8-column words half a region apart (the rotated columns or the rest), which with
-// pairs (i, i + R/2) are each other's partners.  A unit is a block (16 positions where blocks are
-// smaller) of one head's keys or values; its rows stay in registers from the maximum to the
-// codes.  Blocks of more than 16 positions have a warp a tile and meet in shared memory where
-// requests bring many tokens; where they bring few, one warp walks the block's tiles with new
-// rows.  Units are found without a scan: request b's start at qo_indptr[b] / 16m + 2 b (each has
-// at most T_b / 16m + 2), and the slots between stay idle.
+// Bytes bound.  A unit is a block (16 positions of smaller ones) of up to 256 columns' threads of
+// heads' keys or values: eight (or four) threads a row of a head, each with two 8-column words half
+// a region apart (the rotated columns or the rest), which with pairs (i, i + R/2) are each other's
+// partners.  The rows are read twice, for the maxima and, from L2, for the codes: kept in registers
+// or shared memory between, they cost more occupancy than the second reading costs (16,384
+// tokens, 8 heads of 128, keys and values alone: 61 us with a warp's 16 rows in registers, 55
+// so).  Units are found without a scan: request b's start at qo_indptr[b] / unit + 2 b (each
+// has at most T_b / unit + 2), and the slots between stay idle.  Queries are turned by blocks of
+// the same launch, a warp four (or eight) tokens and up to four heads.
+//
+// Measured (one GB300, in a CUDA graph): 16,384 tokens, 32/8 heads of 128, blocks of 64, rotated
+// keys kept, 411 MB: 76 us, 5.4 TB/s (0.81 of the copy rate; units of 8 heads 82, of 2 83; without
+// the L2 prefetch 78); 37 requests of 1 to 700 tokens, 25/5 heads of 64, 49 MB: 17 us; one token of
+// 64 requests, 16/2 heads: 5 us, a chain of request, lists, page, scale and words.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,7 +37,7 @@ namespace {
 using namespace pmla;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kTile = 16;                   // positions a warp takes at a time
+constexpr int kUnit = 16;                   // positions of a unit, or a block of them
 
 struct BlockAppendParams {
   const uint16_t *q, *k, *v;                // bf16 bits
@@ -52,9 +58,8 @@ struct BlockAppendParams {
   int64_t n_tok;
   int B, Hq, Hk;
   int half_rot;                             // R / 2
-  int unit_warps;                           // warps of a unit: 1, or a block's tiles
-  int kv_slots;                             // units of one head's keys
-  unsigned kv_ctas, q_ctas;                 // then some that look the lists over
+  int part_heads, parts;                    // heads a unit takes; units of a block's keys and values
+  unsigned kv_ctas, q_ctas;       // then some blocks that look the lists over
   int strip;                                // query heads a warp takes
   int* err;
 };
@@ -75,6 +80,21 @@ __device__ __forceinline__ void widen8(const uint4& w, float* x) {
     x[2 * i] = lo_f32(v[i]);
     x[2 * i + 1] = hi_f32(v[i]);
   }
+}
+
+// Two fp32 values in a register pair, and their products.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // A lane's columns of a row: two words of eight.
@@ -111,13 +131,22 @@ template <bool kNeox>
 __device__ __forceinline__ void turn(float* x, const Angles& a) {
   float* y = x + 8;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float& u = kNeox ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]);
-    float& w = kNeox ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
-    const float uc = __fmul_rn(u, a.c[k]), ws = __fmul_rn(w, a.s[k]);
-    const float wc = __fmul_rn(w, a.c[k]), us = __fmul_rn(u, a.s[k]);
-    u = __fsub_rn(uc, ws);
-    w = __fadd_rn(wc, us);
+  for (int k = 0; k < 8; k += 2) {          // two pairs at once; the sums are scalar: packed ones
+    float& u0 = kNeox ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]);        // come out fused with the products
+    float& w0 = kNeox ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
+    float& u1 = kNeox ? x[k + 1] : (k < 4 ? x[2 * k + 2] : y[2 * k - 6]);
+    float& w1 = kNeox ? y[k + 1] : (k < 4 ? x[2 * k + 3] : y[2 * k - 5]);
+    const uint64_t u = pair(u0, u1), w = pair(w0, w1);
+    const uint64_t cc = pair(a.c[k], a.c[k + 1]), ss = pair(a.s[k], a.s[k + 1]);
+    float a0, a1, b0, b1;
+    unpair(mul2(u, cc), &a0, &a1);
+    unpair(mul2(w, ss), &b0, &b1);
+    u0 = __fsub_rn(a0, b0);
+    u1 = __fsub_rn(a1, b1);
+    unpair(mul2(w, cc), &a0, &a1);
+    unpair(mul2(u, ss), &b0, &b1);
+    w0 = __fadd_rn(a0, b0);
+    w1 = __fadd_rn(a1, b1);
   }
 }
 
@@ -129,21 +158,27 @@ __device__ __forceinline__ float power_for(float a) {
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-// x / s; s is nearly always a power of two with a normal reciprocal.
-struct Quotient {
-  float s, r;
-  bool exact;
-  __device__ explicit Quotient(float scale) : s(scale) {
-    const uint32_t bits = __float_as_uint(scale);
-    exact = (bits & 0x7FFFFFu) == 0 && bits >= (64u << 23) && bits <= (252u << 23);
-    r = __uint_as_float((254u << 23) - (exact ? bits : 127u << 23));
-  }
-  __device__ float operator()(float x) const { return exact ? x * r : __fdiv_rn(x, s); }
-};
-__device__ __forceinline__ uint2 quantise8(const float* x, const Quotient& d) {
+__device__ __noinline__ float quotient(float x, float scale) { return __fdiv_rn(x, scale); }
+// Eight values over a scale as codes: the scale is nearly always a power of two with a normal
+// reciprocal (r, else 0), which is exact; others divide, out of the way.
+__device__ __forceinline__ float exact_reciprocal(float scale) {
+  const uint32_t bits = __float_as_uint(scale);
+  const bool exact = (bits & 0x7FFFFFu) == 0 && bits >= (64u << 23) && bits <= (252u << 23);
+  return exact ? __uint_as_float((254u << 23) - bits) : 0.f;
+}
+__device__ __forceinline__ uint2 quantise8(const float* x, float scale, float r) {
   uint32_t c[4];
+  if (r != 0.f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(d(x[2 * i + 1]), d(x[2 * i]));
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unpair(mul2(pair(x[2 * i], x[2 * i + 1]), pair(r, r)), &a, &b);
+      c[i] = f32x2_to_e4m3x2(b, a);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(quotient(x[2 * i + 1], scale), quotient(x[2 * i], scale));
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
@@ -158,7 +193,9 @@ __device__ __forceinline__ Request request_of(const BlockAppendParams& p, int b)
   return {t0, static_cast<int>(t1 - t0), held, t0 >= 0 && t1 >= t0 && t1 <= p.n_tok && held >= t1 - t0};
 }
 
-// Queries: a warp takes 32 / (D/16) tokens and a strip of heads, whose angles it reads once.
+// Queries: a warp takes 32 / (D/16) tokens and a strip of up to 4 heads, whose words are all in
+// flight before the angles, which wait for the positions.
+constexpr int kMostStrip = 4;
 template <int D, bool kNeox>
 __device__ __forceinline__ void turn_queries(const BlockAppendParams& p, int64_t item, int lane) {
   constexpr int kPieces = D / 16, kRows = 32 / kPieces;
@@ -166,267 +203,265 @@ __device__ __forceinline__ void turn_queries(const BlockAppendParams& p, int64_t
   const int64_t group = item / strips;
   const int h0 = static_cast<int>(item - group * strips) * p.strip;
   const int64_t t = group * kRows + lane / kPieces;
+  if (t >= p.n_tok) return;
   const int64_t live = __ldg(p.qo_indptr + p.B);
-  if (t >= p.n_tok || t >= live) return;
-  const Columns c = columns_of<D>(lane % kPieces, true, p.half_rot);
-  Angles a;
   const int64_t pos = __ldg(p.positions + t);
+  const Columns c = columns_of<D>(lane % kPieces, true, p.half_rot);
+  const int h1 = h0 + p.strip < p.Hq ? h0 + p.strip : p.Hq;
+  const uint16_t* src = p.q + t * p.q_tok + h0 * p.q_head + c.c0;
+  uint4 w[kMostStrip][2];
+#pragma unroll
+  for (int i = 0; i < kMostStrip; ++i)
+    if (h0 + i < h1) {
+      w[i][0] = *reinterpret_cast<const uint4*>(src + i * p.q_head);
+      w[i][1] = *reinterpret_cast<const uint4*>(src + i * p.q_head + c.half);
+    }
+  if (t >= live) return;
+  Angles a;
   const bool known = pos >= 0 && pos < p.max_pos;
   if (!known && h0 == 0 && c.piece == 0) atomicOr(p.err, kErrBadIndex);
   if (c.rot && !known) return;              // the token's rotated columns stay unwritten
   if (c.rot) load_angles<kNeox>(p, pos, c.piece, &a);
-  const uint16_t* src = p.q + t * p.q_tok + c.c0;
-  uint16_t* dst = p.q_out + t * p.qo_tok + c.c0;
-  const int h1 = h0 + p.strip < p.Hq ? h0 + p.strip : p.Hq;
-  constexpr int kAtOnce = 4;
-  for (int h = h0; h < h1; h += kAtOnce) {
-    uint4 w[kAtOnce][2];
+  uint16_t* dst = p.q_out + t * p.qo_tok + h0 * p.qo_head + c.c0;
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      if (h + i < h1) {
-        w[i][0] = *reinterpret_cast<const uint4*>(src + (h + i) * p.q_head);
-        w[i][1] = *reinterpret_cast<const uint4*>(src + (h + i) * p.q_head + c.half);
+  for (int i = 0; i < kMostStrip; ++i)
+    if (h0 + i < h1) {
+      if (c.rot) {
+        float x[16];
+        widen8(w[i][0], x);
+        widen8(w[i][1], x + 8);
+        turn<kNeox>(x, a);
+        w[i][0] = round8(x);
+        w[i][1] = round8(x + 8);
       }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      if (h + i < h1) {
-        if (c.rot) {
-          float x[16];
-          widen8(w[i][0], x);
-          widen8(w[i][1], x + 8);
-          turn<kNeox>(x, a);
-          w[i][0] = round8(x);
-          w[i][1] = round8(x + 8);
-        }
-        *reinterpret_cast<uint4*>(dst + (h + i) * p.qo_head) = w[i][0];
-        *reinterpret_cast<uint4*>(dst + (h + i) * p.qo_head + c.half) = w[i][1];
-      }
-  }
+      *reinterpret_cast<uint4*>(dst + i * p.qo_head) = w[i][0];
+      *reinterpret_cast<uint4*>(dst + i * p.qo_head + c.half) = w[i][1];
+    }
 }
 
 template <int D, bool kNeox>
-__global__ void __launch_bounds__(kThreads, 2) gqa_block_append_kernel(const BlockAppendParams p) {
-  constexpr int kPieces = D / 16;           // lanes a row
-  constexpr int kRows = 32 / kPieces;       // rows a warp reads at once
-  constexpr int kSteps = kTile / kRows;
-  __shared__ float s_top[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const BlockAppendParams p) {
+  constexpr int kPieces = D / 16;           // threads a row of a head
+  constexpr int kMostHeads = kThreads / kPieces;
+  __shared__ uint32_t s_top[kUnit][kMostHeads];          // largest |x| of each block and head, bits
+  __shared__ float s_scale[kUnit][kMostHeads];
+  __shared__ float s_ratio[kMostHeads];     // of the continued block's old scale to its new one
+  __shared__ bool s_grew[kMostHeads];
+  const int tid = threadIdx.x, lane = tid & 31;
   if (blockIdx.x >= p.kv_ctas + p.q_ctas) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x - p.kv_ctas - p.q_ctas) * kThreads + threadIdx.x;
+    const int64_t i = static_cast<int64_t>(blockIdx.x - p.kv_ctas - p.q_ctas) * kThreads + tid;
     if (i < p.B && !request_of(p, static_cast<int>(i)).sound) atomicOr(p.err, kErrBadIndptr);
     return;
   }
   if (blockIdx.x >= p.kv_ctas) {
-    turn_queries<D, kNeox>(p, static_cast<int64_t>(blockIdx.x - p.kv_ctas) * kWarps + warp, lane);
+    turn_queries<D, kNeox>(p, static_cast<int64_t>(blockIdx.x - p.kv_ctas) * kWarps + (tid >> 5), lane);
     return;
   }
-  // ---- the warp's unit: a request, a block of positions, a head's keys or values
-  const int uw = p.unit_warps, wi = warp & (uw - 1);
-  const int unit = blockIdx.x * (kWarps / uw) + warp / uw;
-  const int slot = unit / (2 * p.Hk);
-  if (slot >= p.kv_slots) return;
-  const int part = unit - slot * (2 * p.Hk);
-  const bool is_k = part < p.Hk;
-  const int h = is_k ? part : part - p.Hk;
+  // ---- the unit: a request, a block of positions (or 16 of smaller blocks), keys or values
+  const int slot = blockIdx.x / p.parts, part = blockIdx.x - slot * p.parts;
+  const bool is_k = (part & 1) == 0;
+  const int first_head = (part >> 1) * p.part_heads;
+  const int heads = p.Hk - first_head < p.part_heads ? p.Hk - first_head : p.part_heads;
   const int bs = 1 << p.log2_block;
-  const int log2_group = p.log2_block > 4 ? p.log2_block : 4;
-  auto start = [&](int b) { return static_cast<int64_t>(__ldg(p.qo_indptr + b) >> log2_group) + 2 * static_cast<int64_t>(b); };
+  const int log2_unit = p.log2_block > 4 ? p.log2_block : 4;
+  auto start = [&](int b) { return static_cast<int64_t>(__ldg(p.qo_indptr + b) >> log2_unit) + 2 * static_cast<int64_t>(b); };
   const int b = warp_owner(p.B, lane, slot, start);
   const Request r = request_of(p, b);
   const int64_t t0 = r.t0;
   const int held = r.held, begin = held - r.tokens;          // the first new position
-  const int64_t g0 = (begin >> log2_group) + (slot - start(b));
-  if (!r.sound || r.tokens == 0 || slot < start(b) || g0 << log2_group >= held) return;   // an idle slot
-  const int base = static_cast<int>(g0) << log2_group;
+  const int64_t g0 = (begin >> log2_unit) + (slot - start(b));
+  if (!r.sound || r.tokens == 0 || slot < start(b) || g0 << log2_unit >= held) return;    // an idle slot
+  const int base = static_cast<int>(g0) << log2_unit, end = base + (1 << log2_unit);
+  const int lo = begin > base ? begin : base, hi = held < end ? held : end;      // its new positions
 
-  const Columns col = columns_of<D>(lane % kPieces, is_k, p.half_rot);
-  const int rr = lane / kPieces;
   const int64_t idx0 = __ldg(p.pages.indptr + b);
   const int ps_mask = (1 << p.pages.log2_page) - 1;
-  const uint16_t* src = is_k ? p.k + h * p.k_head + col.c0 : p.v + h * p.v_head + col.c0;
-  const int64_t src_tok = is_k ? p.k_tok : p.v_tok;
-  uint8_t* cache = (is_k ? p.k_cache : p.v_cache) + h * p.head_pitch;
-  float* scales = (is_k ? p.ks : p.vs) + h * p.sc_head;
-  auto page_at = [&](int pos) -> int64_t {   // -1: outside the cache
-    const int64_t page = __ldg(p.pages.indices + idx0 + (pos >> p.pages.log2_page));
+  uint8_t* cache = is_k ? p.k_cache : p.v_cache;
+  float* scales = is_k ? p.ks : p.vs;
+  auto page_at = [&](int pos) -> int {      // -1: outside the cache
+    const int page = __ldg(p.pages.indices + idx0 + (pos >> p.pages.log2_page));
     return page >= 0 && page < p.n_pages ? page : -1;
   };
-  auto scale_at = [&](int64_t page, int pos) { return scales + page * p.sc_page + ((pos & ps_mask) >> p.log2_block) * p.sc_block; };
-  // the block that the new positions continue, if it is in this unit: its scale
-  const int joined = begin & ~(bs - 1);      // its first position
-  const bool continues = joined < begin && joined >= base && joined < base + (1 << log2_group);
-  float before = 0.f;
-  if (continues) {
-    const int64_t page = page_at(joined);
-    if (page >= 0) before = *scale_at(page, joined);
-  }
+  // a block and head a thread: where its scale is, and the scale where earlier positions have one
+  const int n_scales = ((hi - 1 - base) / bs + 1) * heads;
+  auto scale_of = [&](int i, bool* continued) -> float* {
+    const int at = base + i / heads * bs;
+    const int pos = at > lo ? at : lo;      // the block's first new position
+    *continued = at < begin;
+    if (pos >= hi || at + bs <= lo) return nullptr;
+    const int page = page_at(pos);
+    if (page < 0) return nullptr;
+    return scales + page * p.sc_page + ((pos & ps_mask) >> p.log2_block) * p.sc_block + (first_head + i % heads) * p.sc_head;
+  };
+  for (int i = tid; i < n_scales; i += kThreads) s_top[i / heads][i % heads] = 0;
+  if (tid < heads) s_grew[tid] = false;
+  __syncthreads();
 
-  // ---- a tile's rows, rotated: x, and which of them are there
-  float x[kSteps][16];
-  uint32_t there = 0;
-  auto load = [&](int row0) {
-    uint4 w[kSteps][2];
-    there = 0;
+  // ---- the largest value of each block and head.  A thread has two words of eight columns of a
+  // head; the block goes over the rows `at_once` at a time, a thread `kBatch` rows in flight.
+  const int row_threads = heads * kPieces, at_once = kThreads / row_threads;
+  const int tg = tid / row_threads, hl = tid / kPieces - tg * heads, piece = tid % kPieces;
+  const int h = first_head + hl;
+  const bool active = tg < at_once;
+  const Columns col = columns_of<D>(piece, is_k, p.half_rot);
+  const int64_t src_tok = is_k ? p.k_tok : p.v_tok;
+  const uint16_t* src = (is_k ? p.k + h * p.k_head : p.v + h * p.v_head) + col.c0 + (t0 - begin) * src_tok;
+  constexpr int kBatch = 2;
+  const bool once = lo + at_once * kBatch >= hi;         // one batch: its words stay
+  uint4 w[kBatch][2];
+  int angle[kBatch];
+  auto fetch = [&](int row0) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int row = row0 + s * kRows + rr;
-      const int64_t t = t0 + row - begin;
-      if (row >= begin && row < held) {
-        there |= 1u << s;
-        w[s][0] = *reinterpret_cast<const uint4*>(src + t * src_tok);
-        w[s][1] = *reinterpret_cast<const uint4*>(src + t * src_tok + col.half);
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = row0 + i * at_once;
+      if (active && row < hi) {
+        w[i][0] = *reinterpret_cast<const uint4*>(src + row * src_tok);
+        w[i][1] = *reinterpret_cast<const uint4*>(src + row * src_tok + col.half);
+        angle[i] = col.rot ? __ldg(p.positions + t0 + row - begin) : -1;
       } else {
-        w[s][0] = w[s][1] = make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      widen8(w[s][0], x[s]);
-      widen8(w[s][1], x[s] + 8);
-      if (col.rot && there >> s & 1) {
-        const int64_t pos = __ldg(p.positions + t0 + row0 + s * kRows + rr - begin);
-        if (pos >= 0 && pos < p.max_pos) {
-          Angles a;
-          load_angles<kNeox>(p, pos, col.piece, &a);
-          turn<kNeox>(x[s], a);
-        } else {
-          there &= ~(1u << s);               // these columns stay unwritten
-        }
+        w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+        angle[i] = -1;
       }
     }
   };
-  const int tiles = 1 << (log2_group - 4);
-  auto has_new = [&](int tile) { return base + tile * kTile < held && base + (tile + 1) * kTile > begin; };
-  float top[kSteps];                         // of the lane's row's block, in each step
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) top[s] = 0.f;
-  int loaded = -1, last_tile = -1;
-  for (int tile = wi; tile < tiles; tile += uw) {
-    if (!has_new(tile)) continue;
-    load(base + tile * kTile);
-    loaded = last_tile = tile;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      if (there >> s & 1)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = fabsf(x[s][i]);
-          top[s] = fmaxf(top[s], a < INFINITY ? a : 0.f);     // (a NaN is not either)
-        }
-  }
-  const int lanes = bs >= kRows ? 32 : bs * kPieces;          // lanes whose rows share a block
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-    for (int d = 1; d < lanes; d <<= 1) top[s] = fmaxf(top[s], __shfl_xor_sync(0xffffffffu, top[s], d));
-#pragma unroll
-  for (int d = 1; d < kSteps; d <<= 1)
-    if (bs >= 2 * d * kRows) {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-        if ((s & d) == 0) top[s] = top[s + d] = fmaxf(top[s], top[s + d]);
+  // a rotary position outside the table: the row's rotated columns stay unwritten
+  auto known = [&](int i) { return !col.rot || (angle[i] >= 0 && angle[i] < p.max_pos); };
+  auto values = [&](int i, float* x) {
+    widen8(w[i][0], x);
+    widen8(w[i][1], x + 8);
+    if (col.rot && known(i)) {
+      Angles a;
+      load_angles<kNeox>(p, angle[i], piece, &a);
+      turn<kNeox>(x, a);
     }
-  if (uw > 1) {
-    if (lane == 0) s_top[warp] = top[0];
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / uw), "r"(32 * uw) : "memory");
-    float all = 0.f;
-    for (int w = 0; w < uw; ++w) all = fmaxf(all, s_top[(warp & ~(uw - 1)) + w]);
+  };
+  float top = 0.f;
+#pragma unroll 1
+  for (int row0 = lo + tg; row0 - tg < hi; row0 += at_once * kBatch) {
+    fetch(row0);
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) top[s] = all;
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = row0 + (kBatch + i) * at_once;
+      if (active && row < hi) {             // the next batch's words into L2 meanwhile
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + row * src_tok));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + row * src_tok + col.half));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      float x[16], most = 0.f;
+      values(i, x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(x[k]));     // (passes a NaN over)
+      if (most == INFINITY) {               // the largest that is finite
+        most = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
+      }
+      if (!known(i)) most = 0.f;
+      if (bs >= kUnit) {
+        top = fmaxf(top, most);
+      } else if (most > 0.f) {
+        atomicMax(&s_top[(row0 + i * at_once - base) >> p.log2_block][hl], __float_as_uint(most));
+      }
+    }
   }
-  __syncwarp();                              // every lane has read the old scale
+  if (bs >= kUnit) {
+#pragma unroll
+    for (int d = 1; d < kPieces; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (active && piece == 0 && top > 0.f) atomicMax(&s_top[0][hl], __float_as_uint(top));
+  }
+  __syncthreads();
 
-  // ---- codes, scales, and the rotated keys in bf16
-  float grown = 0.f;                         // the continued block's scale
-  for (int tile = last_tile; tile >= 0; tile -= uw) {
-    if (!has_new(tile)) break;
-    if (tile != loaded) load(base + tile * kTile);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int row = base + tile * kTile + s * kRows + rr;
-      const int block = row & ~(bs - 1);
-      const bool continued = continues && block == joined;
-      const float fit = power_for(top[s]);
-      const float scale = continued && before >= fit ? before : fit;
-      if (row < begin || row >= held) continue;
-      const int64_t t = t0 + row - begin;
-      if (is_k && p.k_out && there >> s & 1) {
-        uint16_t* dst = p.k_out + t * p.ko_tok + h * p.ko_head + col.c0;
-        *reinterpret_cast<uint4*>(dst) = round8(x[s]);
-        *reinterpret_cast<uint4*>(dst + col.half) = round8(x[s] + 8);
+  // ---- the scales
+  for (int i = tid; i < n_scales; i += kThreads) {
+    bool continued;
+    float* at = scale_of(i, &continued);
+    const float fit = power_for(__uint_as_float(s_top[i / heads][i % heads]));
+    float scale = fit;
+    if (at) {
+      const float old = continued ? *at : 0.f;
+      if (continued && old >= fit) {
+        scale = old;
+      } else if (continued && fit > old) {
+        s_grew[i % heads] = true;
+        s_ratio[i % heads] = __fdiv_rn(old, fit);
       }
-      const int64_t page = page_at(row);
+      *at = scale;
+    }
+    s_scale[i / heads][i % heads] = scale;
+  }
+  __syncthreads();
+
+  // ---- codes, and the rotated keys in bf16: the words once more (from L2), or still there
+#pragma unroll 1
+  for (int row0 = lo + tg; row0 - tg < hi; row0 += at_once * kBatch) {
+    if (!once) fetch(row0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = row0 + i * at_once;
+      if (!active || row >= hi) continue;
+      const bool put = known(i);
+      float x[16];
+      values(i, x);
+      if (is_k && p.k_out && put) {
+        uint16_t* dst = p.k_out + (t0 + row - begin) * p.ko_tok + h * p.ko_head + col.c0;
+        *reinterpret_cast<uint4*>(dst) = round8(x);
+        *reinterpret_cast<uint4*>(dst + col.half) = round8(x + 8);
+      }
+      const int page = page_at(row);
       if (page < 0) {
-        if (lane % kPieces == 0) atomicOr(p.err, kErrBadRowId);
-        continue;
+        if (piece == 0) atomicOr(p.err, kErrBadRowId);
+      } else if (!put) {
+        if (piece == 0 && h == 0) atomicOr(p.err, kErrBadIndex);
+      } else {
+        uint8_t* dst = cache + page * p.page_pitch + (row & ps_mask) * p.slot_pitch + h * p.head_pitch + col.c0;
+        const float scale = s_scale[bs >= kUnit ? 0 : (row - base) >> p.log2_block][hl], inv = exact_reciprocal(scale);
+        *reinterpret_cast<uint2*>(dst) = quantise8(x, scale, inv);
+        *reinterpret_cast<uint2*>(dst + col.half) = quantise8(x + 8, scale, inv);
       }
-      if (is_k && h == 0 && col.rot && col.piece == 0 && !(there >> s & 1)) atomicOr(p.err, kErrBadIndex);
-      if (there >> s & 1) {
-        uint8_t* dst = cache + page * p.page_pitch + (row & ps_mask) * p.slot_pitch + col.c0;
-        const Quotient d(scale);
-        *reinterpret_cast<uint2*>(dst) = quantise8(x[s], d);
-        *reinterpret_cast<uint2*>(dst + col.half) = quantise8(x[s] + 8, d);
-      }
-      // the block's first new row writes its scale
-      if (lane % kPieces == 0 && (row == block || row == begin)) *scale_at(page, row) = scale;
     }
   }
+
   // ---- earlier codes of the continued block, where its scale grew
-  if (!continues) return;
-  {
-    // the block's rows share a tile or the whole unit: the lane's own step has its maximum
-    float mine = 0.f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int row = (bs > kTile ? base : joined & ~(kTile - 1)) + s * kRows + rr;
-      if (bs > kTile || (row & ~(bs - 1)) == joined) mine = fmaxf(mine, top[s]);
-    }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, d));
-    grown = power_for(mine);
-  }
-  if (!(grown > before)) return;
-  const float ratio = __fdiv_rn(before, grown);
-  for (int row = (joined & ~(kTile - 1)) + wi * kTile + rr; row < begin; row += kRows) {
-    // (a warp's rows: its tiles, kRows at a time)
-    if (uw > 1 && ((row - base) / kTile) % uw != wi) continue;
-    if (row < joined) continue;
-    const int64_t page = page_at(row);
+  const int joined = begin & ~(bs - 1);      // its first position
+  if (joined >= begin || joined < base || joined >= end || !active || !s_grew[hl]) return;
+  const float ratio = s_ratio[hl];
+  for (int row = joined + tg; row < begin; row += at_once) {
+    const int page = page_at(row);
     if (page < 0) continue;
-    uint4* at = reinterpret_cast<uint4*>(cache + page * p.page_pitch + (row & ps_mask) * p.slot_pitch + 16 * (lane % kPieces));
-    uint4 w = *at;
-    uint32_t* c = reinterpret_cast<uint32_t*>(&w);
+    uint4* at = reinterpret_cast<uint4*>(cache + page * p.page_pitch + (row & ps_mask) * p.slot_pitch + h * p.head_pitch + 16 * piece);
+    uint4 codes = *at;
+    uint32_t* c = reinterpret_cast<uint32_t*>(&codes);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = e4m3x2_to_f16x2(c[i]), hi = e4m3x2_to_f16x2(c[i] >> 16);
-      const __half2 l2 = *reinterpret_cast<const __half2*>(&lo), h2 = *reinterpret_cast<const __half2*>(&hi);
-      const float2 a = __half22float2(l2), e = __half22float2(h2);
+      const uint32_t lo2 = e4m3x2_to_f16x2(c[i]), hi2 = e4m3x2_to_f16x2(c[i] >> 16);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
+      const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
       const uint32_t low = f32x2_to_e4m3x2(a.y * ratio, a.x * ratio), high = f32x2_to_e4m3x2(e.y * ratio, e.x * ratio);
       c[i] = low | (high << 16);
     }
-    *at = w;
+    *at = codes;
   }
 }
 
 template <int D, bool kNeox>
 int launch(BlockAppendParams& p, int sms, cudaStream_t s) {
   constexpr int kRows = 32 / (D / 16);
-  // a warp a tile of a block where requests bring that many tokens, else one that walks them
-  const int tiles = p.log2_block > 4 ? 1 << (p.log2_block - 4) : 1;
-  p.unit_warps = p.n_tok >= 16 * static_cast<int64_t>(p.B) ? tiles : 1;
-  const int group = p.log2_block > 4 ? p.log2_block : 4;
-  const int64_t slots = (p.n_tok >> group) + 2 * static_cast<int64_t>(p.B);
-  const int64_t units = slots * 2 * p.Hk;
-  const int64_t kv_ctas = (units * p.unit_warps + kWarps - 1) / kWarps;
-  // query heads a warp: as many as leave every SM some warps
+  const int unit = p.log2_block > 4 ? p.log2_block : 4;
+  p.part_heads = 32 / (D / 16);            // a warp a row: 1 KB of neighbours in a token
+  if (p.part_heads > p.Hk) p.part_heads = p.Hk;
+  p.parts = 2 * ((p.Hk + p.part_heads - 1) / p.part_heads);
+  const int64_t kv_ctas = ((p.n_tok >> unit) + 2 * static_cast<int64_t>(p.B)) * p.parts;
+  // query heads a warp: the warps of one wave (24 a SM) take all of them where that is up to 4 each
   const int64_t groups = (p.n_tok + kRows - 1) / kRows;
   p.strip = 1;
-  while (p.strip < 8 && groups * (p.Hq / (2 * p.strip)) >= static_cast<int64_t>(sms) * 16) p.strip *= 2;
+  while (p.strip < kMostStrip && p.strip < p.Hq && groups * ((p.Hq + p.strip - 1) / p.strip) > static_cast<int64_t>(sms) * 24) p.strip *= 2;
   const int64_t q_items = groups * ((p.Hq + p.strip - 1) / p.strip);
   const int64_t q_ctas = (q_items + kWarps - 1) / kWarps;
   const int64_t look_ctas = (p.B + kThreads - 1) / kThreads;
   const int64_t ctas = kv_ctas + q_ctas + look_ctas;
-  if (units > 0x7FFFFFF0 || ctas > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
-  p.kv_slots = static_cast<int>(slots);
+  if (ctas > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
   p.kv_ctas = static_cast<unsigned>(kv_ctas);
   p.q_ctas = static_cast<unsigned>(q_ctas);
   gqa_block_append_kernel<D, kNeox><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
