@@ -836,7 +836,11 @@ cudaError_t launch(const BlockDecodeParams& p, int sms, cudaStream_t s) {
 }
 cudaError_t launch(const BlockDecodeParams& p, int64_t D, int sms, cudaStream_t s) {
   if (D == 128) return launch<128, 1>(p, sms, s);
-  return unit_heads(D, p.Hk) == 2 ? launch<64, 2>(p, sms, s) : launch<64, 1>(p, sms, s);
+  // Pairs halve the units, which costs where caches lie in L2: one head each where the page list has
+  // room for no more than 32 MB (37 requests of up to 4,089 positions, four heads: 11.5 us alone,
+  // 13.0 in pairs; 64 of 16,384, two heads: 77 and 62).
+  const bool small = (p.pages.n_idx << p.pages.log2_page) * p.Hk * 2 * D <= 32 << 20;
+  return unit_heads(D, p.Hk) == 2 && !small ? launch<64, 2>(p, sms, s) : launch<64, 1>(p, sms, s);
 }
 
 }  // namespace

@@ -80,7 +80,14 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
   __shared__ Sums s_warp[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps_mask = (1 << p.log2_page) - 1;
-  const int64_t held = p.free_count ? __ldcg(p.free_count) : 0;
+  const int32_t held = p.free_count ? __ldcg(p.free_count) : 0;
+  // the count may be written in place: by the block that is the last to have read it, at its end
+  bool writes = gridDim.x == 1;
+  if (p.free_count_out && gridDim.x > 1 && tid == 0) {
+    int one;                                 // 1, which waits for the read
+    asm volatile("and.b32 %0, %1, 0;\n\tadd.s32 %0, %0, 1;" : "=r"(one) : "r"(held));
+    writes = atomicAdd(p.err + 1, one) == static_cast<int>(gridDim.x) - 1;
+  }
   const int64_t n_free = held >= 0 && held <= p.n_pool ? held : 0;
 
   Sums run = {};
@@ -189,18 +196,9 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
       }
     }
   }
-  // the count changes once every block has read it
-  if (p.free_count_out) {
-    __syncthreads();
-    if (tid == 0) {
-      bool write = true;
-      if (gridDim.x > 1) {
-        __threadfence();
-        write = atomicAdd(p.err + 1, 1) == static_cast<int>(gridDim.x) - 1;
-        if (write) p.err[1] = 0;             // as it was found, for the next call
-      }
-      if (write) *p.free_count_out = static_cast<int32_t>(held - (run.taken < n_free ? run.taken : n_free));
-    }
+  if (p.free_count_out && tid == 0 && writes) {
+    if (gridDim.x > 1) p.err[1] = 0;         // as it was found, for the next call
+    *p.free_count_out = held - static_cast<int32_t>(run.taken < n_free ? run.taken : n_free);
   }
 }
 
@@ -292,7 +290,7 @@ extern "C" int mla_build_page_table(const mla_tensor_t* seq_lens, const mla_tens
   }
   const int64_t longest = p.n_idx > p.n_tok ? p.n_idx : p.n_tok;
   int64_t blocks = (longest + kThreads * kEach - 1) / (kThreads * kEach);
-  if (blocks > 2 * sms) blocks = 2 * sms;
+  if (blocks > 4 * sms) blocks = 4 * sms;
   if (blocks < 1) blocks = 1;
   page_table_kernel<<<static_cast<unsigned>(blocks), kThreads, smem, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
