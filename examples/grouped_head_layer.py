@@ -2,9 +2,12 @@
 as a serving loop runs it: prompts of different lengths packed into one call, then one new
 token a request at a time, over a paged cache.
 
-    python examples/grouped_head_layer.py [--fp8]
+    python examples/grouped_head_layer.py [--fp8 | --blocks]
 
-Each step of the loop is checked against the same layer run over the whole sequences at once.
+With --blocks the cache has a scale for each block of positions and head, the page tables are
+built on the GPU, later prompts run behind their cached prefix, and several new tokens of a
+request (drafts) are attended at once.  Each step of the loop is checked against the same layer
+run over the whole sequences at once.
 """
 import argparse
 import os
@@ -123,8 +126,86 @@ def run(fp8=False, lens=(37, 400, 1, 129), steps=70, device="cuda"):
     return worst
 
 
+class BlockScaledLayer(GroupedHeadLayer):
+    """The layer over an e4m3 cache with a scale for each `block` positions and head.  Requests'
+    lengths, page tables and the stack of free pages live on the GPU."""
+
+    def __init__(self, requests, width=1024, q_heads=16, kv_heads=4, dim=128, page=64, pages=256, block=16,
+                 max_new=8, **kw):
+        super().__init__(width, q_heads, kv_heads, dim, page, pages, fp8=True, **kw)
+        ints = lambda *shape, fill=0: torch.full(shape, fill, dtype=torch.int32, device=self.device)
+        scales = (pages, page // block, kv_heads)
+        self.k_scale, self.v_scale = (torch.zeros(scales, device=self.device) for _ in range(2))
+        self.max_new, self.seq_lens = max_new, ints(requests)
+        self.block_table, self.kv_indices = ints(requests, pages, fill=-1), ints(pages)
+        self.free_pages = torch.tensor(self.free, dtype=torch.int32, device=self.device)
+        self.free_count = ints(1, fill=pages)
+        self.qo_indptr, self.key_indptr, self.kv_indptr = (ints(requests + 1) for _ in range(3))
+        self.last = ints(requests)
+        self.error_word = ints(2)
+        self.workspace = pm.make_gqa_block_decode_workspace(q_heads, kv_heads, dim, max_new, self.device)
+
+    def forward(self, xs):
+        """The next tokens of every request: xs[b] (T_b, width), T_b >= 0.  Returns o of all of
+        them (sum T, heads, dim)."""
+        new = torch.tensor([x.shape[0] for x in xs], dtype=torch.int32, device=self.device)
+        t, d = sum(x.shape[0] for x in xs), self.dim
+        self.seq_lens += new
+        positions, slots = (torch.empty(t, dtype=torch.int32, device=self.device) for _ in range(2))
+        pm.mla_build_page_table(self.seq_lens, new, self.block_table, self.page, self.qo_indptr, self.key_indptr,
+                                self.kv_indptr, self.kv_indices, self.last, self.error_word, positions=positions,
+                                slot_mapping=slots, free_pages=self.free_pages, free_count=self.free_count,
+                                free_count_out=self.free_count)
+        qkv = torch.cat(xs) @ self.w
+        q, k, v = (y.unflatten(1, (-1, d)) for y in qkv.split([self.q_heads * d, self.kv_heads * d, self.kv_heads * d], 1))
+        lists = self.kv_indptr, self.kv_indices, self.last
+        pm.mla_gqa_block_append(q, k, v, positions, self.cos_sin, 1, self.qo_indptr, *lists, q, self.k_cache,
+                                self.v_cache, self.k_scale, self.v_scale, self.error_word, k_out=k)
+        o = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        if max(x.shape[0] for x in xs) <= self.max_new:
+            pm.mla_gqa_block_decode(q, self.k_cache, self.v_cache, self.k_scale, self.v_scale, o, self.qo_indptr,
+                                    *lists, self.max_new, d ** -0.5, workspace=self.workspace)
+            return o
+        rows = int(self.key_indptr[-1])            # prompts: the cached positions as rows, the new ones behind
+        k_rows, v_rows = (torch.empty(rows, self.kv_heads, d, dtype=q.dtype, device=self.device) for _ in range(2))
+        pm.mla_gqa_block_gather(self.k_cache, self.v_cache, self.k_scale, self.v_scale, *lists, self.key_indptr,
+                                k_rows, v_rows, self.error_word, qo_indptr=self.qo_indptr, k_new=k, v_new=v)
+        pm.mla_prompt_attention(q, k_rows, v_rows, o, self.qo_indptr, self.key_indptr, d ** -0.5, self.error_word)
+        return o
+
+    def check(self):
+        status = pm.mla_check_error(self.workspace)
+        bits = int(self.error_word[0])
+        if status or bits:
+            raise RuntimeError(f"{pm.mla_status_string(status)}, error bits {bits}")
+
+
+def run_blocks(lens=(37, 400, 1, 129), steps=20, device="cuda"):
+    """The same for the block-scaled cache: a prompt in two parts, then steps of one to five
+    tokens a request (none, now and then)."""
+    width = 1024
+    counts = [[(i * 7 + 3 * b) % 6 for b in range(len(lens))] for i in range(steps)]
+    more = [n // 2 + 20 for n in lens]
+    total = [n + m + sum(c[b] for c in counts) for b, (n, m) in enumerate(zip(lens, more))]
+    g = torch.Generator(device=device).manual_seed(1)
+    xs = [torch.randn(n, width, generator=g, device=device).bfloat16() for n in total]
+    layer = BlockScaledLayer(len(lens), width, device=device)
+    whole = GroupedHeadLayer(width, device=device).prompt(xs).float()
+    at, worst = [0] * len(lens), 0.0
+    starts = [sum(total[:b]) for b in range(len(lens))]
+    for new in [lens, more] + counts:
+        o = layer.forward([x[a:a + n] for x, a, n in zip(xs, at, new)]).float()
+        want = torch.cat([whole[s + a:s + a + n] for s, a, n in zip(starts, at, new)])
+        at = [a + n for a, n in zip(at, new)]
+        if o.numel():
+            worst = max(worst, (o - want).abs().max().item())
+    layer.check()
+    return worst
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--fp8", action="store_true", help="an e4m3 cache")
-    fp8 = ap.parse_args().fp8
-    print(f"largest difference to the whole prompt: {run(fp8):.4f}")
+    ap.add_argument("--blocks", action="store_true", help="an e4m3 cache with a scale for each block and head")
+    args = ap.parse_args()
+    print(f"largest difference to the whole prompt: {run_blocks() if args.blocks else run(args.fp8):.4f}")
