@@ -24,9 +24,10 @@
 // what falls under f16's range is below 2^-38 of the largest.
 // 64-wide heads are taken in pairs, 128 bytes of a slot at a time: alone they use half of every
 // line that DRAM delivers (64 requests of 32,768 positions, two heads: 170 us alone, 103 paired).
-// A unit has at most 16 rows of each head; more run in units of 16 that read the cache again
-// (32 rows fit the registers with nothing beside them: 64 requests of 2,048 to 65,536 positions,
-// four tokens of eight heads, 209 us in one unit, 186 in two).
+// A unit has at most 16 rows of each head.  More go to the kernel of mla_gqa_block_wide.cu, which feeds
+// the codes to tcgen05 (64 requests of 2,048 to 65,536 positions, four tokens of eight heads: 114
+// us), or, where the cache's layout is none for it, run here in units of 16 that read the cache again
+// (187; 32 rows in one unit fit the registers with nothing beside them: 209).
 //
 // Also tried: e4m3 MMAs (m16n8k32) with q and P as two codes each, whose operands the compiler
 // converts to f16 all the same (102 us for 64 requests of 16,384 positions, two KV heads; 91 as
@@ -41,8 +42,8 @@
 
 #include "../../include/paged_mla.h"
 #include "mla_gqa_check.h"
+#include "mla_gqa_block_decode.cuh"
 #include "mla_gqa_decode_common.cuh"
-#include "mla_gqa_pages.cuh"
 #include "ptx.cuh"
 
 namespace {
@@ -52,42 +53,7 @@ using namespace pmla;
 constexpr int64_t kMaxQ = 64;        // as mla_decode
 constexpr int kSmWarps = 8;          // warps a SM, in two CTAs or in one
 constexpr float kShift = 14.f;       // weights carry 2^14, in the sum too
-constexpr float kLeast = 0x1p-60f;   // smaller scales of values count as this
 
-struct BlockDecodeParams {
-  const uint16_t* q;
-  int64_t q_tok, q_head;
-  const uint8_t *k, *v;
-  int64_t page_pitch, slot_pitch, head_pitch;
-  const float *ks, *vs;
-  int64_t sc_page, sc_block, sc_head;   // strides in elements, both
-  int log2_block;
-  int64_t n_pages;
-  PageList pages;
-  const int32_t* qo_indptr;
-  int64_t n_tok;
-  int max_q;
-  float sm_scale;
-  void* o;
-  int o_f32;
-  int64_t o_tok, o_head;
-  float* lse;
-  int B, Hq, Hk, G;
-  int* err;
-  int* counters;                     // one a CTA: the unit that leaves its span's end
-  float* slots;                      // two a CTA: m[R], l[R], o[R][D], R the rows of a unit
-};
-
-__device__ __forceinline__ float lg2_approx(float x) {
-  float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -105,6 +71,8 @@ struct BlockShape {
   static constexpr int D = D_, NT = NT_, HP = HP_;
   static constexpr int CT = NT * HP;                       // column tiles of 8 rows
   static constexpr int kWarps = W_, kThreads = 32 * W_;
+  static constexpr int kJoinWarps = kWarps, kJoinThreads = kThreads;
+  __device__ static __forceinline__ void join_sync() { __syncthreads(); }
   static constexpr int kCtasPerSm = kSmWarps / W_;
   static constexpr int kMaxCtas = kMaxSms * kCtasPerSm;    // a unit has at most one piece a CTA
   static constexpr int kRow = D * HP;                      // bytes of a K or V row
@@ -134,66 +102,6 @@ struct BlockShape {
   // 256 requests of 500 to 4,000: 170 us with 55 KB's time, 164 with 100, 159 with 150, 167 with 250.
   static constexpr int kUnitCost = (W_ == 8 ? 350000 : 150000) / kTileBytes, kLeastCost = 55000 / kTileBytes;
   static constexpr int kLeastPiece = 55000 / kTileBytes;   // of a cut unit
-};
-
-// The line of work, of all requests or of those before one: tiles of all units, and units.
-struct Line {
-  int64_t tiles, units;
-  __device__ Line operator+(const Line& o) const { return {tiles + o.tiles, units + o.units}; }
-  __device__ Line operator-(const Line& o) const { return {tiles - o.tiles, units - o.units}; }
-  __device__ int64_t length(int cost) const { return tiles + cost * units; }
-};
-__device__ __forceinline__ Line shfl_up(const Line& x, int d) {
-  return {__shfl_up_sync(0xffffffffu, x.tiles, d), __shfl_up_sync(0xffffffffu, x.units, d)};
-}
-
-// Where a span's border, x tiles into a unit of n, cuts it: pieces of fewer than kLeastPiece
-// tiles go to the neighbouring span, so units of fewer than twice as many stay whole.
-template <class S>
-__device__ __forceinline__ int snap(int64_t x, int n) {
-  if (x >= n) return n;
-  if (x < S::kLeastPiece) return 0;
-  return n - x < S::kLeastPiece ? n : static_cast<int>(x);
-}
-
-// A request's positions and new tokens; none where its lists make no sense.
-struct Request {
-  int len, tokens;
-};
-__device__ __forceinline__ Request request_of(const BlockDecodeParams& p, int b, bool flag) {
-  const int64_t s = __ldg(p.qo_indptr + b), e = __ldg(p.qo_indptr + b + 1);
-  int len = p.pages.positions(b);
-  bool sound = len >= 0;
-  if (!sound) len = 0;
-  int tokens = 0;
-  if (s >= 0 && e >= s && e <= p.n_tok && e - s <= p.max_q) tokens = static_cast<int>(e - s);
-  else sound = false;
-  if (!sound && flag) atomicOr(p.err, kErrBadIndptr);
-  return {len, tokens};
-}
-template <class S>
-__device__ __forceinline__ int chunks_of(const BlockDecodeParams& p, int tokens) {
-  return (tokens * p.G + S::kHeads - 1) / S::kHeads;
-}
-// The request's part of the line.
-template <class S>
-__device__ __forceinline__ Line request_line(const BlockDecodeParams& p, const Request& r) {
-  const int64_t units = r.len > 0 ? chunks_of<S>(p, r.tokens) * ((p.Hk + S::HP - 1) / S::HP) : 0;
-  return {(r.len + S::kTile - 1) / S::kTile * units, units};
-}
-
-__device__ __forceinline__ void store_o(const BlockDecodeParams& p, int64_t tok, int h, int d, float x) {
-  const int64_t at = tok * p.o_tok + h * p.o_head + d;
-  if (p.o_f32) static_cast<float*>(p.o)[at] = x;
-  else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
-}
-
-// One piece of a unit.
-struct Piece {
-  Request r;
-  int64_t tok0, idx0;                // the request's first token and first page
-  int hk0, h0, nh;                   // first KV head; first row of the chunk, rows of a head
-  int t0, t1;                        // tiles
 };
 
 // q's rows in f16, scaled, into shared memory, their columns in the order in which K's
@@ -385,7 +293,7 @@ __device__ __forceinline__ void walk_tiles(const BlockDecodeParams& p, const Pie
         for (int k = 0; k < 2; ++k) {
           ksc[hp][mt][k] = scales[hp * kTile + 16 * mt + 8 * k + g];
           const float x = scales[(HP + hp) * kTile + 16 * mt + 8 * k + g];
-          const float y = x < kLeast ? kLeast : x;
+          const float y = x < kLeastScale ? kLeastScale : x;
           lvs[hp][mt][k] = lg2_approx(y);
           rvs[hp][mt][k] = rcp_approx(y);
         }
@@ -475,149 +383,21 @@ __device__ __forceinline__ void walk_tiles(const BlockDecodeParams& p, const Pie
 
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_kernel(const BlockDecodeParams p) {
-  constexpr int D = S::D, HP = S::HP, CT = S::CT, kTile = S::kTile, kHeads = S::kHeads, kRows = S::kRows;
-  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
+  constexpr int D = S::D, HP = S::HP, CT = S::CT, kRows = S::kRows, kWarps = S::kWarps, kThreads = S::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   float* s_m = reinterpret_cast<float*>(smem + S::kBuf);       // [warp][row]
   float* s_l = s_m + kWarps * kRows;
   float* s_sc = s_l + kWarps * kRows;                          // [row]
   uint8_t* s_q = reinterpret_cast<uint8_t*>(s_sc + kRows);     // [row][D], f16
-  __shared__ Line sh_scan[kWarps];
-  __shared__ int64_t sh_base;
-  __shared__ int sh_b, sh_last, sh_empty;
-  __shared__ Request sh_r;
-
+  __shared__ SpanShared<kWarps> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x;
-
-  // ---- the line: its length, this CTA's span, and the request its span starts in.  The
-  // first kThreads requests stay in registers, so that a batch of up to kThreads pays one round
-  // trip to memory here.
-  if (tid == 0) sh_empty = 0;
-  __syncthreads();
-  Line mine = {0, 0};
-  Request r0 = {0, 0};
-#pragma unroll 4
-  for (int b = tid; b < p.B; b += kThreads) {
-    const Request r = request_of(p, b, cta == 0);
-    if (b < kThreads) r0 = r;
-    mine = mine + request_line<S>(p, r);
-    if (r.len == 0 && b % gridDim.x == cta) sh_empty = 1;
-  }
-  const Line mine0 = request_line<S>(p, r0);
-  Line inc = mine0;
-#pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const Line o = shfl_up(inc, i);
-    if (lane >= i) inc = inc + o;
-  }
-  if (p.B > kThreads) {
-#pragma unroll
-    for (int i = 16; i; i >>= 1) {
-      mine.tiles += __shfl_xor_sync(0xffffffffu, mine.tiles, i);
-      mine.units += __shfl_xor_sync(0xffffffffu, mine.units, i);
-    }
-  } else if (lane == 31) {
-    mine = inc;
-  }
-  if (lane == 31) sh_scan[warp] = mine;
-  __syncthreads();
-  Line all = {0, 0}, before = {0, 0};
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before = before + sh_scan[w];
-    all = all + sh_scan[w];
-  }
-  // a unit's cost, less where CTAs have little to do: then cuts pay earlier
-  const int64_t share = quotient(all.tiles, 10 * static_cast<int64_t>(gridDim.x));
-  const int cost = static_cast<int>(share > S::kUnitCost ? S::kUnitCost : (share < S::kLeastCost ? S::kLeastCost : share));
-  const int64_t total = all.length(cost);
-  const int64_t span = quotient(total + gridDim.x - 1, gridDim.x);
-  const int64_t x_begin = cta * span;
-  const int64_t x_end = x_begin + span < total ? x_begin + span : total;
-  if (sh_empty)                                    // empty requests: o = 0, lse = -inf
-    for (int b = cta; b < p.B; b += gridDim.x) {
-      const Request r = request_of(p, b, false);
-      if (r.len != 0) continue;
-      const int64_t tok = __ldg(p.qo_indptr + b);
-      for (int e = tid; e < r.tokens * p.Hq * D; e += kThreads) {
-        const int h = e / D % p.Hq;
-        const int64_t at = tok + e / D / p.Hq;
-        store_o(p, at, h, e % D, 0.f);
-        if (e % D == 0 && p.lse) p.lse[at * p.Hq + h] = -INFINITY;
-      }
-    }
-  if (x_begin >= x_end) return;
-  if (p.B <= kThreads) {
-    const int64_t start = (before + inc - mine0).length(cost), n = mine0.length(cost);
-    if (n > 0 && x_begin >= start && x_begin < start + n) {
-      sh_b = tid;
-      sh_r = r0;
-      sh_base = start;
-    }
-    __syncthreads();
-  } else {
-    Line done = {0, 0};    // the line before this block of kThreads requests
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      const Request r = b < p.B ? request_of(p, b, false) : Request{0, 0};
-      const Line part = request_line<S>(p, r);
-      Line run = part;
-#pragma unroll
-      for (int i = 1; i < 32; i <<= 1) {
-        const Line o = shfl_up(run, i);
-        if (lane >= i) run = run + o;
-      }
-      __syncthreads();
-      if (lane == 31) sh_scan[warp] = run;
-      __syncthreads();
-      Line start = done + run - part;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) start = start + sh_scan[w];
-        done = done + sh_scan[w];
-      }
-      const int64_t at = start.length(cost), n = part.length(cost);
-      if (n > 0 && x_begin >= at && x_begin < at + n) {
-        sh_b = b;
-        sh_r = r;
-        sh_base = at;
-      }
-      if (done.length(cost) > x_begin) break;
-    }
-    __syncthreads();
-  }
-  int b = sh_b;
-  Request r = sh_r;
-  int64_t base = sh_base;              // the line position of request b
   const int g = lane >> 2, cq = lane & 3;
+  Span span;
+  if (!find_span<S>(p, &sh, &span)) return;
 
-  for (int64_t x = x_begin; x < x_end;) {
-    int64_t whole_r;
-    while (x >= base + (whole_r = request_line<S>(p, r).length(cost))) {      // the next request with work
-      base += whole_r;
-      ++b;
-      r = request_of(p, b, false);
-    }
-    const int n_tiles = (r.len + kTile - 1) / kTile;
-    const int64_t weight = n_tiles + cost;
-    const int ui = static_cast<int>(quotient(x - base, weight));
-    const int64_t u0 = base + ui * weight + cost;                  // the unit's first tile
+  for (int64_t x = span.begin; x < span.end;) {
     Piece u;
-    u.t0 = snap<S>(x_begin - u0, n_tiles);
-    u.t1 = snap<S>(x_end - u0, n_tiles);
-    x = u0 + n_tiles;
-    if (u.t0 >= u.t1) continue;                    // the neighbours' spans have all of it
-    const int rows = r.tokens * p.G, chunks = chunks_of<S>(p, r.tokens);
-    u.r = r;
-    u.hk0 = ui / chunks;
-    u.h0 = (ui - u.hk0 * chunks) * kHeads;
-    u.hk0 *= HP;
-    u.nh = rows - u.h0 < kHeads ? rows - u.h0 : kHeads;
-    u.tok0 = __ldg(p.qo_indptr + b);
-    u.idx0 = __ldg(p.pages.indptr + b);
-    const int live_rows = u.hk0 + HP <= p.Hk ? kRows : (p.Hk - u.hk0) * kHeads;    // rows from there on are nobody's
-
+    if (!next_piece<S>(p, span, &x, &u)) continue;
     float acc[CT][D / 16][4], m[CT][2], l[CT][2];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -638,7 +418,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[ct][i] += __shfl_xor_sync(0xffffffffu, l[ct][i], d);
         if (g == 0) {
-          s_m[warp * kRows + 8 * ct + 2 * cq + i] = m[ct][i];
+          s_m[warp * kRows + 8 * ct + 2 * cq + i] = m[ct][i] - kShift;
           s_l[warp * kRows + 8 * ct + 2 * cq + i] = l[ct][i];
         }
       }
@@ -653,25 +433,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
           *reinterpret_cast<float2*>(s_o + (warp * kRows + 8 * ct + 2 * cq + j) * D + 16 * i + 2 * g) =
               make_float2(acc[ct][i][j], acc[ct][i][j + 2]);
     __syncthreads();
-    const bool whole = u.t0 == 0 && u.t1 == n_tiles;
-    auto there = [&](int row) { return row < live_rows && (CT == 1 || row % kHeads < u.nh); };
-    // columns d .. d+3 of a row of the unit, and its lse
-    auto finish = [&](int row, int d, const float* oo, float mm, float ll) {
-      const int h = u.h0 + row % kHeads, of = h / p.G;
-      const int hq = (u.hk0 + row / kHeads) * p.G + h - of * p.G;
-      const int64_t tok = u.tok0 + of;
-      const bool none = ll == 0.f;
-      const float f = none ? 0.f : 1.f / ll;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) store_o(p, tok, hq, d + i, none ? 0.f : oo[i] * f);
-      if (d == 0 && p.lse)
-        p.lse[tok * p.Hq + hq] = none ? -INFINITY : (mm == -INFINITY ? 0.f : mm) * kLn2 + logf(ll) - kShift * kLn2;
-    };
-    const int used = CT == 1 ? u.nh : live_rows;             // rows to look at
-    float* slot = p.slots + (2 * static_cast<int64_t>(cta) + (u.t0 == 0 ? 1 : 0)) * S::kSlotFloats;
+    const bool whole = u.t0 == 0 && u.t1 == u.n_tiles;
+    const int used = HP == 1 ? u.nh : u.live_rows;           // rows to look at
+    float* slot = part_slot<S>(p, u);
     for (int e = 4 * tid; e < used * D; e += 4 * kThreads) {
       const int h = e / D, d = e - h * D;
-      if (!there(h)) continue;
+      if (!row_there<S>(u, h)) continue;
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * kRows + h]);
@@ -690,7 +457,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
         oo[3] += f * y.w;
       }
       if (whole) {
-        finish(h, d, oo, mm, ll);
+        finish_row<S, 4>(p, u, h, d, oo, mm, ll);
       } else {
         *reinterpret_cast<float4*>(slot + 2 * kRows + e) = make_float4(oo[0], oo[1], oo[2], oo[3]);
         if (d == 0) {
@@ -699,89 +466,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
         }
       }
     }
-    if (!whole) {
-      // ---- the last span to arrive joins the unit's pieces, in the spans' order
-      const int64_t first = quotient(u0 + S::kLeastPiece - 1, span);
-      const int64_t last = quotient(u0 + n_tiles - S::kLeastPiece, span);
-      __syncthreads();
-      if (tid == 0) {
-        int* c = p.counters + first;
-        __threadfence();                   // the CTA's part before its arrival
-        const int seen = atomicAdd(c, 1);
-        sh_last = seen == last - first;
-        if (sh_last) *c = 0;               // as it was found, for the next call
-        __threadfence();                   // the others' parts after theirs
-      }
-      __syncthreads();
-      if (sh_last) {
-        const int np = static_cast<int>(last - first) + 1;
-        float* s_f = reinterpret_cast<float*>(smem);         // [piece][row], over the rings
-        float* s_s = s_f + np * kRows;
-        // parts lie two slots apart, the first one a slot further on
-        const float* parts = p.slots + 2 * first * S::kSlotFloats;
-        for (int e = tid; e < np * kRows; e += kThreads) {
-          const int i = e / kRows, h = e - i * kRows;
-          const float* sl = parts + (2 * i + (i == 0 ? 1 : 0)) * S::kSlotFloats;
-          s_f[e] = there(h) ? __ldcg(sl + h) : 0.f;
-          s_s[e] = there(h) ? __ldcg(sl + kRows + h) : 0.f;
-        }
-        __syncthreads();
-        // a warp a row, lanes over pieces
-        for (int h = warp; h < used; h += kWarps) {
-          if (!there(h)) continue;
-          float mm = -INFINITY, ll = 0.f;
-          for (int i = lane; i < np; i += 32) mm = fmaxf(mm, s_f[i * kRows + h]);
-#pragma unroll
-          for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-          for (int i = lane; i < np; i += 32) {
-            const float mw = s_f[i * kRows + h];
-            const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - mm);
-            s_f[i * kRows + h] = f;
-            ll += f * s_s[i * kRows + h];
-          }
-#pragma unroll
-          for (int d = 16; d; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-          if (lane == 0) {
-            s_m[h] = mm;
-            s_l[h] = ll;
-          }
-        }
-        __syncthreads();
-        constexpr int kEach = 4 * kThreads;  // columns the threads take at once
-        for (int e0 = 4 * tid; e0 < used * D; e0 += 2 * kEach) {
-          const bool two = S::kTwo && e0 + kEach < used * D;
-          const int h = e0 / D, h2 = (e0 + kEach) / D;
-          float oo[8] = {};
-          for (int i0 = 0; i0 < np; i0 += S::kAhead) {       // all their loads in flight at once
-            float4 y[2 * S::kAhead];       // (the odd ones unused without a second word)
-#pragma unroll
-            for (int i = 0; i < S::kAhead; ++i)
-              if (i0 + i < np) {
-                const float* at = parts + (2 * (i0 + i) + (i0 + i == 0 ? 1 : 0)) * S::kSlotFloats + 2 * kRows + e0;
-                y[2 * i] = __ldcg(reinterpret_cast<const float4*>(at));
-                if (two) y[2 * i + 1] = __ldcg(reinterpret_cast<const float4*>(at + kEach));
-              }
-#pragma unroll
-            for (int i = 0; i < S::kAhead; ++i) {
-              if (i0 + i >= np) break;
-              const float f = s_f[(i0 + i) * kRows + h];
-              oo[0] += f * y[2 * i].x;
-              oo[1] += f * y[2 * i].y;
-              oo[2] += f * y[2 * i].z;
-              oo[3] += f * y[2 * i].w;
-              if (!two) continue;
-              const float f2 = s_f[(i0 + i) * kRows + h2];
-              oo[4] += f2 * y[2 * i + 1].x;
-              oo[5] += f2 * y[2 * i + 1].y;
-              oo[6] += f2 * y[2 * i + 1].z;
-              oo[7] += f2 * y[2 * i + 1].w;
-            }
-          }
-          if (there(h)) finish(h, e0 % D, oo, s_m[h], s_l[h]);
-          if (two && there(h2)) finish(h2, (e0 + kEach) % D, oo + 4, s_m[h2], s_l[h2]);
-        }
-      }
-    }
+    if (!whole) join_parts<S>(p, span, u, &sh, s_m, s_l, s_o);
     __syncthreads();                       // the rings are free for the next piece
   }
 }
@@ -835,6 +520,7 @@ cudaError_t launch(const BlockDecodeParams& p, int sms, cudaStream_t s) {
   return nt == 1 ? launch<D, 1, HP>(p, sms, s) : launch<D, 2, HP>(p, sms, s);
 }
 cudaError_t launch(const BlockDecodeParams& p, int64_t D, int sms, cudaStream_t s) {
+  if (block_wide_takes(p, D)) return launch_block_wide(p, D, sms, s);
   if (D == 128) return launch<128, 1>(p, sms, s);
   // Pairs halve the units, which costs where caches lie in L2: one head each where the page list has
   // room for no more than 32 MB (37 requests of up to 4,089 positions, four heads: 11.5 us alone,

@@ -203,9 +203,13 @@ def values(pages, b, cache, scale, n=None):
 # range it loses half of 2^-24, 2^-39 of the largest.
 WEIGHT = ref.F16
 LOST = 2.0 ** -39
+# With more than 16 rows a KV head the rounded weight counts at least 2^5 where it is largest and is
+# written as three e4m3 codes h + 2^-5 l + 2^-10 l', exact down to the last one's smallest step,
+# 2^-9 2^-10: half of it is 2^-25 of the largest.
+LOST_MANY = 2.0 ** -25
 
 
-def attend(pages, b, q, k_cache, v_cache, ks, vs, sm):
+def attend(pages, b, q, k_cache, v_cache, ks, vs, sm, least=LOST):
     """o, lse, mass and largest score of the newest q.shape[0] tokens of request b, fp64, and what
     their smallest weights can lose."""
     t, hq, d = q.shape
@@ -223,7 +227,7 @@ def attend(pages, b, q, k_cache, v_cache, ks, vs, sm):
         if n:
             s = torch.where(torch.arange(n, device=q.device) < limit[:, None], qq @ k[:, h].T * sm, -math.inf)
             w = torch.exp(s - lse.clamp_min(-1e300)[:, None]) * scale[:, h]
-            lost = LOST * w.amax(1, keepdim=True) * codes[h]
+            lost = least * w.amax(1, keepdim=True) * codes[h]
         else:
             lost = torch.zeros_like(o)
         out.append((o, lse, mass, big, lost))

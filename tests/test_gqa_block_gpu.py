@@ -363,12 +363,13 @@ class Decode:
                                      lse, ws, **kw)
         return o, lse, ws
 
-    def check(self, o, lse, what=""):
+    def check(self, o, lse, what="", least=blk.LOST):
         at = 0
         for b, t in enumerate(self.new):
             if t == 0:
                 continue
-            want = blk.attend(self.pages, b, self.q[at:at + t], self.kc, self.vc, self.ks, self.vs, self.sm)
+            want = blk.attend(self.pages, b, self.q[at:at + t], self.kc, self.vc, self.ks, self.vs, self.sm,
+                              least)
             blk.check(o[at:at + t], lse[at:at + t], want, self.pages.held[b], self.q.shape[2],
                       ref.F32 if o.dtype == torch.float32 else ref.BF16,
                       f"{what}, request {b}: {t} of {self.pages.held[b]}")
@@ -543,4 +544,112 @@ def test_decode_shares_a_workspace_with_the_plain_decode(pm):
     o2, lse2, _ = c.run(pm, ws=ws)
     pm.mla_gqa_decode(*args, workspace=ws)
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(first, args[3])
+    assert pm.mla_check_error(ws) == 0
+
+
+# More than 16 query rows a KV head (its own kernel where the cache's layout allows it).
+@pytest.mark.parametrize("held,new,Hq,Hk,D,ps,bs,layout", [
+    ([1, 0, 127, 128, 129, 255, 300], [1] * 7, 20, 1, 128, 8, 8, "nhd"),
+    ([700, 3, 64, 0], [3] * 4, 18, 3, 64, 8, 4, "nhd"),                # the last head has no partner
+    ([700, 3, 64], [3] * 3, 18, 3, 64, 16, 16, "hnd"),
+    ([700, 3], [2] * 2, 24, 2, 64, 16, 16, "shared"),
+    ([700, 3], [2] * 2, 24, 2, 128, 16, 16, "shared"),
+    ([4100, 17], [5, 2], 48, 4, 128, 1024, 128, "hnd"),
+    ([300], [64], 8, 1, 128, 256, 64, "nhd"),
+    ([300, 70], [64, 33], 4, 2, 64, 128, 128, "nhd"),
+    ([2001] * 5, [2] * 5, 40, 2, 128, 4, 4, "nhd"),
+    ([65001], [4], 16, 2, 128, 64, 64, "nhd"),
+    ([33001], [4], 16, 2, 64, 64, 64, "nhd"),
+    ([(i * 131) % 1200 for i in range(170)], [2] * 170, 40, 2, 128, 16, 16, "nhd"),
+    ([40001] + [i % 7 for i in range(199)], [1] * 200, 34, 2, 64, 32, 32, "nhd"),
+])
+def test_decode_of_many_rows(pm, held, new, Hq, Hk, D, ps, bs, layout):
+    c = Decode(held, new, Hq, Hk, D, ps, bs, layout, pad=2)
+    o, lse, ws = c.run(pm, torch.float32)
+    assert pm.mla_check_error(ws) == 0
+    c.check(o, lse, "", blk.LOST_MANY)
+    o2, lse2, _ = c.run(pm, torch.float32, ws=ws)
+    n = sum(new)
+    assert torch.equal(o[:n], o2[:n]) and torch.equal(lse[:n], lse2[:n])
+
+
+@pytest.mark.parametrize("rows", [4, 32])
+def test_decode_of_one_large_score_among_many_small(pm, rows):
+    """The first position has e^14 times the weight of each of 60,000 others, whose 4 % of the mass
+    (weights of 2^-20 of the largest) are all of the output that is not zero."""
+    c = Decode([60001], [1], rows, 1, 128, 64, 64)
+    page, slot = c.pages.where(0, 0, 60001)
+    for cache, code in ((c.kc, 0.0), (c.vc, 1.0)):
+        cache.view(torch.uint8)[page, slot] = torch.tensor(code, device=DEV).to(blk.F8).view(torch.uint8)
+    c.kc.view(torch.uint8)[page[0], slot[0]] = torch.tensor(20.0, device=DEV).to(blk.F8).view(torch.uint8)
+    c.vc.view(torch.uint8)[page[0], slot[0]] = 0
+    c.ks[page, slot // 64] = 2.0 ** -4
+    c.vs[page, slot // 64] = 1.0
+    c.q.fill_(1.0)
+    o, lse, ws = c.run(pm, torch.float32)
+    assert pm.mla_check_error(ws) == 0
+    want = 60000 / (60000 + math.exp(128 ** 0.5 * 20 / 16))
+    # each weight, 2^-20.4 of the largest: rounded to a multiple of 2^-24 (by 2^-25 at most)
+    assert 0.04 < want < 0.05 and ((o.double() - want).abs() / want).max().item() < 2.0 ** -25 * 2.0 ** 20.5 + 2.0 ** -10
+    c.check(o, lse, "", blk.LOST_MANY)
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(40, 2, 128), (36, 2, 64)])
+def test_decode_of_many_rows_reads_only_its_lists(pm, Hq, Hk, D):
+    """Poison behind the lists, infinite scales there, a page that is not in the cache, a list that
+    makes no sense: as with few rows."""
+    c = Decode([37, 300, 130], [1, 3, 2], Hq, Hk, D, 16, 16)
+    good, lse_good, ws = c.run(pm)
+    c.check(good, lse_good, "", blk.LOST_MANY)
+    c.ks.copy_(torch.where(c.ks.isnan(), math.inf, c.ks))
+    c.vs.copy_(torch.where(c.vs.isnan(), -math.inf, c.vs))
+    o, lse, _ = c.run(pm, ws=ws)
+    assert pm.mla_check_error(ws) == 0 and torch.equal(o, good) and torch.equal(lse, lse_good)
+    for wrong in (c.pages.pool, -1, 1 << 30):
+        keep = c.pages.indices
+        c.pages.indices = keep.clone()
+        c.pages.indices[1] = wrong             # request 0's second page: zeros
+        o, lse, _ = c.run(pm, ws=ws)
+        c.pages.indices = keep
+        assert pm.mla_check_error(ws) == 5
+        assert torch.equal(o[1:], good[1:]) and o.isfinite().all()
+        k, v = (blk.values(c.pages, 0, x, s).double() for x, s in ((c.kc, c.ks), (c.vc, c.vs)))
+        k[16:32] = 0
+        v[16:32] = 0
+        q = c.q[0].double().view(Hk, Hq // Hk, D)
+        p = torch.softmax(torch.einsum("hgd,nhd->hgn", q, k) * c.sm, -1)
+        want = torch.einsum("hgn,nhd->hgd", p, v).reshape(Hq, D)
+        most = torch.einsum("hgn,nhd->hgd", p, v.abs()).reshape(Hq, D)
+        assert ((o[0].double() - want).abs() <= most * 2.0 ** -7 + 1e-6).all()
+    keep = c.pages.indptr.clone()
+    c.pages.indptr[2] = 1 << 20
+    o, lse, _ = c.run(pm, ws=ws)
+    assert pm.mla_check_error(ws) == 5
+    assert torch.equal(o[0], good[0]) and (o[1:] == 0).all() and torch.isneginf(lse[1:]).all()
+    c.pages.indptr = keep
+    o, lse, _ = c.run(pm, ws=ws)
+    assert pm.mla_check_error(ws) == 0 and torch.equal(o, good)
+
+
+def test_decode_of_many_rows_in_a_graph(pm):
+    """Captured once, replayed after lengths, pages and rows have changed in place."""
+    a, b = (Decode(held, [2, 2, 2], 40, 2, 128, 16, 16, seed=3) for held in ([500, 40, 3000], [2, 3000, 530]))
+    ws = pm.make_gqa_block_decode_workspace(40, 2, 128, 2, DEV)
+    want = [x.run(pm, ws=ws)[:2] for x in (a, b)]
+    assert a.pages.indices.shape == b.pages.indices.shape and a.kc.shape == b.kc.shape
+    o, lse = (torch.empty_like(x) for x in want[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        pm.mla_gqa_block_decode(a.q, a.kc, a.vc, a.ks, a.vs, o, a.qo, a.pages.indptr, a.pages.indices,
+                                a.pages.last, 2, a.sm, lse, ws)
+    g.replay()
+    assert torch.equal(o, want[0][0]) and torch.equal(lse, want[0][1])
+    for x, y in ((a.q, b.q), (a.kc.view(torch.uint8), b.kc.view(torch.uint8)),
+                 (a.vc.view(torch.uint8), b.vc.view(torch.uint8)), (a.ks, b.ks), (a.vs, b.vs),
+                 (a.pages.indptr, b.pages.indptr), (a.pages.indices, b.pages.indices), (a.pages.last, b.pages.last)):
+        x.copy_(y)
+    g.replay()
+    assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
     assert pm.mla_check_error(ws) == 0
