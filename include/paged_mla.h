@@ -450,7 +450,7 @@ int mla_get_prompt_workspace_size(int64_t n_keys, int32_t v_head_dim, int32_t nu
  *   *free_count_out   = n - sum_b (P_b - O_b),   n = *free_count
  *   qo_indptr, key_indptr, kv_indptr = running sums of T, L and P, each from 0
  *   kv_indices[kv_indptr[b] + j] = block_table[b][j]                             (j < P_b)
- *   kv_last_page_lens[b] = L_b - (P_b - 1) PS  (1 where L_b = 0)
+ *   kv_last_page_lens[b] = L_b - (P_b - 1) PS  (PS where L_b = 0)
  *   positions[qo_indptr[b] + i]    = L_b - T_b + i                               (i < T_b)
  *   slot_mapping[qo_indptr[b] + i] = its page * PS + its place in it
  *   seq_lens, new_lens  (B,) INT32: L_b and T_b, 0 <= T_b <= L_b; B <= 16384

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
   for (int b0 = 0; b0 < p.B || b0 == 0; b0 += kThreads) {
     const int b = b0 + tid;
     Sums x = {};
-    int last = 1;
+    int last = ps_mask + 1;                  // of no page: the formula all the same
     if (b < p.B) {
       const int64_t len = __ldg(p.seq_lens + b), fresh = __ldg(p.new_lens + b);
       const int64_t pages = (len + ps_mask) >> p.log2_page;

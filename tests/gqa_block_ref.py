@@ -44,7 +44,7 @@ def page_table(seq, new, rows, ps, free=None, n_idx=None):
         out["kv"].append(out["kv"][-1] + pages)
         out["qo"].append(out["qo"][-1] + t)
         out["key"].append(out["key"][-1] + n)
-        out["last"].append(n - (pages - 1) * ps if n else 1)
+        out["last"].append(n - (pages - 1) * ps)
         for p in range(n - t, n):
             page = rows[b][p // ps]
             out["pos"].append(p)
