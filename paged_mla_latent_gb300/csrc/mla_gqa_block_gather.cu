@@ -90,7 +90,7 @@ __device__ __forceinline__ Source source_of(const BlockGatherParams& p, int64_t 
     t0 = __ldg(p.qo_indptr + lo);
     t1 = __ldg(p.qo_indptr + lo + 1);
   }
-  if (held < 0 || s < 0 || e - s != held || t0 < 0 || t1 < t0 || t1 > p.n_new || t1 - t0 > held) return from;
+  if (held < 0 || s < 0 || e - s != held || e > p.n_rows || t0 < 0 || t1 < t0 || t1 > p.n_new || t1 - t0 > held) return from;
   const int j = static_cast<int>(row - s), cached = held - static_cast<int>(t1 - t0);
   if (j >= cached) {
     from.at = t0 + j - cached;

@@ -339,6 +339,18 @@ def test_gather_many_requests_and_errors(pm):
     assert err.item() == 2
     lo, hi = rows[2].item(), rows[3].item()
     assert (k_rows[lo:hi] == 7).all() and _same(k_rows[hi:], want[hi:]) and _same(k_rows[:lo], want[:lo])
+    # rows for all but part of the last request: it is left out whole
+    err.zero_()
+    short = torch.full((sum(held) - 1, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    end = max(i for i, n in enumerate(held) if n > 1)
+    stop = sum(held[:end])
+    rows, keep = rows.clone(), rows
+    pages_end = pages.indptr.clone()
+    rows[end + 1:] = stop + held[end]           # nothing behind it
+    pages_end[end + 2:] = pages_end[end + 1]
+    pm.mla_gqa_block_gather(kc, vc, ks, vs, pages_end, pages.indices, pages.last, rows, short[:stop + 1],
+                            torch.empty_like(short[:stop + 1]), err)
+    assert err.item() == 2 and (short[stop] == 7).all() and _same(short[:stop], want[:stop])
 
 
 # -------------------------------------------------------------------------------- decode
@@ -557,6 +569,8 @@ def test_decode_shares_a_workspace_with_the_plain_decode(pm):
     ([4100, 17], [5, 2], 48, 4, 128, 1024, 128, "hnd"),
     ([300], [64], 8, 1, 128, 256, 64, "nhd"),
     ([300, 70], [64, 33], 4, 2, 64, 128, 128, "nhd"),
+    ([5, 300, 40], [64, 64, 50], 2, 1, 128, 16, 16, "nhd"),            # queries that see nothing
+    ([5, 300, 40], [64, 64, 50], 4, 4, 64, 8, 8, "nhd"),
     ([2001] * 5, [2] * 5, 40, 2, 128, 4, 4, "nhd"),
     ([65001], [4], 16, 2, 128, 64, 64, "nhd"),
     ([33001], [4], 16, 2, 64, 64, 64, "nhd"),
