@@ -11,7 +11,7 @@
 // the others copy, eight columns of a row at a time, K and V together.
 //
 // Measured (one GB300, in a CUDA graph): 63,911 cached and 4,089 new positions, 8 heads of 128, 426
-// MB: 73 us, 5.9 TB/s, which a plain copy of as many bytes takes, too (75 us; 85 us without the
+// MB: 72 us, 5.9 TB/s, which a plain copy of as many bytes takes, too (75 us; 85 us without the
 // warp ahead, a block a tile); 53 prompts of 1 to 700 tokens behind 0 to 300, two heads of 64: 5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
