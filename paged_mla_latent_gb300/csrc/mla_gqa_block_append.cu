@@ -8,7 +8,8 @@
 //   scale grew.  Powers of two cost no precision (e4m3 has three bits whatever the scale) and
 //   make quotients and the earlier codes' growth exact but for e4m3's subnormals.
 //
-// Bytes bound.  A unit is a block (16 positions of smaller ones) of up to 256 columns' threads of
+// Bytes bound.  A unit is a block (32 positions of smaller ones; 16,384 tokens of 32/8 heads in
+// blocks of 16: 82 us, 90 with 16, chunks as below 15, 17 and with 64 19) of up to 256 columns' threads of
 // heads' keys or values: eight (or four) threads a row of a head, each with two 8-column words half
 // a region apart (the rotated columns or the rest), which with pairs (i, i + R/2) are each other's
 // partners.  The rows are read twice, for the maxima and, from L2, for the codes: kept in registers
@@ -20,7 +21,7 @@
 //
 // Measured (one GB300, in a CUDA graph): 16,384 tokens, 32/8 heads of 128, blocks of 64, rotated
 // keys kept, 411 MB: 76 us, 5.4 TB/s (0.81 of the copy rate; units of 8 heads 82, of 2 83; without
-// the L2 prefetch 78); 37 requests of 1 to 700 tokens, 25/5 heads of 64, 49 MB: 17 us; one token of
+// the L2 prefetch 78); 37 requests of 1 to 700 tokens, 25/5 heads of 64, 49 MB: 15 us; one token of
 // 64 requests, 16/2 heads: 5 us, a chain of request, lists, page, scale and words.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -37,7 +38,7 @@ namespace {
 using namespace pmla;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnit = 16;                   // positions of a unit, or a block of them
+constexpr int kLog2Unit = 5, kUnit = 1 << kLog2Unit;         // positions of a unit, where blocks have fewer
 
 struct BlockAppendParams {
   const uint16_t *q, *k, *v;                // bf16 bits
@@ -257,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const Blo
     turn_queries<D, kNeox>(p, static_cast<int64_t>(blockIdx.x - p.kv_ctas) * kWarps + (tid >> 5), lane);
     return;
   }
-  // ---- the unit: a request, a block of positions (or 16 of smaller blocks), keys or values
+  // ---- the unit: a request, a block of positions (or 32 of smaller blocks), keys or values
   const int slot = blockIdx.x / p.parts, part = blockIdx.x - slot * p.parts;
   const bool is_k = (part & 1) == 0;
   const int first_head = (part >> 1) * p.part_heads;
   const int heads = p.Hk - first_head < p.part_heads ? p.Hk - first_head : p.part_heads;
   const int bs = 1 << p.log2_block;
-  const int log2_unit = p.log2_block > 4 ? p.log2_block : 4;
+  const int log2_unit = p.log2_block > kLog2Unit ? p.log2_block : kLog2Unit;
   auto start = [&](int b) { return static_cast<int64_t>(__ldg(p.qo_indptr + b) >> log2_unit) + 2 * static_cast<int64_t>(b); };
   const int b = warp_owner(p.B, lane, slot, start);
   const Request r = request_of(p, b);
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const Blo
 template <int D, bool kNeox>
 int launch(BlockAppendParams& p, int sms, cudaStream_t s) {
   constexpr int kRows = 32 / (D / 16);
-  const int unit = p.log2_block > 4 ? p.log2_block : 4;
+  const int unit = p.log2_block > kLog2Unit ? p.log2_block : kLog2Unit;
   p.part_heads = 32 / (D / 16);            // a warp a row: 1 KB of neighbours in a token
   if (p.part_heads > p.Hk) p.part_heads = p.Hk;
   p.parts = 2 * ((p.Hk + p.part_heads - 1) / p.part_heads);
