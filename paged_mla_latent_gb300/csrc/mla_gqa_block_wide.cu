@@ -4,10 +4,10 @@
 // 128-wide head or of a pair of 64-wide ones, whose 128 bytes of a slot are one row of a tile.
 //
 // A tile is 128 positions: the MMA's M (tensor memory's lanes).
-//   S^T (128 x 64) = K (128 x 128 bytes) . q^T, q's rows as two e4m3 planes side by side in N:
+//   S^T (128 x 64) = K (128 x 128 bytes) . q^T, a head's rows as two e4m3 planes side by side in N:
 //     q up = high + 2^-5 low, its largest in [2^7, 2^8): bf16's eight bits are four and four, and what
-//     is lost is below 2^-22 of the row's largest.  Rows of a pair of heads are zero in the other
-//     head's columns.
+//     is lost is below 2^-22 of the row's largest.  A head of a pair takes its 64 bytes of K only: a
+//     NaN there is no other head's.
 //   a_j = log2(e) s_j + log2 vscale(j), p_j = 2^(a_j - m + 5) for a reference m that moves only where an
 //     a_j passes it by more than 3: p stays below 2^8, e4m3 ends at 448.  (Moving costs some 800
 //     cycles: with room for 4, 3, 2 and 1 the first case below takes 112, 114, 117 and 120 us.)
@@ -15,7 +15,7 @@
 //     planes: p (rounded to f16) = h + 2^-5 l + 2^-10 l', 11 bits down to 2^-13 of the largest
 //     weight times scale, below that multiples of 2^-24 of it: what 131,072 positions lose by
 //     rounding is under 2^-8 of what the largest has, bf16's half step.
-// Eight MMAs a tile, 64 and 96 columns wide: about 400 cycles of the tensor pipe for 32 KB, which take
+// Eight MMAs a tile, 64 (32 for a pair) and 96 columns wide: about 400 cycles of the tensor pipe for 32 KB, which take
 // 1,420 from memory.
 //
 // Warps: two groups of four take a TMEM lane a thread (a position: its scales, its weights of 16
@@ -157,7 +157,7 @@ __device__ __forceinline__ void landed(float (&v)[N]) {
 // Byte offset of 16-byte chunk c of row r: rows of 128 bytes, eight of them a swizzle atom.
 __device__ __forceinline__ uint32_t atom_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-// q's rows: high planes of the unit's 32, then low ones; sc: each row's factor from a product of
+// q's rows: a head's high planes, then its low ones; sc: each row's factor from a product of
 // high to a score in units of log2.  By the softmax warps, four rows each.
 template <class S>
 __device__ __forceinline__ void stage_queries(const BlockDecodeParams& p, const Piece& u, uint8_t* s_q, float* s_sc,
@@ -197,8 +197,9 @@ __device__ __forceinline__ void stage_queries(const BlockDecodeParams& p, const 
       high |= c << (16 * i);
       low |= static_cast<uint32_t>(f32x2_to_e4m3x2((b - back.y) * 32.f, (a - back.x) * 32.f)) << (16 * i);
     }
-    *reinterpret_cast<uint32_t*>(s_q + atom_at(ur, lane >> 2) + 4 * (lane & 3)) = high;
-    *reinterpret_cast<uint32_t*>(s_q + atom_at(S::kRows + ur, lane >> 2) + 4 * (lane & 3)) = low;
+    const int at = ur / S::kHeads * S::kHeads + ur;      // behind the planes of the heads before
+    *reinterpret_cast<uint32_t*>(s_q + atom_at(at, lane >> 2) + 4 * (lane & 3)) = high;
+    *reinterpret_cast<uint32_t*>(s_q + atom_at(at + S::kHeads, lane >> 2) + 4 * (lane & 3)) = low;
     if (lane == 0) s_sc[ur] = p.sm_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
   }
 }
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
     S::join_sync();
     if (warp == kMmaWarp) {
       // ---- the MMAs: the whole warp runs the loop, an elected lane issues
-      constexpr uint32_t idesc_qk = idesc_f8(128, 2 * kRows, false, false);
+      constexpr uint32_t idesc_qk = idesc_f8(128, 2 * kHeads, false, false);
       constexpr uint32_t idesc_pv = idesc_f8(128, 3 * kRows, true, true);
       const uint64_t k0 = smem_desc(sbase, 16, 1024, kSw128);
       const uint64_t v0 = smem_desc(sbase + S::kHalf, S::kHalf, 1024, kSw128);
@@ -382,9 +383,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
         if (!wait(misc->full + stage, (it / kStages) & 1)) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f8_warp(tmem + (it & 1) * S::kScores, desc_at(k0, stage * S::kStageBytes + 32 * kk), desc_at(q0, 32 * kk),
-                      idesc_qk, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          const int hp = kk / (D / 32);
+          mma_f8_warp(tmem + (it & 1) * S::kScores + hp * 2 * kHeads, desc_at(k0, stage * S::kStageBytes + 32 * kk),
+                      desc_at(q0, hp * 2 * kHeads * 128 + 32 * kk), idesc_qk, kk % (D / 32) > 0 ? 1u : 0u);
+        }
         mma_commit_warp(bar(misc->s_full + (it & 1)));
         if (i > 0) weigh(i - 1);
       }
@@ -394,6 +397,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
       // ---- weights: a thread a position and 16 rows, of one head
       const int grp = warp >> 2, c0 = 16 * grp, hp = c0 / kHeads;
       const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+      const uint32_t s_at = tl + hp * kHeads + c0;       // the scores of its rows' high planes
       const int prow = 32 * (warp & 3) + lane;
       const int least = len - u.r.tokens + 1;            // positions that the first token sees
       const float* const s_scale = reinterpret_cast<const float*>(smem + S::kScaleOff) + hp * kTile + prow;
@@ -414,8 +418,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
         mbar_wait(bar(misc->s_full + (it & 1)), (it >> 1) & 1, abort_flag, p.err);
         tc_fence_after();
         float a[16], lo[16];
-        tmem_ld16(tl + (it & 1) * S::kScores + c0, a);
-        tmem_ld16(tl + (it & 1) * S::kScores + kRows + c0, lo);
+        tmem_ld16(s_at + (it & 1) * S::kScores, a);
+        tmem_ld16(s_at + (it & 1) * S::kScores + kHeads, lo);
         tmem_wait_ld();
         landed(a);
         landed(lo);

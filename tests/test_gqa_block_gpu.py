@@ -667,3 +667,40 @@ def test_decode_of_many_rows_in_a_graph(pm):
     g.replay()
     assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
     assert pm.mla_check_error(ws) == 0
+
+
+@pytest.mark.parametrize("new", [1, 3])       # 8 rows a KV head, and 24
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_keeps_heads_apart(pm, D, new):
+    """NaN codes, NaN scales and infinite queries of one head leave the others' bits as they were."""
+    c = Decode([300, 2000], [new, new], 24, 3, D, 16, 16)
+    c.pages.indices = torch.cat([c.pages.indices, torch.full((1 << 22,), 1 << 30, dtype=torch.int32, device=DEV)])
+    good, lse_good, ws = c.run(pm)
+    page, slot = c.pages.where(1, 70, 90)
+    group = lambda x, h: x.view(2 * new, 3, 8, -1)[:, h]
+    for h in range(3):
+        others = [x for x in range(3) if x != h]
+        for what in ("k code", "v code", "k scale", "v scale", "q"):
+            if what == "q":
+                x, at, bad = c.q, (slice(None), slice(8 * h, 8 * h + 8)), math.inf
+            else:
+                x = {"k code": c.kc, "v code": c.vc, "k scale": c.ks, "v scale": c.vs}[what]
+                at, bad = ((page, slot, h), 0x7F) if "code" in what else ((page, 0, h), math.nan)
+                x = x.view(torch.uint8) if "code" in what else x
+            keep = x[at].clone()
+            x[at] = bad
+            o, lse, _ = c.run(pm, ws=ws)
+            x[at] = keep
+            for g in others:
+                assert torch.equal(group(o, g), group(good, g)) and torch.equal(group(lse, g), group(lse_good, g)), (what, h, g)
+    o, lse, _ = c.run(pm, ws=ws)
+    assert torch.equal(o, good) and torch.equal(lse, lse_good) and pm.mla_check_error(ws) == 0
+
+
+def test_decode_of_many_rows_and_requests(pm):
+    """More requests than a CTA scans at once, empty ones among them."""
+    held = [(i * 37) % 290 for i in range(900)]
+    c = Decode(held, [2 if i % 11 else 0 for i in range(900)], 20, 2, 64, 8, 8, pad=7)
+    o, lse, ws = c.run(pm, torch.float32)
+    assert pm.mla_check_error(ws) == 0
+    c.check(o, lse, "900 requests", blk.LOST_MANY)
