@@ -665,8 +665,8 @@ def mla_gqa_block_decode(q, k_cache, v_cache, k_scale, v_scale, o, qo_indptr, kv
         with _on_stream(stream, q.device):      # made and zeroed on the stream that uses it
             workspace = make_gqa_block_decode_workspace(q.shape[1], k_cache.shape[2], q.shape[2],
                                                         max_seqlen_q, q.device)
-    elif workspace.get_device() != d:
-        raise ValueError(f"the workspace must be on CUDA device {d}")
+    elif workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on CUDA device {d}")
     rc = _native.mla_gqa_block_decode(
         d, q, k_cache, v_cache, k_scale, v_scale, o, qo_indptr, kv_indptr, kv_indices, kv_last_page_lens,
         max_seqlen_q, sm_scale, lse_out, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, d))

@@ -1,6 +1,7 @@
 """The block-scaled operators together, as a serving loop runs them: the example's layer, and its
 steps captured into a graph."""
 import importlib.util
+import math
 import os
 
 import pytest
@@ -192,3 +193,62 @@ def test_caches_past_31_bits(pm):
     want = torch.einsum("hgn,nhd->hgd", torch.softmax(s, -1), rows[1].double()).reshape(16, d)
     # weights rounded to 2^-11, against rows that are themselves rounded to bf16 exactly (powers of two)
     assert ((o[0].double() - want).abs() <= 2.0 ** -10 * rows[1].float().abs().max()).all()
+
+
+def test_many_rows_past_31_bits(pm):
+    """The same offsets for more than 16 rows a KV head, pairs of 64-wide heads among them."""
+    ps, pages, held, new = 128, 18000, 300, 9
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    lists = ints([0, 3]), ints([pages - 1, 0, pages - 3]), ints([held - 2 * ps])
+    g = blk.gen(2, DEV)
+    both = [torch.zeros(pages * ps * 1024, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for hk, d in ((8, 128), (16, 64)):
+        kc, vc = (x.view(pages, ps, hk, d) for x in both)
+        ks, vs = (torch.zeros(pages, 2, hk, device=DEV) for _ in range(2))
+        for cache, scale in ((kc, ks), (vc, vs)):
+            for page in lists[1].tolist():
+                x = torch.randn(ps, hk, d, generator=g, device=DEV) * 100
+                cache[page] = x.clamp(-448, 448).to(blk.F8).view(torch.uint8)
+                scale[page] = torch.exp2(torch.randint(-9, -5, (2, hk), generator=g, device=DEV).float())
+        q = torch.randn(new, 2 * hk, d, generator=g, device=DEV).bfloat16()
+        o, lse = torch.empty(q.shape, device=DEV), torch.empty(q.shape[:2], device=DEV)
+        ws = pm.mla_gqa_block_decode(q, kc.view(blk.F8), vc.view(blk.F8), ks, vs, o, ints([0, new]), *lists, new,
+                                     d ** -0.5, lse)
+        assert pm.mla_check_error(ws) == 0
+        j = torch.arange(held, device=DEV)
+        page, slot = lists[1].long()[j // ps], j % ps
+        k, v = (c.view(blk.F8)[page, slot].double() * s[page, slot // 64].double()[..., None] for c, s in ((kc, ks), (vc, vs)))
+        s = torch.einsum("thgd,nhd->thgn", q.view(new, hk, 2, d).double(), k) * d ** -0.5
+        s = s.masked_fill((j > held - new + torch.arange(new, device=DEV)[:, None])[:, None, None, :], -math.inf)
+        want = torch.einsum("thgn,nhd->thgd", torch.softmax(s, -1), v).reshape(o.shape)
+        # weights times scale rounded to 2^-11, or a multiple of 2^-24 of the largest; fp32 scores
+        most = torch.einsum("thgn,nhd->thgd", torch.softmax(s, -1), v.abs()).reshape(o.shape)
+        assert ((o.double() - want).abs() <= 2.0 ** -9 * most + 2.0 ** -24 * held * v.abs().max()).all()
+
+
+def test_decodes_of_few_and_many_rows_share_a_workspace(pm):
+    """In turn on one workspace, the one-scale decode among them; too small and scattered ones are
+    refused."""
+    from tests.test_gqa_block_gpu import Decode
+    ws = max((pm.make_gqa_block_decode_workspace(32, 2, d, 4, DEV) for d in (64, 128)), key=lambda x: x.numel())
+    cases = [Decode([30001, 5], [1, 1], 32, 2, 128, 64, 64), Decode([20001, 40], [4, 2], 16, 2, 128, 16, 16),
+             Decode([30001], [4], 32, 2, 64, 64, 64)]
+    want = [c.run(pm)[:2] for c in cases]
+    one = torch.tensor(0.02, device=DEV)
+    c = cases[0]
+    plain = torch.empty_like(c.q)
+    for i in range(3):
+        for c, (o0, lse0) in zip(cases, want):
+            o, lse, _ = c.run(pm, ws=ws)
+            assert torch.equal(o, o0) and torch.equal(lse, lse0)
+        c = cases[0]
+        pm.mla_gqa_decode(c.q, c.kc, c.vc, plain, c.pages.indptr, c.pages.indices, c.pages.last, c.sm, one, one,
+                          workspace=ws)
+        if i == 0:
+            first = plain.clone()
+        assert torch.equal(plain, first)
+    assert pm.mla_check_error(ws) == 0
+    with pytest.raises(ValueError):
+        cases[1].run(pm, ws=torch.zeros(1, dtype=torch.uint8, device=DEV).expand(1 << 26))
+    with pytest.raises(pm.MlaError):
+        cases[1].run(pm, ws=ws[:4096])
