@@ -9,7 +9,7 @@
 //   make quotients and the earlier codes' growth exact but for e4m3's subnormals.
 //
 // Bytes bound.  A unit is a block (32 positions of smaller ones; 16,384 tokens of 32/8 heads in
-// blocks of 16: 82 us, 90 with 16, chunks as below 15, 17 and with 64 19) of up to 256 columns' threads of
+// blocks of 16: 76 us, 90 before with 16, chunks as below 15, 17 and with 64 19) of up to 256 columns' threads of
 // heads' keys or values: eight (or four) threads a row of a head, each with two 8-column words half
 // a region apart (the rotated columns or the rest), which with pairs (i, i + R/2) are each other's
 // partners.  The rows are read twice, for the maxima and, from L2, for the codes: kept in registers
@@ -20,9 +20,10 @@
 // the same launch, a warp four (or eight) tokens and up to four heads.
 //
 // Measured (one GB300, in a CUDA graph): 16,384 tokens, 32/8 heads of 128, blocks of 64, rotated
-// keys kept, 411 MB: 76 us, 5.4 TB/s (0.81 of the copy rate; units of 8 heads 82, of 2 83; without
-// the L2 prefetch 78); 37 requests of 1 to 700 tokens, 25/5 heads of 64, 49 MB: 15 us; one token of
-// 64 requests, 16/2 heads: 5 us, a chain of request, lists, page, scale and words.
+// keys kept, 411 MB: 73 us, 5.6 TB/s (0.84 of the copy rate; with keys and values before the
+// queries 76, so with units of 8 heads 82, of 2 83, without the L2 prefetch 78); 37 requests of 1 to
+// 700 tokens, 25/5 heads of 64, 49 MB: 15 us; one token of 64 requests, 16/2 heads: 5 us, a chain of
+// request, lists, page, scale and words.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -60,7 +61,8 @@ struct BlockAppendParams {
   int B, Hq, Hk;
   int half_rot;                             // R / 2
   int part_heads, parts;                    // heads a unit takes; units of a block's keys and values
-  unsigned kv_ctas, q_ctas;       // then some blocks that look the lists over
+  unsigned kv_ctas, q_ctas;                 // then some blocks that look the lists over
+  unsigned every;                           // of them one of so many is for keys and values, until those are out
   int strip;                                // query heads a warp takes
   int* err;
 };
@@ -254,12 +256,14 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const Blo
     if (i < p.B && !request_of(p, static_cast<int>(i)).sound) atomicOr(p.err, kErrBadIndptr);
     return;
   }
-  if (blockIdx.x >= p.kv_ctas) {
-    turn_queries<D, kNeox>(p, static_cast<int64_t>(blockIdx.x - p.kv_ctas) * kWarps + (tid >> 5), lane);
+  const unsigned nth = blockIdx.x / p.every;
+  if (nth >= p.kv_ctas || blockIdx.x != nth * p.every) {
+    const unsigned before = nth + 1 < p.kv_ctas ? nth + 1 : p.kv_ctas;     // blocks for keys and values
+    turn_queries<D, kNeox>(p, static_cast<int64_t>(blockIdx.x - before) * kWarps + (tid >> 5), lane);
     return;
   }
   // ---- the unit: a request, a block of positions (or 32 of smaller blocks), keys or values
-  const int slot = blockIdx.x / p.parts, part = blockIdx.x - slot * p.parts;
+  const int slot = nth / p.parts, part = nth - slot * p.parts;
   const bool is_k = (part & 1) == 0;
   const int first_head = (part >> 1) * p.part_heads;
   const int heads = p.Hk - first_head < p.part_heads ? p.Hk - first_head : p.part_heads;
@@ -465,6 +469,11 @@ int launch(BlockAppendParams& p, int sms, cudaStream_t s) {
   if (ctas > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
   p.kv_ctas = static_cast<unsigned>(kv_ctas);
   p.q_ctas = static_cast<unsigned>(q_ctas);
+  // Keys and values, the longer chains, come first; where they are more than two waves (three blocks a
+  // SM) every other block turns queries, which stream while the others wait: 16,384 tokens in
+  // blocks of 64, 1,056 blocks here, 73.4 us (76.7 with keys and values first), in blocks of 16, 2,080,
+  // 76 (81); 37 chunks, 742 blocks, 17.2 and 14.8; 8,192 tokens, 544 blocks, 41.1 and 41.5.
+  p.every = kv_ctas > 6 * static_cast<int64_t>(sms) && q_ctas >= kv_ctas ? 2 : 1;
   gqa_block_append_kernel<D, kNeox><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

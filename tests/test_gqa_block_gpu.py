@@ -103,6 +103,9 @@ APPENDS = [
     ([128, 256], [128, 384], 8, 8, 64, 64, 0, 128, 128, "nhd"),
     ([5] * 40, [i * 7 % 140 for i in range(40)], 4, 2, 128, 128, 1, 128, 128, "nhd"),
     ([20] * 40, [i * 7 % 140 for i in range(40)], 2, 2, 128, 128, 0, 128, 128, "hnd"),
+    # more than two waves of keys' and values' blocks, with the queries' between them
+    ([1000], [5], 256, 64, 128, 128, 1, 16, 16, "nhd"),
+    ([1900], [5], 256, 64, 64, 32, 0, 64, 32, "hnd"),
 ]
 
 
