@@ -569,7 +569,8 @@ int mla_get_gqa_block_decode_workspace_size(int32_t num_heads, int32_t num_kv_he
  * The result does not depend on the order in which the pieces of a split request finish.
  * Device-side errors go to the workspace's error word (mla_check_error): a page list that makes
  * no sense makes that request empty, a token range outside sum_T or of more than max_seqlen_q
- * leaves it out, a page id outside the cache reads as zeros; all give MLA_ERR_BAD_INDEX.
+ * leaves it out, a page id outside the cache reads as zeros; all give MLA_ERR_BAD_INDEX.  A wait
+ * inside the kernel that runs out (2 s) gives MLA_ERR_TIMEOUT: some of the call's rows are wrong then.
  */
 int mla_gqa_block_decode(const mla_tensor_t* q, const mla_tensor_t* k_cache,
                          const mla_tensor_t* v_cache, const mla_tensor_t* k_scale,
