@@ -14,8 +14,9 @@
 // and then takes groups of four entries of the lists, found by bisection in shared memory.
 //
 // Measured (one GB300, in a CUDA graph): 64 requests of up to 65,536 positions, one new token each, pages
-// of 128: 4.9 us; 24 of 68,000 positions, 4,089 new, one-token pages, 7.4 MB of lists: 6.9 us (8.0 with two
-// blocks a SM and the stack's count claimed at the end).
+// of 128: 5.0 us; 24 of 68,000 positions, 4,089 new, one-token pages, 7.4 MB of lists: 7.2 us (8.0 with two
+// blocks a SM and the stack's count claimed at the end; 6.4 and 7.2 with it read and claimed by a thread that
+// writes entries, too).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,7 +30,8 @@ namespace {
 
 using namespace pmla;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;        // a block's, and a warp for the pool's count
+constexpr int kBlock = kThreads + 32;
 constexpr int kEach = 4;               // consecutive entries a thread takes
 constexpr int64_t kMaxRequests = 16384;      // three sums of each in shared memory
 constexpr int64_t kIntMax = 0x7FFFFFFF;
@@ -76,7 +78,7 @@ __device__ __forceinline__ int owner(const int32_t* pre, int B, int64_t i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTableParams p) {
+__global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParams p) {
   extern __shared__ int32_t s_pre[];         // running sums: pages, tokens, pages taken
   int32_t* s_kv = s_pre;
   int32_t* s_qo = s_kv + p.B + 1;
@@ -84,19 +86,13 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
   __shared__ Sums s_warp[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps_mask = (1 << p.log2_page) - 1;
-  const int32_t held = p.free_count ? __ldcg(p.free_count) : 0;
-  // the count may be written in place: by the block that is the last to have read it, at its end
-  bool writes = gridDim.x == 1;
-  if (p.free_count_out && gridDim.x > 1 && tid == 0) {
-    int one;                                 // 1, which waits for the read
-    asm volatile("and.b32 %0, %1, 0;\n\tadd.s32 %0, %0, 1;" : "=r"(one) : "r"(held));
-    writes = atomicAdd(p.err + 1, one) == static_cast<int>(gridDim.x) - 1;
-  }
-  const int64_t n_free = held >= 0 && held <= p.n_pool ? held : 0;
+  __shared__ int32_t s_held;                 // the pool's count, read once for all of the block
+  const bool counts = tid == kThreads;
+  if (counts) s_held = p.free_count ? __ldcg(p.free_count) : 0;
 
   Sums run = {};
   for (int b0 = 0; b0 < p.B || b0 == 0; b0 += kThreads) {
-    const int b = b0 + tid;
+    const int b = tid < kThreads ? b0 + tid : p.B;
     Sums x = {};
     int last = ps_mask + 1;                  // of no page: the formula all the same
     if (b < p.B) {
@@ -117,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
       if (lane >= d) inc = inc + o;
     }
     __syncthreads();
-    if (lane == 31) s_warp[warp] = inc;
+    if (lane == 31 && warp < kWarps) s_warp[warp] = inc;
     __syncthreads();
     Sums all = run;
 #pragma unroll
@@ -138,16 +134,32 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
       }
     }
   }
-  if (tid == 0) {
-    s_kv[0] = s_qo[0] = s_taken[0] = 0;
-    if (blockIdx.x == 0) {
-      p.kv_indptr[0] = p.qo_indptr[0] = p.key_indptr[0] = 0;
-      if (run.pages > p.n_idx || run.keys > kIntMax || (p.positions && run.tokens > p.n_tok))
-        atomicOr(p.err, kErrBadOutput);
-      if (run.taken > n_free) atomicOr(p.err, kErrBadIndex);
-    }
-  }
+  if (tid == 0) s_kv[0] = s_qo[0] = s_taken[0] = 0;
   __syncthreads();
+  const int32_t held = s_held;
+  const int64_t n_free = held >= 0 && held <= p.n_pool ? held : 0;
+  if (warp == kWarps) {
+    // The count may be written in place, so a block arrives when it has read it, and the one that
+    // arrives last writes it.  (By a warp that writes nothing else: fences wait for a warp's
+    // stores, 1.5 us on a warp with entries of the lists.)
+    if (counts && p.free_count_out) {
+      bool last = true;
+      if (gridDim.x > 1) {
+        __threadfence();                     // the read before the arrival
+        last = atomicAdd(p.err + 1, 1) == static_cast<int>(gridDim.x) - 1;
+        __threadfence();                     // the others' arrivals before the write
+        if (last) p.err[1] = 0;              // as it was found, for the next call
+      }
+      if (last) *p.free_count_out = held - static_cast<int32_t>(run.taken < n_free ? run.taken : n_free);
+    }
+    return;
+  }
+  if (tid == 0 && blockIdx.x == 0) {
+    p.kv_indptr[0] = p.qo_indptr[0] = p.key_indptr[0] = 0;
+    if (run.pages > p.n_idx || run.keys > kIntMax || (p.positions && run.tokens > p.n_tok))
+      atomicOr(p.err, kErrBadOutput);
+    if (run.taken > n_free) atomicOr(p.err, kErrBadIndex);
+  }
 
   // page j of request b: one that it had, or a new one by its place in the stack
   auto page_of = [&](int b, int j, int fresh_from) -> int32_t {
@@ -199,10 +211,6 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
         p.slots[i] = slot;
       }
     }
-  }
-  if (p.free_count_out && tid == 0 && writes) {
-    if (gridDim.x > 1) p.err[1] = 0;         // as it was found, for the next call
-    *p.free_count_out = held - static_cast<int32_t>(run.taken < n_free ? run.taken : n_free);
   }
 }
 
@@ -296,6 +304,6 @@ extern "C" int mla_build_page_table(const mla_tensor_t* seq_lens, const mla_tens
   int64_t blocks = (longest + kThreads * kEach - 1) / (kThreads * kEach);
   if (blocks > 4 * sms) blocks = 4 * sms;
   if (blocks < 1) blocks = 1;
-  page_table_kernel<<<static_cast<unsigned>(blocks), kThreads, smem, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
+  page_table_kernel<<<static_cast<unsigned>(blocks), kBlock, smem, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
