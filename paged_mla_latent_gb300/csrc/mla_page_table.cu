@@ -48,8 +48,8 @@ struct PageTableParams {
   int32_t* free_count_out;
   int32_t *qo_indptr, *key_indptr, *kv_indptr, *kv_indices, *last;
   int64_t n_idx;
-  int32_t *positions, *slots;                // may be null
-  int64_t n_tok;
+  int32_t *positions, *slots;
+  int64_t n_tok;                             // -1: neither is wanted
   int* err;                                  // error bits, arrivals
 };
 
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParam
   }
   if (tid == 0 && blockIdx.x == 0) {
     p.kv_indptr[0] = p.qo_indptr[0] = p.key_indptr[0] = 0;
-    if (run.pages > p.n_idx || run.keys > kIntMax || (p.positions && run.tokens > p.n_tok))
+    if (run.pages > p.n_idx || run.keys > kIntMax || (p.n_tok >= 0 && run.tokens > p.n_tok))
       atomicOr(p.err, kErrBadOutput);
     if (run.taken > n_free) atomicOr(p.err, kErrBadIndex);
   }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParam
     for (int k = 0; k < kEach; ++k)
       if (i0 + k < n_list && i0 + k < p.n_idx) p.kv_indices[i0 + k] = page[k];
   }
-  if (p.positions) {
+  if (p.n_tok > 0) {
     const int64_t total = run.tokens < kIntMax ? run.tokens : kIntMax;
     for (int64_t i0 = first; i0 < p.n_tok; i0 += stride) {
       int b = i0 < total ? owner(s_qo, p.B, i0) : 0;
@@ -276,11 +276,11 @@ extern "C" int mla_build_page_table(const mla_tensor_t* seq_lens, const mla_tens
   p.kv_indices = static_cast<int32_t*>(kv_indices->ptr);
   p.n_idx = kv_indices->shape[0];
   p.last = static_cast<int32_t*>(kv_last_page_lens->ptr);
+  p.n_tok = -1;
   if (positions) {
     p.positions = static_cast<int32_t*>(positions->ptr);
     p.slots = static_cast<int32_t*>(slot_mapping->ptr);
     p.n_tok = positions->shape[0];
-    if (p.n_tok == 0) p.positions = nullptr;
   }
   p.err = error_word;
 

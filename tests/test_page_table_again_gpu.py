@@ -40,3 +40,13 @@ def test_count_in_place_over_many_steps(pm, B):
     taken = mine.table[mine.table >= 0]
     assert taken.numel() == sum(-(-n // ps) for n in seq) == pool - mine.count.item()
     assert taken.unique().numel() == taken.numel()
+
+
+def test_buffers_of_no_entries(pm):
+    """Positions and slots of length 0 are lists like any other: cut, and flagged where the step has a
+    token."""
+    for t, bits in ((0, 0), (1, 8), (5, 8)):
+        s = Step([7, 5], [0, t], 4, 2, n_tok=0)
+        s.run(pm)
+        assert s.err[0].item() == bits
+        s.check()
