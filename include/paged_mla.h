@@ -467,8 +467,9 @@ int mla_get_prompt_workspace_size(int64_t n_keys, int32_t v_head_dim, int32_t nu
  *   error_word    two INT32 on the device (required): [0] error bits, [1] is the call's own, zero
  *                 before first use and left so; calls that share it must not overlap on the GPU.
  * Device-side errors: a request whose lengths make no sense (negative, T_b > L_b, P_b > W) counts
- * as empty and sets bit 2; a list longer than its buffer (or sums past 2^31) is cut and sets bit
- * 8; a pool that runs out gives pages of -1 (which readers flag) and slots of -1, *free_count_out
+ * as empty and sets bit 2; a list longer than its buffer is cut, sums past 2^31 - 1 are that, and
+ * either sets bit 8 (pages of more than that in all make no lists: no table entry, page or slot is
+ * given out, the count stays); a pool that runs out gives pages of -1 (which readers flag) and slots of -1, *free_count_out
  * is then 0, bit 1 (a *free_count outside [0, F] counts as 0 and stays).  The rest of the outputs
  * must not overlap one another or the inputs.
  */

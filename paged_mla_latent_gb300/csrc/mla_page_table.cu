@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParam
     }
   }
   if (tid == 0) s_kv[0] = s_qo[0] = s_taken[0] = 0;
+  const bool cut = run.pages > p.n_idx || run.keys > kIntMax || (p.n_tok >= 0 && run.tokens > p.n_tok);
+  if (run.pages > kIntMax) run = {};         // no lists of pages that their sums cannot tell apart
   __syncthreads();
   const int32_t held = s_held;
   const int64_t n_free = held >= 0 && held <= p.n_pool ? held : 0;
@@ -156,8 +158,7 @@ __global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParam
   }
   if (tid == 0 && blockIdx.x == 0) {
     p.kv_indptr[0] = p.qo_indptr[0] = p.key_indptr[0] = 0;
-    if (run.pages > p.n_idx || run.keys > kIntMax || (p.n_tok >= 0 && run.tokens > p.n_tok))
-      atomicOr(p.err, kErrBadOutput);
+    if (cut) atomicOr(p.err, kErrBadOutput);
     if (run.taken > n_free) atomicOr(p.err, kErrBadIndex);
   }
 
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParam
     return s_kv[b + 1] - s_kv[b] - (s_taken[b + 1] - s_taken[b]);
   };
 
-  const int64_t n_list = run.pages < kIntMax ? run.pages : kIntMax;
+  const int64_t n_list = run.pages;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads * kEach;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kThreads + tid) * kEach;
   for (int64_t i0 = first; i0 < n_list; i0 += stride) {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kBlock) page_table_kernel(const PageTableParam
         int32_t position = 0, slot = -1;     // behind the last request: no token
         if (i < total) {
           while (i >= s_qo[b + 1]) ++b;
-          position = __ldg(p.seq_lens + b) - (s_qo[b + 1] - static_cast<int32_t>(i));
+          position = __ldg(p.seq_lens + b) - __ldg(p.new_lens + b) + static_cast<int32_t>(i - s_qo[b]);
           const int32_t page = page_of(b, position >> p.log2_page, fresh_from(b));
           const int64_t at = (static_cast<int64_t>(page) << p.log2_page) + (position & ps_mask);
           if (page >= 0 && at <= kIntMax) slot = static_cast<int32_t>(at);

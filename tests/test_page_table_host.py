@@ -129,3 +129,28 @@ def test_tables(kernel, seq, new, ps, width, pool, blocks):
     s = Step(seq, new, ps, width, pool, blocks, table=table)
     s.run(kernel)
     s.check()
+
+
+@pytest.mark.parametrize("blocks", [1, 2])
+def test_pages_past_the_largest_index(lib, blocks):
+    """More pages in all than an index reaches (of 31 bits: here of 10, 999): bit 8, the sums end there,
+    and no table entry, page or slot is given out."""
+    s = Step([300, 500, 400, 7], [1, 100, 250, 7], 1, 500, pool=700, blocks=blocks, n_idx=900, n_tok=40)
+    before = {n: list(s.a[n]) for n in ("table", "idx")}
+    s.run(lib(limit=999))
+    assert list(s.a["err"]) == [8, 0] and s.a["count"][0] == 700
+    assert {n: list(s.a[n]) for n in before} == before
+    assert list(s.a["kv"]) == list(s.a["key"]) == [0, 300, 800, 999, 999] and list(s.a["qo"]) == [0, 1, 101, 351, 358]
+    assert list(s.a["pos"]) == [0] * 40 and list(s.a["slots"]) == [-1] * 40
+
+
+@pytest.mark.parametrize("blocks", [1, 2])
+def test_tokens_past_the_largest_index(lib, blocks):
+    """More tokens than an index reaches, on fewer pages: those that the buffers hold are right."""
+    s = Step([30, 1500], [20, 1400], 16, 100, pool=100, blocks=blocks, n_tok=900)
+    s.run(lib(limit=999))
+    want = blk.page_table(s.seq, s.new, s.rows, 16, s.free)
+    # (slots are past the largest index here as well: -1, bit 1)
+    assert list(s.a["err"]) == [9, 0] and s.a["count"][0] == len(s.free)
+    assert list(s.a["pos"]) == want["pos"][:900] and list(s.a["slots"]) == [x if x <= 999 else -1 for x in want["slots"][:900]]
+    assert list(s.a["idx"])[:len(want["idx"])] == want["idx"] and list(s.a["qo"]) == [0, 20, 999]
