@@ -501,7 +501,8 @@ int mla_build_page_table(const mla_tensor_t* seq_lens, const mla_tensor_t* new_l
  * out, their rows of q_out and k_out as they were.
  *   error_word    device int32 (required).  A request whose lists make no sense (token range not
  *                 inside T, page list not monotone or not inside kv_indices, T_b > L_b) appends
- *                 nothing (no k_out either) and sets bit 2; a page outside the cache is skipped
+ *                 nothing (no k_out either) and sets bit 2 (where qo_indptr falls from one entry
+ *                 inside T to another, requests beside it may be left out, too); a page outside the cache is skipped
  *                 and sets bit 64; a rotary position outside [0, max_pos) sets bit 1 and leaves
  *                 that token's rotated columns (of q_out, k_out and its key entry) unwritten.
  */

@@ -207,7 +207,8 @@ __device__ __forceinline__ void turn_queries(const BlockAppendParams& p, int64_t
   const int h0 = static_cast<int>(item - group * strips) * p.strip;
   const int64_t t = group * kRows + lane / kPieces;
   if (t >= p.n_tok) return;
-  const int64_t live = __ldg(p.qo_indptr + p.B);
+  int64_t live = __ldg(p.qo_indptr + p.B);
+  if (live < 0) live = p.n_tok;             // an end that makes no sense
   const int64_t pos = __ldg(p.positions + t);
   const Columns c = columns_of<D>(lane % kPieces, true, p.half_rot);
   const int h1 = h0 + p.strip < p.Hq ? h0 + p.strip : p.Hq;
@@ -269,7 +270,10 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const Blo
   const int heads = p.Hk - first_head < p.part_heads ? p.Hk - first_head : p.part_heads;
   const int bs = 1 << p.log2_block;
   const int log2_unit = p.log2_block > kLog2Unit ? p.log2_block : kLog2Unit;
-  auto start = [&](int b) { return static_cast<int64_t>(__ldg(p.qo_indptr + b) >> log2_unit) + 2 * static_cast<int64_t>(b); };
+  auto start = [&](int b) -> int64_t {      // -1: no token of the call
+    const int64_t t = __ldg(p.qo_indptr + b);
+    return t < 0 || t > p.n_tok ? -1 : (t >> log2_unit) + 2 * static_cast<int64_t>(b);
+  };
   const int b = warp_owner(p.B, lane, slot, start);
   const Request r = request_of(p, b);
   const int64_t t0 = r.t0;
