@@ -196,6 +196,31 @@ __device__ __forceinline__ Request request_of(const BlockAppendParams& p, int b)
   return {t0, static_cast<int>(t1 - t0), held, t0 >= 0 && t1 >= t0 && t1 <= p.n_tok && held >= t1 - t0};
 }
 
+// The first of a request's slots, where its units are.
+__device__ __forceinline__ int64_t first_slot(const BlockAppendParams& p, int b, int log2_unit) {
+  return static_cast<int64_t>(__ldg(p.qo_indptr + b) >> log2_unit) + 2 * static_cast<int64_t>(b);
+}
+// The unit of request b that a slot stands for, the g0-th of the request's positions; no tokens where it is none.
+struct Unit {
+  Request r;
+  int64_t g0;
+  int b;
+};
+__device__ __forceinline__ Unit unit_of(const BlockAppendParams& p, int b, int64_t slot, int log2_unit) {
+  Unit u = {request_of(p, b), 0, b};
+  const int64_t nth = slot - first_slot(p, b, log2_unit);
+  u.g0 = ((u.r.held - u.r.tokens) >> log2_unit) + nth;
+  if (!u.r.sound || nth < 0 || u.g0 << log2_unit >= u.r.held) u.r.tokens = 0;
+  return u;
+}
+// Entries of the token list that lie outside the call lead a search astray: past them, then.
+__device__ __noinline__ int owner_beside_bad_lists(const BlockAppendParams& p, int lane, int64_t slot, int log2_unit) {
+  return warp_owner<true>(p.B, lane, slot, [&](int b) -> int64_t {
+    const int t = __ldg(p.qo_indptr + b);
+    return t < 0 || t > p.n_tok ? -1 : first_slot(p, b, log2_unit);
+  });
+}
+
 // Queries: a warp takes 32 / (D/16) tokens and a strip of up to 4 heads, whose words are all in
 // flight before the angles, which wait for the positions.
 constexpr int kMostStrip = 4;
@@ -270,16 +295,15 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const Blo
   const int heads = p.Hk - first_head < p.part_heads ? p.Hk - first_head : p.part_heads;
   const int bs = 1 << p.log2_block;
   const int log2_unit = p.log2_block > kLog2Unit ? p.log2_block : kLog2Unit;
-  auto start = [&](int b) -> int64_t {      // -1: no token of the call
-    const int64_t t = __ldg(p.qo_indptr + b);
-    return t < 0 || t > p.n_tok ? -1 : (t >> log2_unit) + 2 * static_cast<int64_t>(b);
-  };
-  const int b = warp_owner(p.B, lane, slot, start);
-  const Request r = request_of(p, b);
-  const int64_t t0 = r.t0;
+  Unit found = unit_of(p, warp_owner<false>(p.B, lane, slot, [&](int b) { return first_slot(p, b, log2_unit); }), slot, log2_unit);
+  if (!found.r.tokens) {                    // an idle slot, or hidden by a bad list
+    found = unit_of(p, owner_beside_bad_lists(p, lane, slot, log2_unit), slot, log2_unit);
+    if (!found.r.tokens) return;
+  }
+  const int b = found.b;
+  const Request r = found.r;
+  const int64_t t0 = r.t0, g0 = found.g0;
   const int held = r.held, begin = held - r.tokens;          // the first new position
-  const int64_t g0 = (begin >> log2_unit) + (slot - start(b));
-  if (!r.sound || r.tokens == 0 || slot < start(b) || g0 << log2_unit >= held) return;    // an idle slot
   const int base = static_cast<int>(g0) << log2_unit, end = base + (1 << log2_unit);
   const int lo = begin > base ? begin : base, hi = held < end ? held : end;      // its new positions
 

@@ -22,20 +22,25 @@ struct PageList {
   }
 };
 
-// The last b in [0, n) with start(b) <= x, by a whole warp: 31 probes at a time, so that lists of
-// up to 32 take one round trip to memory, of 1,024 two.  Starts rise, but for those of entries
-// that make no sense, which are negative: the next one that does speaks for a probe's stretch.
-template <class Start>
+// The last b in [0, n) with start(b) <= x, by a whole warp (starts rise): 31 probes at a time, so
+// that lists of up to 32 take one round trip to memory, of 1,024 two.  With kBad, starts may be
+// negative, where a list's entry makes no sense: the next one that does speaks for a probe's stretch.
+template <bool kBad, class Start>
 __device__ __forceinline__ int warp_owner(int n, int lane, int64_t x, Start start) {
   int lo = 0, width = n;                    // the answer lies in [lo, lo + width)
   while (width > 1) {
     const int step = (width + 31) / 32;
     int at = (lane + 1) * step;             // lane 31's probe is never inside
-    const int end = at + step < width ? at + step : width;
-    int64_t s = at < width ? start(lo + at) : -1;
-    while (s < 0 && ++at < end) s = start(lo + at);
-    const uint32_t before = __ballot_sync(0xffffffffu, s >= 0 && s <= x);
-    const int passed = 32 - __clz(before);  // up to the last one
+    bool before;
+    if constexpr (kBad) {
+      const int end = at + step < width ? at + step : width;
+      int64_t s = at < width ? start(lo + at) : -1;
+      while (s < 0 && ++at < end) s = start(lo + at);
+      before = s >= 0 && s <= x;
+    } else {
+      before = at < width && start(lo + at) <= x;
+    }
+    const int passed = 32 - __clz(__ballot_sync(0xffffffffu, before));     // up to the last one
     lo += passed * step;
     width = width - passed * step < step ? width - passed * step : step;
   }
