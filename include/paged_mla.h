@@ -530,7 +530,8 @@ int mla_gqa_block_append(const mla_tensor_t* q, const mla_tensor_t* k, const mla
  *                 multiples of 8 elements, outputs' rows not overlapping)
  *   error_word    device int32 (required).  A request whose lists make no sense (page list, token
  *                 range or row range, or a row range that is not L_b long) is left out and sets
- *                 bit 2; a page outside the cache gives zeros and sets bit 64.
+ *                 bit 2 (where row_indptr falls from one entry inside n to another, requests beside
+ *                 it may be left out, too); a page outside the cache gives zeros and sets bit 64.
  */
 int mla_gqa_block_gather(const mla_tensor_t* k_cache, const mla_tensor_t* v_cache,
                          const mla_tensor_t* k_scale, const mla_tensor_t* v_scale,

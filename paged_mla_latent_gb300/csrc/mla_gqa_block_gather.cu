@@ -71,18 +71,36 @@ __device__ __forceinline__ uint4 widen(const uint2& codes, float scale) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// The last request that starts at or before a row.  Starts rise; with kBad, but for those outside the
+// output: the next one that is not speaks for them.
+template <bool kBad, class Start>
+__device__ __forceinline__ int request_at(const BlockGatherParams& p, int64_t row, Start start) {
+  int lo = 0, hi = p.B;                     // the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    int at = mid;
+    int64_t s = start(at);
+    if constexpr (kBad)
+      while ((s < 0 || s > p.n_rows) && ++at < hi) s = start(at);
+    if (s <= row && (!kBad || at < hi)) lo = at;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // Where a row of the output comes from, by its request's lists.
 template <class Start>
 __device__ __forceinline__ Source source_of(const BlockGatherParams& p, int64_t row, Start start) {
   Source from = {-1, -1};
-  if (row >= p.n_rows || row < start(0) || row >= start(p.B)) return from;
-  int lo = 0, hi = p.B;                     // start(lo) <= row < start(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start(mid) <= row) lo = mid;
-    else hi = mid;
+  if (row >= p.n_rows) return from;
+  int lo = request_at<false>(p, row, start);
+  int64_t s = start(lo), e = start(lo + 1);
+  if (row < s || row >= e || s < 0 || e > p.n_rows) {          // a row of none, or hidden by a bad list
+    lo = request_at<true>(p, row, start);
+    s = start(lo);
+    e = start(lo + 1);
+    if (row < s || row >= e) return from;
   }
-  const int64_t s = start(lo), e = start(lo + 1);
   const int held = p.pages.positions(lo);
   const int64_t idx0 = __ldg(p.pages.indptr + lo);
   int64_t t0 = 0, t1 = 0;
@@ -118,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 4) gqa_block_gather_kernel(const Blo
     __syncthreads();
   }
   auto start = [&](int b) -> int64_t { return fits ? s_start[b] : __ldg(p.row_indptr + b); };
-  const int64_t rows = start(p.B) < p.n_rows ? start(p.B) : p.n_rows;
+  const int64_t end = start(p.B), rows = end < 0 || end > p.n_rows ? p.n_rows : end;
   const bool ahead = tid >= kCopy;
   int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.tile;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * p.tile;

@@ -53,3 +53,30 @@ def test_append_serves_the_requests_beside_a_bad_token_list(pm, n, bad):
         assert _same(got.view(blk.F8), x.view(blk.F8)) if x.dtype == torch.uint8 else _same(got, x)
     assert _same(a.k_out[:total][~gone], k[~gone]) and a.k_out[:total][gone].isnan().all()
     assert _same(a.q_out[:total], q)           # queries need no list but the end of the last one
+
+
+@pytest.mark.parametrize("n,bad", [(3, {1: 1000000}), (4, {0: -1}), (4, {4: 2 ** 31 - 1}), (4, {4: -2 ** 31})] +
+                         [(n, {random.Random(9 * n + i).randrange(0, n + 1): FAR[(n + i) % 4] for i in range(k)})
+                          for n, k in ((5, 1), (5, 2), (33, 5), (700, 5), (1500, 1), (1500, 5))])
+def test_gather_serves_the_requests_beside_a_bad_row_list(pm, n, bad):
+    rng = random.Random(n)
+    held = [rng.choice((0, 1, 3, 40, 70) if n < 100 else (0, 1, 2, 5)) for _ in range(n)]
+    g = blk.gen(n, DEV)
+    pages = blk.Pages(held, 16, 16, DEV)
+    kc, vc, ks, vs = blk.caches(pages.pool, 16, 16, 2, 64, "nhd", DEV)
+    blk.fill(pages, kc, ks, g)
+    blk.fill(pages, vc, vs, g)
+    rows = blk.sums(held, DEV)
+    starts = rows.tolist()
+    for i, x in bad.items():
+        rows[i] = x
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    k_rows, v_rows = (torch.full((sum(held) + 3, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pm.mla_gqa_block_gather(kc, vc, ks, vs, pages.indptr, pages.indices, pages.last, rows, k_rows, v_rows, err)
+    assert err.item() == 2
+    for got, cache, scale in ((k_rows, kc, ks), (v_rows, vc, vs)):
+        want = torch.full_like(got, 7.0)
+        for b in range(n):
+            if held[b] and b not in bad and b + 1 not in bad:
+                want[starts[b]:starts[b + 1]] = blk.values(pages, b, cache, scale).bfloat16()
+        assert _same(got, want)
