@@ -51,7 +51,7 @@ using namespace pmla;
 
 constexpr float kTop = 5.f;            // log2 of a weight at the reference
 constexpr float kRoom = 3.f;           // how far a score may pass it
-constexpr float kNone = -1e30f;        // the reference of a row that has seen no position
+constexpr float kNone = -3.402823466e38f;      // the reference of a row that has seen no position: the lowest finite one
 constexpr int kSoftmaxWarps = 8, kMmaWarp = kSoftmaxWarps, kLoadWarp = kMmaWarp + 1, kScaleWarps = 2;
 
 // D columns, KV heads a unit.
