@@ -180,9 +180,10 @@ class BlockScaledLayer(GroupedHeadLayer):
             raise RuntimeError(f"{pm.mla_status_string(status)}, error bits {bits}")
 
 
-def run_blocks(lens=(37, 400, 1, 129), steps=20, device="cuda"):
+def block_errors(lens=(37, 400, 1, 129), steps=20, device="cuda"):
     """The same for the block-scaled cache: a prompt in two parts, then steps of one to five
-    tokens a request (none, now and then)."""
+    tokens a request (none, now and then).  Returns {(part, request): (largest difference, root mean
+    square of the differences over that of the outputs)}, parts "prompt", "prefix" and "decode"."""
     width = 1024
     counts = [[(i * 7 + 3 * b) % 6 for b in range(len(lens))] for i in range(steps)]
     more = [n // 2 + 20 for n in lens]
@@ -190,17 +191,24 @@ def run_blocks(lens=(37, 400, 1, 129), steps=20, device="cuda"):
     g = torch.Generator(device=device).manual_seed(1)
     xs = [torch.randn(n, width, generator=g, device=device).bfloat16() for n in total]
     layer = BlockScaledLayer(len(lens), width, device=device)
-    whole = GroupedHeadLayer(width, device=device).prompt(xs).float()
-    at, worst = [0] * len(lens), 0.0
-    starts = [sum(total[:b]) for b in range(len(lens))]
-    for new in [lens, more] + counts:
+    whole = GroupedHeadLayer(width, device=device).prompt(xs).float().split(total)
+    at, rows = [0] * len(lens), {}
+    for part, new in [("prompt", lens), ("prefix", more)] + [("decode", c) for c in counts]:
         o = layer.forward([x[a:a + n] for x, a, n in zip(xs, at, new)]).float()
-        want = torch.cat([whole[s + a:s + a + n] for s, a, n in zip(starts, at, new)])
+        for b, (got, w, a, n) in enumerate(zip(o.split(list(new)), whole, at, new)):
+            if n:
+                rows.setdefault((part, b), []).append((got, w[a:a + n]))
         at = [a + n for a, n in zip(at, new)]
-        if o.numel():
-            worst = max(worst, (o - want).abs().max().item())
     layer.check()
-    return worst
+    out = {}
+    for key, pairs in rows.items():
+        got, want = (torch.cat(x) for x in zip(*pairs))
+        out[key] = (got - want).abs().max().item(), ((got - want).norm() / want.norm()).item()
+    return out
+
+
+def run_blocks(lens=(37, 400, 1, 129), steps=20, device="cuda"):
+    return max(largest for largest, _ in block_errors(lens, steps, device).values())
 
 
 if __name__ == "__main__":
