@@ -6,7 +6,8 @@ Every function here has the name of the C entry point it calls in
 a compiled module, and passes the current CUDA stream.  Calls run on the
 device of their tensors, whichever one is current.  All arithmetic runs in the library's
 CUDA kernels; there is no Python or CPU fallback: if the library cannot
-be loaded, importing this package raises.
+be loaded, importing this package raises, and calls that go through the module raise
+where it is missing.
 
 The operation ("[Kimi-K3 MLA TP8] MLA performance", §2-§5; "Scaling Kimi K3 on AMD
 Instinct MI355X", §1 and §4): absorbed MLA decode over a paged FP8 cache (one token a
@@ -62,7 +63,7 @@ class MlaError(RuntimeError):
 
 
 def _load() -> ctypes.CDLL:
-    path = _build.build()   # no-op when the in-tree library is up to date
+    path = _build.build_library()   # no-op when the in-tree library is up to date
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(MlaTensor)
     c_i32, c_sz, vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
@@ -117,11 +118,24 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+class _NoModule:
+    """Stands for the call module where it cannot be loaded: the calls that need it raise."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs the call module {_build.NATIVE_PATH}: {self._why}")
+
+
 def _load_native():
     """The module whose calls take torch tensors (built next to the library, which it links)."""
-    spec = importlib.util.spec_from_file_location("pmla_native", _build.NATIVE_PATH)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        spec = importlib.util.spec_from_file_location("pmla_native", _build.build_native())
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except (ImportError, OSError, RuntimeError) as e:
+        return _NoModule(e)
     return module
 
 
