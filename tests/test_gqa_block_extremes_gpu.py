@@ -45,3 +45,52 @@ def test_decode_of_equal_scores_far_from_zero(pm, D, rows, new, q):
             else:
                 assert (o[at + t] == 0).all() and torch.isneginf(lse[at + t]).all()
         at += new
+
+
+def _scales(c, g, span, zero=None):
+    """Scales of v over `span` powers of two and of k up to twice what they were, none a power of two;
+    zero: positions of request 0 whose codes and scales are zero."""
+    c.vs.copy_(torch.where(c.vs.isnan(), c.vs, torch.exp2(torch.rand(c.vs.shape, generator=g, device=DEV) * span - span / 2)))
+    c.ks.copy_(torch.where(c.ks.isnan(), c.ks, c.ks * (1 + torch.rand(c.ks.shape, generator=g, device=DEV))))
+    if zero:
+        at = c.pages.where(0, *zero)
+        for cache, scale in ((c.kc, c.ks), (c.vc, c.vs)):
+            cache.view(torch.uint8)[at] = 0
+            scale[at[0], at[1] // c.pages.bs] = 0
+
+
+@pytest.mark.parametrize("span", [4, 20, 40])
+@pytest.mark.parametrize("held,new,Hq,Hk,D,ps,bs,layout", [
+    ([200, 1, 77], [1, 1, 1], 20, 1, 128, 16, 16, "nhd"),
+    ([200, 31, 777], [4, 3, 4], 16, 2, 128, 64, 16, "hnd"),
+    ([400, 31, 777], [4, 3, 4], 16, 2, 64, 16, 4, "nhd"),
+    ([400, 64, 9001], [2, 1, 2], 36, 3, 64, 128, 128, "shared"),
+    ([30001], [3], 8, 1, 128, 8, 1, "nhd"),
+])
+def test_decode_of_many_rows_and_scales_far_apart(pm, held, new, Hq, Hk, D, ps, bs, layout, span):
+    """As test_decode_scales_far_apart, with more than 16 query rows a KV head."""
+    c = Decode(held, new, Hq, Hk, D, ps, bs, layout)
+    _scales(c, blk.gen(5, DEV), span, (128, 144))
+    o, lse, ws = c.run(pm, torch.float32)
+    assert pm.mla_check_error(ws) == 0
+    c.check(o, lse, str(span), blk.LOST_MANY)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,new", [(4, 1), (3, 4), (20, 1), (8, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_into_outputs_with_strides(pm, D, rows, new, dtype):
+    """Rows apart, heads outside tokens, slices of wider tensors: the same bits, and nothing beside them."""
+    c = Decode([300, 0, 5, 9001], [new] * 4, 2 * rows, 2, D, 16, 16, pad=3)
+    want, lse, ws = c.run(pm, dtype)
+    n, (T, H, _) = 4 * new, c.q.shape
+    for wide, view in ((torch.full((T, H, D + 3), 7.0, dtype=dtype, device=DEV), lambda x: x[:, :, :D]),
+                       (torch.full((H, T + 1, D), 7.0, dtype=dtype, device=DEV), lambda x: x[:, 1:].transpose(0, 1)),
+                       (torch.full((T, 3, H, D), 7.0, dtype=dtype, device=DEV), lambda x: x[:, 1])):
+        o = view(wide)
+        pm.mla_gqa_block_decode(c.q, c.kc, c.vc, c.ks, c.vs, o, c.qo, c.pages.indptr, c.pages.indices, c.pages.last,
+                                new, c.sm, workspace=ws)
+        assert pm.mla_check_error(ws) == 0
+        assert torch.equal(o[:n], want[:n])
+        o[:n] = 7.0
+        assert (wide == 7.0).all()
