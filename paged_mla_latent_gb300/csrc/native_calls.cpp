@@ -63,7 +63,7 @@ struct Arg<const mla_tensor_t*> {
         PyErr_Format(PyExc_TypeError, "unsupported dtype %s", c10::toString(t->scalar_type()));
         return nullptr;
     }
-    d.ptr = const_cast<void*>(t->const_data_ptr());
+    d.ptr = t->mutable_data_ptr();           // (a lazy clone gets its own memory: it may be an output)
     d.ndim = static_cast<int32_t>(t->dim());
     for (int i = 0; i < d.ndim; ++i) {
       d.shape[i] = t->size(i);
