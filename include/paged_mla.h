@@ -559,9 +559,8 @@ int mla_get_gqa_block_decode_workspace_size(int32_t num_heads, int32_t num_kv_he
  * weights times their v scale are rounded to 11 bits for the product with the codes, those below
  * 2^-38 of the largest are lost; with more than 16 rows a KV head (G * max_seqlen_q) they may be
  * rounded to multiples of 2^-24 of the largest besides.  Scales of v are finite and not negative; one
- * below 2^-60 (zero among them) counts as 2^-60.  A NaN code or scale among the new tokens' values
- * reaches all of the request's rows of that KV head, those that do not see it too; what lies behind
- * the request's list reaches none.
+ * below 2^-60 (zero among them) counts as 2^-60.  A NaN code or scale reaches the rows that see its
+ * position, of its KV head, and no others; what lies behind the request's list reaches none.
  *   q             (sum_T, Hq, D) BF16, D 64 or 128, as above
  *   o             (sum_T, Hq, D) BF16 or FP32, last dim contiguous, no two rows overlapping
  *                 (written; rows of no request are not)

@@ -70,10 +70,12 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint
       : "r"(codes));
 }
 
-// D columns, n-tiles of 8 query rows of a head, KV heads a unit, warps a CTA.
-template <int D_, int NT_, int HP_, int W_>
+// D columns, n-tiles of 8 query rows of a head, KV heads a unit, warps a CTA, whether a request may
+// have several new tokens.
+template <int D_, int NT_, int HP_, int W_, bool kMany_>
 struct BlockShape {
   static constexpr int D = D_, NT = NT_, HP = HP_;
+  static constexpr bool kMany = kMany_;
   static constexpr int CT = NT * HP;                       // column tiles of 8 rows
   static constexpr int kWarps = W_, kThreads = 32 * W_;
   static constexpr int kJoinWarps = kWarps, kJoinThreads = kThreads;
@@ -94,7 +96,7 @@ struct BlockShape {
   static constexpr int kPieceBytes = 2 * kMaxCtas * kRows * 4;     // m and l of a unit's pieces, over them too
   static constexpr int kOverBytes = kJoinBytes > kPieceBytes ? kJoinBytes : kPieceBytes;
   static constexpr int kBuf = kWarps * kWarpBytes > kOverBytes ? kWarps * kWarpBytes : kOverBytes;
-  static constexpr int kSmem = kBuf + 2 * kWarps * kRows * 4 + kRows * D * 2 + kRows * 4;
+  static constexpr int kSmem = kBuf + 2 * kWarps * kRows * 4 + kRows * D * 2 + kRows * 4 + (kMany ? sizeof(NanMarks) : 0);
   static_assert(kCtasPerSm * (kSmem + 1024 + 64) <= 233472, "shared memory of a SM");
   static constexpr int kSlotFloats = kRows * (D + 2);
   static constexpr bool kTwo = kRows * D > 4 * kThreads;   // a join's thread has two words of o
@@ -149,11 +151,24 @@ __device__ __forceinline__ void stage_queries(const BlockDecodeParams& p, const 
   }
 }
 
+// New tokens' values that are NaN, of a tile's rows that not all query rows see: marked.
+template <class S>
+__device__ __noinline__ void clean_values(uint8_t* v, float* scales, NanMarks* marks, int at0, int from, int end, int lane) {
+  constexpr int kChunks = S::kRow / 16, kTile = S::kTile;
+  if (from < 0) from = 0;
+  if (end > kTile) end = kTile;
+#pragma unroll 1
+  for (int e = kChunks * from + lane; e < kChunks * end; e += 32)
+    marks->look(reinterpret_cast<uint4*>(v + chunk_at<S::kRow>(e / kChunks, e % kChunks)), at0 + e / kChunks, 16 * (e % kChunks));
+  if (lane >= from && lane < end)
+    for (int hp = 0; hp < S::HP; ++hp) marks->look(scales + hp * kTile + lane, at0 + lane, hp);
+}
+
 // The warp's tiles of a piece: output, maximum and sum of its rows (o's columns 16 i + 2 g and
 // the next of rows 2 cq, 2 cq + 1 of each column tile; m and l of those rows, l per lane).
 template <class S>
 __device__ __forceinline__ void walk_tiles(const BlockDecodeParams& p, const Piece& u, uint8_t* smem, uint8_t* s_q,
-                                           float* s_sc, int warp, int lane, float (&acc)[S::CT][S::D / 16][4],
+                                           float* s_sc, NanMarks* marks, int warp, int lane, float (&acc)[S::CT][S::D / 16][4],
                                            float (&m)[S::CT][2], float (&l)[S::CT][2]) {
   constexpr int D = S::D, NT = S::NT, HP = S::HP, CT = S::CT, MT = S::MT, kTile = S::kTile, kRow = S::kRow;
   constexpr int kStages = S::kStages;
@@ -234,6 +249,7 @@ __device__ __forceinline__ void walk_tiles(const BlockDecodeParams& p, const Pie
     page = ahead[kStages - 1];
   }
   stage_queries<S>(p, u, s_q, s_sc, warp, lane);
+  if constexpr (S::kMany) marks->clear(32 * warp + lane, S::kThreads);
   __syncthreads();
   uint32_t qf[CT][D / 32][4];              // of two 16-column steps
   float sc[CT][2];                         // of rows 2 cq, 2 cq + 1
@@ -259,7 +275,13 @@ __device__ __forceinline__ void walk_tiles(const BlockDecodeParams& p, const Pie
       t_load += S::kWarps;
     }
     const uint32_t kt = ring + stage * S::kStageBytes, vt = kt + kTile * kRow;
-    const float* scales = reinterpret_cast<const float*>(ring_ptr + stage * S::kStageBytes + S::kTileBytes);
+    float* scales = reinterpret_cast<float*>(ring_ptr + stage * S::kStageBytes + S::kTileBytes);
+    if constexpr (S::kMany)
+      if ((t + 1) * kTile > least) {
+        const int at0 = t * kTile;
+        clean_values<S>(ring_ptr + (stage * S::kStageBytes + kTile * kRow), scales + HP * kTile, marks, at0, least - at0, len - at0, lane);
+        __syncwarp();
+      }
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
     float s[CT][MT][4];
@@ -394,6 +416,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
   float* s_l = s_m + kWarps * kRows;
   float* s_sc = s_l + kWarps * kRows;                          // [row]
   uint8_t* s_q = reinterpret_cast<uint8_t*>(s_sc + kRows);     // [row][D], f16
+  NanMarks* marks = reinterpret_cast<NanMarks*>(s_q + kRows * D * 2);      // of the piece
   __shared__ SpanShared<kWarps> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, cq = lane & 3;
@@ -413,7 +436,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
       m[ct][0] = m[ct][1] = -INFINITY;
       l[ct][0] = l[ct][1] = 0.f;
     }
-    walk_tiles<S>(p, u, smem, s_q, s_sc, warp, lane, acc, m, l);
+    walk_tiles<S>(p, u, smem, s_q, s_sc, marks, warp, lane, acc, m, l);
 
     // ---- the warps' partial results meet in shared memory (over the idle rings)
 #pragma unroll
@@ -461,6 +484,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtasPerSm) gqa_block_decode_k
         oo[2] += f * y.z;
         oo[3] += f * y.w;
       }
+      if constexpr (S::kMany)
+        if (marks->any) {
+          const int hp = h / S::kHeads, seen = u.r.len - u.r.tokens + 1 + (u.h0 + h % S::kHeads) / p.G;
+          for (int i = 0; i < 4; ++i)
+            if (marks->reach(hp * D + d + i, hp, seen)) oo[i] = NAN;
+          if (marks->scale[hp] < seen) ll = NAN;
+        }
       if (whole) {
         finish_row<S, 4>(p, u, h, d, oo, mm, ll);
       } else {
@@ -488,9 +518,9 @@ size_t workspace_for(int sms, int64_t rows, int64_t D, int64_t Hk) {
          2 * 2 * static_cast<size_t>(sms) * 8 * row_tiles(rows) * unit_heads(D, Hk) * static_cast<size_t>(D + 2) * 4;
 }
 
-template <int D, int NT, int HP, int W>
+template <int D, int NT, int HP, int W, bool kMany>
 cudaError_t launch_as(const BlockDecodeParams& p, int sms, cudaStream_t stream) {
-  using S = BlockShape<D, NT, HP, W>;
+  using S = BlockShape<D, NT, HP, W, kMany>;
   static std::mutex mu;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -515,8 +545,9 @@ template <int D, int NT, int HP>
 cudaError_t launch(const BlockDecodeParams& p, int sms, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.G) * p.max_q;
   const int64_t units = static_cast<int64_t>(p.B) * ((p.Hk + HP - 1) / HP) * ((rows + 8 * NT - 1) / (8 * NT));
-  if (units <= sms) return launch_as<D, NT, HP, 8>(p, sms, stream);
-  return launch_as<D, NT, HP, 4>(p, sms, stream);
+  // (One new token sees all positions: without the marks of those that others do not.)
+  if (units <= sms) return p.max_q == 1 ? launch_as<D, NT, HP, 8, false>(p, sms, stream) : launch_as<D, NT, HP, 8, true>(p, sms, stream);
+  return p.max_q == 1 ? launch_as<D, NT, HP, 4, false>(p, sms, stream) : launch_as<D, NT, HP, 4, true>(p, sms, stream);
 }
 
 template <int D, int HP>

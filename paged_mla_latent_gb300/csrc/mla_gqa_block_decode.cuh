@@ -58,6 +58,46 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Positions that some rows of a unit see and some do not are the new tokens' but the first.  A NaN
+// among their values would reach all rows, zero times NaN being NaN.  So values that are NaN give
+// way (codes to zero, scales to one), and the first such position is kept for the rows that see it:
+// of each column, and of each head's scales.
+constexpr int kNoPosition = 0x7FFFFFFF;
+struct NanMarks {
+  int first[128], scale[2];
+  int any;
+  __device__ __forceinline__ void clear(int i, int step) {
+    for (int c = i; c < 128; c += step) first[c] = kNoPosition;
+    if (i < 2) scale[i] = kNoPosition;
+    if (i == 2) any = 0;
+  }
+  // Whether the column, of the unit's head hp, is NaN in a row that sees `seen` positions.
+  __device__ __forceinline__ bool reach(int column, int hp, int seen) const {
+    return first[column] < seen || scale[hp] < seen;
+  }
+  __device__ __noinline__ void drop(uint4* chunk, int at, int column) {
+    any = 1;
+    uint8_t* const code = reinterpret_cast<uint8_t*>(chunk);
+    for (int b = 0; b < 16; ++b)
+      if ((code[b] & 0x7F) == 0x7F) {
+        atomicMin(first + column + b, at);
+        code[b] = 0;
+      }
+  }
+  // 16 codes of position `at` from a column on.
+  __device__ __forceinline__ void look(uint4* chunk, int at, int column) {
+    const uint4 w = *chunk;
+    auto sevens = [](uint32_t x) { return (x & 0x7F7F7F7Fu) + 0x01010101u; };      // 0x80 where a byte is 0x7F or 0xFF
+    if ((sevens(w.x) | sevens(w.y) | sevens(w.z) | sevens(w.w)) & 0x80808080u) drop(chunk, at, column);
+  }
+  __device__ __forceinline__ void look(float* v_scale, int at, int hp) {
+    if (!isnan(*v_scale)) return;
+    any = 1;
+    atomicMin(scale + hp, at);
+    *v_scale = 1.f;
+  }
+};
+
 // The line of work, of all requests or of those before one: tiles of all units, and units.
 struct Line {
   int64_t tiles, units;

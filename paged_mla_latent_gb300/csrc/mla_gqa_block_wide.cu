@@ -71,7 +71,11 @@ struct WideShape {
   static constexpr int kScaleOff = kQOff + (kJoinBytes > kQBytes + 2 * kPBytes ? kJoinBytes : kQBytes + 2 * kPBytes),
                        kStageScales = 2 * HP * kTile;   // floats: K's, V's
   static constexpr int kMisc = kScaleOff + kStages * kStageScales * 4;
-  static constexpr int kSmem = kMisc + 2048;
+  // NaN among new tokens' values, by piece: the scale warps are at most kStages tiles ahead of the
+  // weights, each of another piece, and what a piece has is read while its weights' last product is awaited
+  static constexpr int kMarks = kMisc + 2048, kMarkPieces = 8;
+  static_assert(kMarkPieces >= kStages + 2, "");
+  static constexpr int kSmem = kMarks + kMarkPieces * sizeof(NanMarks);
   static_assert(kMisc % 16 == 0 && kQOff % 1024 == 0 && kPOff % 1024 == 0 && kScaleOff % 16 == 0, "");
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
   static constexpr int kJoinWarps = kMmaWarp + 1, kJoinThreads = 32 * kJoinWarps;
@@ -93,12 +97,14 @@ struct WideMisc {                              // m, sc, l and part are read 16 
   int64_t out[32];                             // where a row's output goes, -1: nowhere
   uint32_t tmem;
   int abort_flag;
+  uint32_t pieces;                             // of the softmax warps, the one at hand the last
 };
 static_assert(sizeof(WideMisc) <= 2048 && offsetof(WideMisc, m) % 16 == 0 && offsetof(WideMisc, sc) % 16 == 0 &&
                   offsetof(WideMisc, l) % 16 == 0 && offsetof(WideMisc, part) % 16 == 0 && offsetof(WideMisc, out) % 8 == 0,
               "");
 
-// Barriers of a group of 128 threads.
+// Barriers: of the scale warps, of a group of 128 threads.
+__device__ __forceinline__ void bar_scales() { asm volatile("bar.sync 4, %0;" ::"n"(32 * kScaleWarps) : "memory"); }
 __device__ __forceinline__ void bar_group(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 __device__ __forceinline__ bool any_group(int g, bool x) {
   uint32_t r;
@@ -204,6 +210,49 @@ __device__ __forceinline__ void stage_queries(const BlockDecodeParams& p, const 
   }
 }
 
+// A tile's values, by the scale warps.  What lies behind the list may be NaN: zeros instead.  So may
+// new tokens' values, in rows that not all query rows see, from `from` to `end`: marked.
+template <class S>
+__device__ __forceinline__ void clean_values(uint8_t* v, float* scales, NanMarks* marks, int tile0, int from, int end, int thread) {
+  constexpr int kTile = S::kTile, kStep = 32 * kScaleWarps;
+#pragma unroll 1
+  for (int row = thread; row < kTile; row += kStep) {
+    if (row >= end) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + row * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+    } else if (row >= from) {
+      for (int h = 0; h < S::HP; ++h) marks->look(scales + h * kTile + row, tile0 + row, h);
+    }
+  }
+#pragma unroll 1
+  for (int e = 8 * (from > 0 ? from : 0) + thread; e < 8 * (end < kTile ? end : kTile); e += kStep)     // (16-byte chunks)
+    marks->look(reinterpret_cast<uint4*>(v + atom_at(e >> 3, e & 7)), tile0 + (e >> 3), 16 * (e & 7));
+}
+
+template <class S>
+__device__ __noinline__ void clean_values_call(uint8_t* v, float* scales, NanMarks* marks, int tile0, int from, int end, int thread) {
+  clean_values<S>(v, scales, marks, tile0, from, end, thread);
+}
+
+// NaN in the rows of a piece that see one among the new tokens' values: a thread a column, in rows'
+// outputs; and a thread a row, in their lse (or in a part's sums).  The head's rows start at r0.
+template <class S>
+__device__ __noinline__ void mark_rows(const NanMarks& marks, const int64_t* out, void* o, bool bf16, int r0, int G, int least,
+                                       int thread, float* sums, int64_t lse0, int Hq) {
+  const int column = thread & 127;
+  for (int row = thread >> 7; row < S::kRows && thread < 256; row += 2) {
+    const int hp = row / S::kHeads;
+    if (out[row] < 0 || (S::HP > 1 && column / S::D != hp) || !marks.reach(column, hp, least + (r0 + row % S::kHeads) / G)) continue;
+    if (bf16) static_cast<__nv_bfloat16*>(o)[out[row] + column % S::D] = __float2bfloat16_rn(NAN);
+    else static_cast<float*>(o)[out[row] + column % S::D] = NAN;
+  }
+  if (thread < S::kRows && out[thread] >= 0 && sums) {
+    const int hp = thread / S::kHeads, r = r0 + thread % S::kHeads, of = r / G;
+    if (marks.scale[hp] < least + of)
+      sums[lse0 < 0 ? thread : lse0 + static_cast<int64_t>(of) * Hq + hp * G + r - of * G] = NAN;
+  }
+}
+
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const BlockDecodeParams p) {
@@ -234,6 +283,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
     }
     mbar_init(bar(&misc->drain), 1);
     *abort_flag = 0;
+    misc->pieces = ~0u;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -246,8 +296,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
   const uint32_t tmem = misc->tmem;
 
   uint32_t done = 0;                         // the CTA's tiles before this piece
+  NanMarks* const all_marks = reinterpret_cast<NanMarks*>(smem + S::kMarks);
   bool ok = true;                            // MMA and copying warps: no wait has given up
-  uint32_t issued = 0;                       // tiles that the copying warp has asked for
+  uint32_t issued = 0;                       // tiles that the copying warp has asked for, pieces of the scale warps
   auto wait = [&](const uint64_t* b, uint32_t parity) {
     if (ok) ok = warp_bcast(mbar_wait(bar(b), parity, abort_flag, p.err));
     return ok;
@@ -292,6 +343,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
     }
     if (warp > kLoadWarp) {
       // ---- scales: two positions a lane, the loads of four tiles in flight
+      NanMarks* const marks = all_marks + issued++ % S::kMarkPieces;
+      const int least = len - u.r.tokens + 1;            // positions that every row sees
+      marks->clear(tid - 32 * (kLoadWarp + 1), 32 * kScaleWarps);
+      __syncwarp();
+      bar_scales();
       constexpr int kMine = 4 / kScaleWarps, kBatch = 4;
       const int row0 = 32 * (warp - kLoadWarp - 1) + lane;
       const int ps_mask = (1 << p.pages.log2_page) - 1;
@@ -334,17 +390,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
           for (int k = 0; k < kMine; ++k)
 #pragma unroll
             for (int h = 0; h < 2 * HP; ++h) s_scale[h * kTile + row0 + 32 * kScaleWarps * k] = sc[b][k][h];
-          // What lies behind the list may be NaN: zeros instead.  Weights, which come after the
-          // scales, keep the product waiting.
-          if (const int end = len - (u.t0 + i) * kTile; end < kTile) {
+          // Weights, which come after the scales, keep the product waiting.
+          if (const int tile0 = (u.t0 + i) * kTile; tile0 + kTile > least) {
             mbar_wait(bar(misc->full + stage), (it / kStages) & 1, abort_flag, p.err);
-#pragma unroll 1
-            for (int row = row0; row < kTile; row += 32 * kScaleWarps)
-              if (row >= end)
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(smem + stage * S::kStageBytes + S::kHalf + row * 128 + 16 * c) =
-                      make_uint4(0, 0, 0, 0);
+            // (As a call where units have one head, in place where they have two: 115 and 71 us for four
+            // tokens of eight heads, 128 and 64 wide; a call for both 115 and 76, in place 118 and 71.)
+            uint8_t* const v = smem + stage * S::kStageBytes + S::kHalf;
+            float* const v_scale = s_scale + HP * kTile;
+            if constexpr (HP == 1) clean_values_call<S>(v, v_scale, marks, tile0, least - tile0, len - tile0, row0);
+            else clean_values<S>(v, v_scale, marks, tile0, least - tile0, len - tile0, row0);
             fence_proxy_async_smem();
           }
           mbar_arrive(bar(misc->scales + stage));
@@ -515,6 +569,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
       const float sum = over_lanes<false>(l, lane);
       if ((lane & 1) == 0) misc->part[c0 + row16(lane)][warp & 3] = sum;
       bar_group(grp);
+      if (tid == 0) ++misc->pieces;            // (read between this piece's last barrier and the next one's first)
       const bool whole = u.t0 == 0 && u.t1 == u.n_tiles;
       float* slot = part_slot<S>(p, u);
       if (prow < 16) {
@@ -565,6 +620,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
     done += n;
     S::join_sync();                          // the piece's MMAs are done, its rows written
     tc_fence_after();
+    if (const NanMarks* marks = all_marks + misc->pieces % S::kMarkPieces; marks->any) {
+      const bool whole = u.t0 == 0 && u.t1 == u.n_tiles;
+      mark_rows<S>(*marks, misc->out, whole ? p.o : part_slot<S>(p, u), whole && !p.o_f32, u.h0, p.G, len - u.r.tokens + 1, tid,
+                   whole ? p.lse : part_slot<S>(p, u) + kRows, whole ? u.tok0 * p.Hq + u.hk0 * p.G : -1, p.Hq);
+    }
     if (!(u.t0 == 0 && u.t1 == u.n_tiles)) {
       join_parts<S>(p, span, u, &sh, misc->m, misc->l, reinterpret_cast<float*>(smem + S::kQOff));
       S::join_sync();
