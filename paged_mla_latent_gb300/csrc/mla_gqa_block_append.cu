@@ -497,11 +497,12 @@ int launch(BlockAppendParams& p, int sms, cudaStream_t s) {
   if (ctas > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
   p.kv_ctas = static_cast<unsigned>(kv_ctas);
   p.q_ctas = static_cast<unsigned>(q_ctas);
-  // Keys and values, the longer chains, come first; where they are more than two waves (three blocks a
-  // SM) every other block turns queries, which stream while the others wait: 16,384 tokens in
-  // blocks of 64, 1,056 blocks here, 73.4 us (76.7 with keys and values first), in blocks of 16, 2,080,
-  // 76 (81); 37 chunks, 742 blocks, 17.2 and 14.8; 8,192 tokens, 544 blocks, 41.1 and 41.5.
-  p.every = kv_ctas > 6 * static_cast<int64_t>(sms) && q_ctas >= kv_ctas ? 2 : 1;
+  // Keys and values, the longer chains, come first; where their units, without the slots between
+  // requests, are more than two waves (three blocks a SM) every other block turns queries, which stream
+  // while the others wait.  Units, us with keys and values first and in turns: prompts of one length
+  // 512 41.3 and 41.0, 768 58.8 and 55.6, 1,024 77.2 and 73.7, 2,048 150 and 144; ragged chunks 334 15.2
+  // and 17.6, 612 28.0 and 29.1, 852 33.5 and 34.2, 1,704 73.2 and 67.2.
+  p.every = (p.n_tok >> unit) * p.parts > 6 * static_cast<int64_t>(sms) && q_ctas >= kv_ctas ? 2 : 1;
   gqa_block_append_kernel<D, kNeox><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
