@@ -205,11 +205,14 @@ struct Unit {
   Request r;
   int64_t g0;
   int b;
+  bool sure;                                // that it is no other request's
 };
 __device__ __forceinline__ Unit unit_of(const BlockAppendParams& p, int b, int64_t slot, int log2_unit) {
-  Unit u = {request_of(p, b), 0, b};
-  const int64_t nth = slot - first_slot(p, b, log2_unit);
+  Unit u = {request_of(p, b), 0, b, false};
+  const int64_t nth = slot - first_slot(p, b, log2_unit), t1 = u.r.t0 + u.r.tokens;
   u.g0 = ((u.r.held - u.r.tokens) >> log2_unit) + nth;
+  u.sure = nth >= 0 && u.r.t0 >= 0 && u.r.tokens >= 0 && t1 <= p.n_tok &&
+           (b + 1 == p.B || slot < (t1 >> log2_unit) + 2 * static_cast<int64_t>(b + 1));
   if (!u.r.sound || nth < 0 || u.g0 << log2_unit >= u.r.held) u.r.tokens = 0;
   return u;
 }
@@ -297,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_block_append_kernel(const Blo
   const int log2_unit = p.log2_block > kLog2Unit ? p.log2_block : kLog2Unit;
   Unit found = unit_of(p, warp_owner<false>(p.B, lane, slot, [&](int b) { return first_slot(p, b, log2_unit); }), slot, log2_unit);
   if (!found.r.tokens) {                    // an idle slot, or hidden by a bad list
+    if (found.sure) return;
     found = unit_of(p, owner_beside_bad_lists(p, lane, slot, log2_unit), slot, log2_unit);
     if (!found.r.tokens) return;
   }
