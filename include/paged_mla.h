@@ -555,12 +555,16 @@ int mla_get_gqa_block_decode_workspace_size(int32_t num_heads, int32_t num_kv_he
  * head h / G, over positions j <= L_b - T_b + t (as mla_decode: causal among the new tokens):
  *   s_j = sm_scale * kscale(j) * sum_d q[r, h, d] * kcode_j[d],   r = qo_indptr[b] + t
  *   lse = ln sum_j exp(s_j),   o[r, h] = sum_j exp(s_j - lse) * vscale(j) * vcode_j
- * No position (or no finite maximum) gives o = 0 and lse = -inf.  Sums and maxima are fp32; the
- * weights times their v scale are rounded to 11 bits for the product with the codes, those below
- * 2^-38 of the largest are lost; with more than 16 rows a KV head (G * max_seqlen_q) they may be
- * rounded to multiples of 2^-24 of the largest besides.  Scales of v are finite and not negative; one
- * below 2^-60 (zero among them) counts as 2^-60.  A NaN code or scale reaches the rows that see its
- * position, of its KV head, and no others; what lies behind the request's list reaches none.
+ * No position (or every score -inf) gives o = 0 and lse = -inf; a score of +inf or NaN gives NaN.
+ * Sums and maxima are fp32.  For the product with the codes the weights times their v scale are
+ * rounded to 11 bits, below 2^-28 of a row's largest to multiples of 2^-38 of it; with more than 16
+ * rows a KV head (G * max_seqlen_q) it may be multiples of 2^-24 of it below 2^-13.  Half a multiple
+ * each at most is lost so, times the position's code, in o (not in lse), and adds up over positions:
+ * in all at most 2^-8 of the largest times the mean |code| for 131,072 of them, 2^-5 for 1,048,576.
+ * Which kernel runs, and with it the last bits, follows from shapes, strides and the length of
+ * kv_indices.  Scales of v are finite and not negative; one below 2^-60 (zero among them) counts as
+ * 2^-60.  A NaN code or scale reaches the rows that see its position, of its KV head, and no others;
+ * what lies behind the request's list reaches none.
  *   q             (sum_T, Hq, D) BF16, D 64 or 128, as above
  *   o             (sum_T, Hq, D) BF16 or FP32, last dim contiguous, no two rows overlapping
  *                 (written; rows of no request are not)

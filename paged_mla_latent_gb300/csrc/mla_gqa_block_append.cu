@@ -20,8 +20,8 @@
 // the same launch, a warp four (or eight) tokens and up to four heads.
 //
 // Measured (one GB300, in a CUDA graph): 16,384 tokens, 32/8 heads of 128, blocks of 64, rotated
-// keys kept, 411 MB: 73 us, 5.6 TB/s (0.84 of the copy rate; with keys and values before the
-// queries 76, so with units of 8 heads 82, of 2 83, without the L2 prefetch 78); 37 requests of 1 to
+// keys kept, 411 MB: 74 us, 5.5 TB/s (0.83 of the copy rate; with keys and values before the
+// queries 77, so with units of 8 heads 82, of 2 83, without the L2 prefetch 78); 37 requests of 1 to
 // 700 tokens, 25/5 heads of 64, 49 MB: 15 us; one token of 64 requests, 16/2 heads: 5 us, a chain of
 // request, lists, page, scale and words.
 #include <cuda_bf16.h>

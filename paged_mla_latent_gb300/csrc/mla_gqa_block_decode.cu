@@ -25,14 +25,18 @@
 // 64-wide heads are taken in pairs, 128 bytes of a slot at a time: alone they use half of every
 // line that DRAM delivers (64 requests of 32,768 positions, two heads: 170 us alone, 103 paired).
 // A unit has at most 16 rows of each head.  More go to the kernel of mla_gqa_block_wide.cu, which feeds
-// the codes to tcgen05 (64 requests of 2,048 to 65,536 positions, four tokens of eight heads: 114
+// the codes to tcgen05 (64 requests of 2,048 to 65,536 positions, four tokens of eight heads: 116
 // us), or, where the cache's layout is none for it, run here in units of 16 that read the cache again
 // (187; 32 rows in one unit fit the registers with nothing beside them: 209).
 //
+// With several new tokens a NaN among their values must not reach rows that do not see it (zero times
+// NaN): edge tiles are looked over, and rows marked at a piece's end (64 requests of 8,192, two tokens of
+// eight heads: 65.5 us, 63 without).
+//
 // Measured (one GB300, in a CUDA graph): 64 requests of 2,048 to 65,536 positions, 16/2 heads of 128, 507
-// MB: 86 us, 5.9 TB/s (0.87 of the copy rate); one of 142,000, 64/8 heads: 57 us, of which 44 stream the
+// MB: 86 us, 5.9 TB/s (0.88 of the copy rate); one of 142,000, 64/8 heads: 56 us, of which 44 stream the
 // cache and the rest are the plan, the first tiles and the join; 37 of up to 4,089, 20/4 heads of 64: 12
-// us; one of 137, 32/8 heads: 5.9 us.
+// us; one of 137, 32/8 heads: 6.2 us.
 //
 // Also tried: e4m3 MMAs (m16n8k32) with q and P as two codes each, whose operands the compiler
 // converts to f16 all the same (102 us for 64 requests of 16,384 positions, two KV heads; 91 as
@@ -560,7 +564,8 @@ cudaError_t launch(const BlockDecodeParams& p, int64_t D, int sms, cudaStream_t 
   if (D == 128) return launch<128, 1>(p, sms, s);
   // Pairs halve the units, which costs where caches lie in L2: one head each where the page list has
   // room for no more than 32 MB (37 requests of up to 4,089 positions, four heads: 11.5 us alone,
-  // 13.0 in pairs; 64 of 16,384, two heads: 77 and 62).
+  // 13.0 in pairs; 64 of 16,384, two heads: 77 and 62).  The lengths themselves are the device's, so
+  // that a list with room to spare counts as long, and gets pairs.
   const bool small = (p.pages.n_idx << p.pages.log2_page) * p.Hk * 2 * D <= 32 << 20;
   return unit_heads(D, p.Hk) == 2 && !small ? launch<64, 2>(p, sms, s) : launch<64, 1>(p, sms, s);
 }

@@ -1,7 +1,8 @@
 // mla_gqa_block_decode for many query rows a KV head (several new tokens, large groups): the products
 // on tcgen05 straight from the cache's e4m3 codes.  The work's split, the units on their line and the
-// join of pieces are the narrow kernel's (mla_gqa_block_decode.cu); a unit has up to 32 rows, of one
-// 128-wide head or of a pair of 64-wide ones, whose 128 bytes of a slot are one row of a tile.
+// join of pieces are the narrow kernel's (mla_gqa_block_decode.cu); a unit has up to 32 rows of one
+// 128-wide head, or 16 of each of a pair of 64-wide ones, whose 128 bytes of a slot are one row of a
+// tile: more rows of a head are more units, each of which reads the cache again.
 //
 // A tile is 128 positions: the MMA's M (tensor memory's lanes).
 //   S^T (128 x 64) = K (128 x 128 bytes) . q^T, a head's rows as two e4m3 planes side by side in N:
@@ -10,11 +11,12 @@
 //     NaN there is no other head's.
 //   a_j = log2(e) s_j + log2 vscale(j), p_j = 2^(a_j - m + 5) for a reference m that moves only where an
 //     a_j passes it by more than 3: p stays below 2^8, e4m3 ends at 448.  (Moving costs some 800
-//     cycles: with room for 4, 3, 2 and 1 the first case below takes 112, 114, 117 and 120 us.)
+//     cycles: with room for 4, 3, 2 and 1 the first case below took 112, 114, 117 and 120 us.)
 //   O^T (128 columns x 96) += V^T . P^T, V^T read MN-major from the same layout, P as three e4m3
 //     planes: p (rounded to f16) = h + 2^-5 l + 2^-10 l', 11 bits down to 2^-13 of the largest
-//     weight times scale, below that multiples of 2^-24 of it: what 131,072 positions lose by
-//     rounding is under 2^-8 of what the largest has, bf16's half step.
+//     weight times scale, below that multiples of 2^-24 of it.  A position loses half of one at
+//     most, n of them n 2^-25 of what the largest has: 2^-8, bf16's half step, at 131,072, and 2^-5 at
+//     1,048,576, where weights that small are all that there is.
 // Eight MMAs a tile, 64 (32 for a pair) and 96 columns wide: about 400 cycles of the tensor pipe for 32 KB, which take
 // 1,420 from memory.
 //
@@ -22,10 +24,12 @@
 // rows), one issues the MMAs, one copies tiles (TMA, a box a page, five stages), two fetch scales.
 // The last three go from piece to piece without the others, so that a piece's first tiles are there
 // when its queries are; scores of the next tile are formed while this one's weights are.  Every wait
-// is bounded.
+// is bounded.  The scale warps also look over the new tokens' values, which some rows see and some do
+// not: NaN among them give way, and the rows that see them are marked behind the piece.
 //
 // Measured, us in a graph: 64 requests of 2,048 to 65,536 positions, 4 new tokens, 16/2 heads of 128
-// (544 MB): 114, the narrow kernel 187; 64 of 8,192, 4 tokens, 16/2 heads of 64: 71 and 84.  A tile
+// (544 MB): 116, the narrow kernel 187; 64 of 8,192, 4 tokens, 16/2 heads of 64: 72 and 84 (134 MB, read
+// twice: two units a pair).  A tile
 // takes 1,500 to 1,700 cycles: the softmax warps are busy 1,100 of them (the vote on the reference
 // 120, the fence before the MMAs 160, two waits 300).  Copies by 16-byte cp.async kept seven warps busy
 // and the first case at 176; scales loaded by the softmax warps held each tile for a trip to memory
@@ -692,7 +696,8 @@ cudaError_t launch(const BlockDecodeParams& p, int sms, cudaStream_t stream) {
 // More than 16 query rows a KV head, the narrow kernel's unit: up to there a unit of it reads a cache
 // once as well, and is faster or equal (us here and there: 32/2 heads of 128, 64 requests of 8,192:
 // 65 and 63; 16/2 heads, 16,384: 105 and 92).  Above, the narrow one reads it once for every 16
-// rows, and this one once for every 32 (32 rows: 114 and 187).  Boxes want pages of at
+// rows, and this one once for every 32 of a 128-wide head (32 rows: 116 and 187); of 64-wide heads it
+// reads it once for every 16, too, and is faster all the same (32 rows: 72 and 84).  Boxes want pages of at
 // least a swizzle atom's eight slots, strides that a tensor map can hold, and pairs of 64-wide heads
 // side by side.
 bool pmla::block_wide_takes(const BlockDecodeParams& p, int64_t D) {

@@ -14,7 +14,7 @@
 // and then takes groups of four entries of the lists, found by bisection in shared memory.
 //
 // Measured (one GB300, in a CUDA graph): 64 requests of up to 65,536 positions, one new token each, pages
-// of 128: 5.0 us; 24 of 68,000 positions, 4,089 new, one-token pages, 7.4 MB of lists: 7.2 us (8.0 with two
+// of 128: 5.1 us; 24 of 68,000 positions, 4,089 new, one-token pages, 7.4 MB of lists: 7.2 us (8.0 with two
 // blocks a SM and the stack's count claimed at the end; 6.4 and 7.2 with it read and claimed by a thread that
 // writes entries, too).
 #include <cuda_runtime.h>

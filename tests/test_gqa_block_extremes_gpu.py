@@ -94,3 +94,35 @@ def test_decode_into_outputs_with_strides(pm, D, rows, new, dtype):
         assert torch.equal(o[:n], want[:n])
         o[:n] = 7.0
         assert (wide == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,new", [(4, 1), (8, 2), (32, 1), (8, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_of_infinite_scores(pm, D, rows, new):
+    """A block of infinite key scale: rows that score it -inf give it no weight, +inf and NaN make theirs
+    NaN; a row whose scores are all -inf is zero."""
+    n, Hk = 300, 2
+    c = Decode([n, 40], [new] * 2, rows * Hk, Hk, D, 16, 16)
+    good, lse_good, ws = c.run(pm, torch.float32)
+    page, slot = c.pages.where(0, 32, 48)
+    code = torch.tensor(1.0).to(blk.F8).view(torch.uint8).item()
+    c.kc.view(torch.uint8)[page, slot] = code
+    c.ks[page[0], 0] = math.inf
+    sign = torch.where(torch.arange(rows * Hk, device=DEV) % 3 == 0, 1.0, -1.0)        # of the heads' scores
+    c.q.copy_((c.q.float().abs() * sign[:, None]).bfloat16())
+    o, lse, _ = c.run(pm, torch.float32, ws=ws)
+    up = sign > 0
+    assert o[:new, up].isnan().all() and lse[:new, up].isnan().all()
+    assert o[:new, ~up].isfinite().all() and lse[:new, ~up].isfinite().all()
+    # the same without those positions: their keys out of reach by a finite score
+    c.ks[page[0], 0] = 2.0 ** 40
+    want, lse_want, _ = c.run(pm, torch.float32, ws=ws)
+    assert torch.equal(o[:new, ~up], want[:new, ~up]) and torch.equal(lse[:new, ~up], lse_want[:new, ~up])
+    assert torch.equal(o[new:], want[new:])
+    # every score -inf
+    page, slot = c.pages.where(0, 0, n)
+    c.kc.view(torch.uint8)[page, slot] = code
+    c.ks[page, slot // 16] = math.inf
+    o, lse, _ = c.run(pm, torch.float32, ws=ws)
+    assert (o[:new, ~up] == 0).all() and torch.isneginf(lse[:new, ~up]).all() and o[:new, up].isnan().all()
+    assert torch.equal(o[new:], want[new:]) and pm.mla_check_error(ws) == 0
