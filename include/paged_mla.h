@@ -502,9 +502,10 @@ int mla_build_page_table(const mla_tensor_t* seq_lens, const mla_tensor_t* new_l
  *   error_word    device int32 (required).  A request whose lists make no sense (token range not
  *                 inside T, page list not monotone or not inside kv_indices, T_b > L_b) appends
  *                 nothing (no k_out either) and sets bit 2 (where qo_indptr falls from one entry
- *                 inside T to another, requests beside it may be left out, too); a page outside the cache is skipped
- *                 and sets bit 64; a rotary position outside [0, max_pos) sets bit 1 and leaves
- *                 that token's rotated columns (of q_out, k_out and its key entry) unwritten.
+ *                 inside T to another, requests beside it may be left out, too); a page outside
+ *                 the cache is skipped and sets bit 64; a rotary position outside [0, max_pos) sets
+ *                 bit 1 and leaves that token's rotated columns (of q_out, k_out and its key
+ *                 entry) unwritten.
  */
 int mla_gqa_block_append(const mla_tensor_t* q, const mla_tensor_t* k, const mla_tensor_t* v,
                          const mla_tensor_t* positions, const mla_tensor_t* cos_sin,
