@@ -136,17 +136,9 @@ __device__ __forceinline__ float over_lanes(float* v, int lane) {
 }
 __device__ __forceinline__ int row16(int lane) { return lane >> 1; }
 
-__device__ __forceinline__ uint32_t to_e4m3x2(uint32_t f16x2) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
-  return r;
-}
 // What two f16 values lack as e4m3 codes, times 32.
 __device__ __forceinline__ uint32_t rest_f16x2(uint32_t x, uint32_t codes) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(e4m3x2_to_f16x2(codes)));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x50005000u));
-  return r;
+  return f16x2_mul(f16x2_sub(x, e4m3x2_to_f16x2(codes)), 0x50005000u);
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar) {
@@ -551,10 +543,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) gqa_block_wide_kernel(
             l[k + 2 * e] = fmaf(w0, rv, l[k + 2 * e]);
             l[k + 2 * e + 1] = fmaf(w1, rv, l[k + 2 * e + 1]);
             const uint32_t y = f32x2_to_f16x2(w1, w0);
-            c[e][0] = to_e4m3x2(y);
+            c[e][0] = f16x2_to_e4m3x2(y);
             const uint32_t y1 = rest_f16x2(y, c[e][0]);
-            c[e][1] = to_e4m3x2(y1);
-            c[e][2] = to_e4m3x2(rest_f16x2(y1, c[e][1]));
+            c[e][1] = f16x2_to_e4m3x2(y1);
+            c[e][2] = f16x2_to_e4m3x2(rest_f16x2(y1, c[e][1]));
           }
           h[k / 4] = c[0][0] | c[1][0] << 16;
           lo1[k / 4] = c[0][1] | c[1][1] << 16;
